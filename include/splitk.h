@@ -110,6 +110,8 @@ typedef enum {
 
 #define SPLITK_MAX_DIM (1 << 22)
 #define SPLITK_MAX_SPLITS 4096
+/* Runs (experts) of a grouped product. */
+#define SPLITK_MAX_GROUPS 1024
 /* Size of the scratch array gemm_bt_noalloc keeps in device memory. */
 #define SPLITK_NOALLOC_MAX_BYTES (32 << 20)
 
@@ -348,6 +350,105 @@ int splitk_autotune_splits(const void *A, const void *B, float *out,
                            int64_t N, int64_t K, int dtype, int fused,
                            int reps, void *stream, int64_t *splits,
                            int64_t *k_per_split, float *us);
+
+/* ---- 8-bit operands and rows grouped by expert
+ *
+ * 8-bit values are E4M3 (largest value 448, no infinities), stored one to a
+ * byte.  Along K they share an F32 scale in blocks of 128, the last block
+ * possibly short: the number that q stands for is q * scale.
+ *   activations  q [M,K], scales [M, ceil(K/128)]: a scale for each 128
+ *                values of a row
+ *   weights      q [G,N,K], scales [G, ceil(N/128), ceil(K/128)]: a scale for
+ *                each 128 x 128 block (edge blocks smaller)
+ * Scales may be any F32 values (no power of two is assumed).
+ *
+ * Every tensor is dense and row-major; rows follow one another without
+ * padding.  K is a positive multiple of 16 with 8-bit operands and of 8 with
+ * 16-bit ones, whatever N and M (or T) are, unless said otherwise.  M (or T)
+ * may be 0: nothing is written then, except by gemm_grouped_dw.  M, T, N, K <=
+ * SPLITK_MAX_DIM, G <= SPLITK_MAX_GROUPS (else SPLITK_ERR_SHAPE).  Pointers are
+ * 16-byte aligned (`offsets`: 4-byte), outputs overlap nothing (exceptions are
+ * named), and out_dtype is SPLITK_F32, _F16 or _BF16, rounded once from the
+ * F32 sum.  Checks come before any device work, in the order shape, dtype,
+ * NULL, alignment, overlap.  The calls take no workspace, may be captured,
+ * and give the same bits for the same call every time. */
+
+/* Residual addition, root-mean-square norm, 8-bit output:
+ *   h = x + residual, rounded to `dtype` (h = x without a residual)
+ *   y = h * weight / sqrt(mean_k h^2 + eps), in F32
+ *   scales[m,b] = max(max_{k in b} |y[m,k]| / 448, 2^-126)
+ *   q[m,k]      = y[m,k] / scales[m,b] to E4M3, to nearest even
+ *   x, residual  device, [M,K] of `dtype` (SPLITK_F32, _F16, _BF16); residual
+ *                may be NULL
+ *   weight       device, [K] of `dtype`
+ *   sum          device, [M,K] of `dtype` or NULL: receives h; may be exactly
+ *                x or residual (in place)
+ *   y            device, [M,K] of `dtype` or NULL: receives y, rounded once
+ *   q, scales    device, as above
+ * A row that holds a NaN or an infinity gets NaN scales and codes.  eps >= 0
+ * (else SPLITK_ERR_CONFIG). */
+int rmsnorm_fp8(const void *x, const void *residual, const void *weight,
+                void *sum, void *y, void *q, float *scales, int64_t M,
+                int64_t K, float eps, int dtype, void *stream);
+
+/* Activations x [M,K] of `dtype` to 8 bits, as rmsnorm_fp8 does with y = x. A
+ * block that holds a NaN gets NaN scale and codes; one that holds an infinity
+ * an infinite scale (and NaN for the infinity, 0 for the rest). */
+int fp8_quantize(const void *x, void *q, float *scales, int64_t M, int64_t K,
+                 int dtype, void *stream);
+
+/* Weight preparation, once: B [G,N,K] of `dtype` to 8 bits with a scale for
+ * each 128 x 128 block (max |B| / 448, at least 2^-126).  G = 1 for a single
+ * weight. */
+int fp8_prepare_bt(const void *B, void *Bq, float *scales, int64_t G,
+                   int64_t N, int64_t K, int dtype, void *stream);
+
+/* out[m,n] = sum_b a_scales[m,b] * b_scales[n/128,b] * sum_{k in b} A[m,k]*B[n,k]
+ * with A [M,K] and B [N,K] in 8 bits.  The sum over a block runs on the
+ * tensor cores; the scaled sum over blocks is in F32. */
+int gemm_fp8_bt(const void *A, const float *a_scales, const void *B,
+                const float *b_scales, void *out, int64_t M, int64_t N,
+                int64_t K, int out_dtype, void *stream);
+
+/* Products grouped by expert: the rows of A [T,K] stand sorted by expert, run
+ * g being rows offsets[g] .. offsets[g+1]-1, and each run meets its own weight:
+ *   out[t,n] = sum_k A[t,k] * B[g,n,k]        t in run g
+ *   offsets  device, int32 [G+1], not decreasing, within [0,T]; runs may be
+ *            empty.  It is read on the device: no synchronisation.  (Offsets
+ *            that break the rule are clamped to it, so that no access leaves
+ *            the tensors; the result is then that of the clamped runs.)
+ *   out      device, [T,N]; rows before offsets[0] and from offsets[G] on are
+ *            left as they are
+ * gemm_grouped_fp8_bt: 8-bit operands with scales, as gemm_fp8_bt. */
+int gemm_grouped_fp8_bt(const void *A, const float *a_scales, const void *B,
+                        const float *b_scales, const int32_t *offsets,
+                        void *out, int64_t T, int64_t G, int64_t N, int64_t K,
+                        int out_dtype, void *stream);
+
+/* 16-bit operands (dtype SPLITK_F16 or _BF16; else SPLITK_ERR_DTYPE), weights
+ * B [G,N,K]. */
+int gemm_grouped_bt(const void *A, const void *B, const int32_t *offsets,
+                    void *out, int64_t T, int64_t G, int64_t N, int64_t K,
+                    int dtype, int out_dtype, void *stream);
+
+/* The same with weights W [G,K,N] (N a multiple of 8).  It is also the
+ * gradient of gemm_grouped_bt's A: dA = gemm_grouped_kn(dOut, B) with N and K
+ * exchanged. */
+int gemm_grouped_kn(const void *A, const void *W, const int32_t *offsets,
+                    void *out, int64_t T, int64_t G, int64_t N, int64_t K,
+                    int dtype, int out_dtype, void *stream);
+
+/* The gradient of gemm_grouped_bt's B:
+ *   dB[g,n,k] = sum_{t in run g} D[t,n] * A[t,k]
+ *   A   device, [T,K]; D device, [T,N], the output's gradient (N a multiple of
+ *       8); both of `dtype`
+ *   dB  device, [G,N,K] of out_dtype, fully overwritten: zeros for an empty
+ *       run
+ * (gemm_grouped_kn's W has the gradient dW[g,k,n]: the same call with A and D,
+ * and N and K, exchanged.) */
+int gemm_grouped_dw(const void *A, const void *D, const int32_t *offsets,
+                    void *dB, int64_t T, int64_t G, int64_t N, int64_t K,
+                    int dtype, int out_dtype, void *stream);
 
 /* Reads and clears the device status word on the current device,
  * synchronising `stream` first.  Returns SPLITK_OK, SPLITK_ERR_DEVICE_TIMEOUT

@@ -16,4 +16,6 @@ from .binding import (  # noqa: F401
     splitk_selftest_bounded_wait, splitk_selftest_kernel_timeout, splitk_set_overlap, splitk_set_tile_override,
     splitk_status_string,
     status_string,
+    fp8_prepare_bt, fp8_quantize, gemm_fp8_bt, gemm_grouped_bt, gemm_grouped_dw, gemm_grouped_fp8_bt,
+    gemm_grouped_kn, rmsnorm_fp8,
 )

@@ -29,6 +29,8 @@ EXPORTS = (
     "gemm_bt_host_staging_bytes", "gemm_bt_host_batch", "splitk_choose_splits", "splitk_autotune_splits",
     "gemm_splitk_kn", "gemm_kn", "splitk_set_overlap", "splitk_last_launch", "splitk_selftest_kernel_timeout",
     "gemm_bt_batch",
+    "rmsnorm_fp8", "fp8_quantize", "fp8_prepare_bt", "gemm_fp8_bt", "gemm_grouped_fp8_bt", "gemm_grouped_bt",
+    "gemm_grouped_kn", "gemm_grouped_dw",
 )
 NOALLOC_MAX_BYTES = 32 << 20   # SPLITK_NOALLOC_MAX_BYTES
 
@@ -84,7 +86,17 @@ def lib() -> ctypes.CDLL:
             L.splitk_last_launch.argtypes = [vp]
             L.splitk_selftest_kernel_timeout.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, i32, vp]
             L.splitk_last_error.restype = ctypes.c_char_p
-            for name in ("splitk_check_geometry", "gemm_splitk_bt", "splitk_reduce", "gemm_bt",
+            f32 = ctypes.c_float
+            L.rmsnorm_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, f32, i32, vp]
+            L.fp8_quantize.argtypes = [vp, vp, vp, i64, i64, i32, vp]
+            L.fp8_prepare_bt.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp]
+            L.gemm_fp8_bt.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i32, vp]
+            L.gemm_grouped_fp8_bt.argtypes = [vp] * 6 + [i64] * 4 + [i32, vp]
+            for name in ("gemm_grouped_bt", "gemm_grouped_kn", "gemm_grouped_dw"):
+                getattr(L, name).argtypes = [vp] * 4 + [i64] * 4 + [i32, i32, vp]
+            for name in ("rmsnorm_fp8", "fp8_quantize", "fp8_prepare_bt", "gemm_fp8_bt", "gemm_grouped_fp8_bt",
+                         "gemm_grouped_bt", "gemm_grouped_kn", "gemm_grouped_dw",
+                         "splitk_check_geometry", "gemm_splitk_bt", "splitk_reduce", "gemm_bt",
                          "gemm_splitk_kn", "gemm_kn",
                          "gemm_bt_workspace_init", "gemm_bt_noalloc", "splitk_prepare_bt",
                          "gemm_bt_host_batch", "splitk_choose_splits", "splitk_autotune_splits",
@@ -309,3 +321,57 @@ def splitk_selftest_kernel_timeout(A, B, out, M, N, K, splits, k_per_split, dtyp
     (ERR_DEVICE_TIMEOUT expected).  Never raises."""
     return lib().splitk_selftest_kernel_timeout(_ptr(A), _ptr(B), _ptr(out), M, N, K, splits, k_per_split,
                                                 dtype_code(dtype), _stream(stream))
+
+
+def rmsnorm_fp8(x, weight, q, scales, M, K, dtype, eps=1e-6, residual=None, sum_out=None, y=None,
+                stream=None) -> None:
+    """Residual addition, root-mean-square norm and 8-bit output with a scale
+    for each 128 values: q [M,K] (torch.float8_e4m3fn), scales [M, ceil(K/128)]
+    F32; sum_out (x + residual; may be x or residual) and y (the norm in
+    `dtype`) where given."""
+    _check(lib().rmsnorm_fp8(_ptr(x), _ptr(residual), _ptr(weight), _ptr(sum_out), _ptr(y), _ptr(q), _ptr(scales),
+                             M, K, eps, dtype_code(dtype), _stream(stream)), "rmsnorm_fp8")
+
+
+def fp8_quantize(x, q, scales, M, K, dtype, stream=None) -> None:
+    """Activations x [M,K] to 8 bits: q [M,K], scales [M, ceil(K/128)] F32."""
+    _check(lib().fp8_quantize(_ptr(x), _ptr(q), _ptr(scales), M, K, dtype_code(dtype), _stream(stream)),
+           "fp8_quantize")
+
+
+def fp8_prepare_bt(B, Bq, scales, G, N, K, dtype, stream=None) -> None:
+    """Weights B [G,N,K] to 8 bits: Bq [G,N,K], scales [G, ceil(N/128), ceil(K/128)] F32."""
+    _check(lib().fp8_prepare_bt(_ptr(B), _ptr(Bq), _ptr(scales), G, N, K, dtype_code(dtype), _stream(stream)),
+           "fp8_prepare_bt")
+
+
+def gemm_fp8_bt(A, a_scales, B, b_scales, out, M, N, K, out_dtype, stream=None) -> None:
+    """out [M,N] = A B^T from 8-bit operands with their scales."""
+    _check(lib().gemm_fp8_bt(_ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales), _ptr(out), M, N, K,
+                             dtype_code(out_dtype), _stream(stream)), "gemm_fp8_bt")
+
+
+def gemm_grouped_fp8_bt(A, a_scales, B, b_scales, offsets, out, T, G, N, K, out_dtype, stream=None) -> None:
+    """gemm_fp8_bt per run of rows: rows offsets[g]..offsets[g+1]-1 of A [T,K]
+    meet B[g] ([G,N,K]); offsets: int32 [G+1] on the device."""
+    _check(lib().gemm_grouped_fp8_bt(_ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales), _ptr(offsets), _ptr(out),
+                                     T, G, N, K, dtype_code(out_dtype), _stream(stream)), "gemm_grouped_fp8_bt")
+
+
+def gemm_grouped_bt(A, B, offsets, out, T, G, N, K, dtype, out_dtype, stream=None) -> None:
+    """out [T,N]: rows offsets[g]..offsets[g+1]-1 of A [T,K] times B[g]^T (B [G,N,K]), 16-bit operands."""
+    _check(lib().gemm_grouped_bt(_ptr(A), _ptr(B), _ptr(offsets), _ptr(out), T, G, N, K, dtype_code(dtype),
+                                 dtype_code(out_dtype), _stream(stream)), "gemm_grouped_bt")
+
+
+def gemm_grouped_kn(A, W, offsets, out, T, G, N, K, dtype, out_dtype, stream=None) -> None:
+    """gemm_grouped_bt with weights W [G,K,N]; with N and K exchanged, the
+    gradient of gemm_grouped_bt's A."""
+    _check(lib().gemm_grouped_kn(_ptr(A), _ptr(W), _ptr(offsets), _ptr(out), T, G, N, K, dtype_code(dtype),
+                                 dtype_code(out_dtype), _stream(stream)), "gemm_grouped_kn")
+
+
+def gemm_grouped_dw(A, D, offsets, dB, T, G, N, K, dtype, out_dtype, stream=None) -> None:
+    """The gradient of gemm_grouped_bt's B: dB[g] [N,K] = D_g^T A_g over the rows of run g."""
+    _check(lib().gemm_grouped_dw(_ptr(A), _ptr(D), _ptr(offsets), _ptr(dB), T, G, N, K, dtype_code(dtype),
+                                 dtype_code(out_dtype), _stream(stream)), "gemm_grouped_dw")

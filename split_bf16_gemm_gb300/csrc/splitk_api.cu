@@ -433,6 +433,169 @@ int gemm_kn(const void *A, const void *W, float *out, void *workspace, size_t wo
     return gemm_impl(A, W, out, workspace, workspace_bytes, M, N, K, splits, k_per_split, dtype, fused, true, stream);
 }
 
+// ---- 8-bit operands, rows grouped by expert
+
+namespace {
+
+constexpr int kFp8Block = 128;
+
+struct Extent {
+    const void *p;
+    uint64_t bytes;
+};
+
+// NULL and alignment of every pointer, then each output against the inputs and
+// the other outputs.  `in_place` (may be -1): the one output that may be
+// exactly one of the inputs (same address; the extents are equal).
+int validate_extents(const Extent *in, int n_in, const Extent *out, int n_out, int in_place = -1)
+{
+    for (int i = 0; i < n_in; ++i)
+        if (!in[i].p) return SPLITK_ERR_NULL;
+    for (int i = 0; i < n_out; ++i)
+        if (!out[i].p) return SPLITK_ERR_NULL;
+    for (int i = 0; i < n_in; ++i)
+        if (!aligned16(in[i].p)) return SPLITK_ERR_ALIGN;
+    for (int i = 0; i < n_out; ++i)
+        if (!aligned16(out[i].p)) return SPLITK_ERR_ALIGN;
+    for (int o = 0; o < n_out; ++o) {
+        const Range r = range_of(out[o].p, out[o].bytes);
+        for (int i = 0; i < n_in; ++i)
+            if (overlap(r, range_of(in[i].p, in[i].bytes)) &&
+                !(o == in_place && in[i].p == out[o].p && in[i].bytes == out[o].bytes))
+                return SPLITK_ERR_ALIAS;
+        for (int i = 0; i < o; ++i)
+            if (overlap(r, range_of(out[i].p, out[i].bytes))) return SPLITK_ERR_ALIAS;
+    }
+    return SPLITK_OK;
+}
+
+int64_t blocks_of(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
+
+int rows_fp8(const void *x, const void *residual, const void *weight, void *sum, void *y, void *q, float *scales,
+             int64_t M, int64_t K, float eps, int dtype, void *stream)
+{
+    if (M < 0 || M > SPLITK_MAX_DIM || K <= 0 || K > SPLITK_MAX_DIM || K % 16) return SPLITK_ERR_SHAPE;
+    const int e = elem_bytes(dtype);
+    if (e == 0) return SPLITK_ERR_DTYPE;
+    const uint64_t bytes = static_cast<uint64_t>(M * K) * e;
+    Extent in[3] = {{x, bytes}}, out[4] = {{q, static_cast<uint64_t>(M * K)},
+                                           {scales, static_cast<uint64_t>(M * blocks_of(K)) * 4}};
+    int n_in = 1, n_out = 2, in_place = -1;
+    if (weight) in[n_in++] = {weight, static_cast<uint64_t>(K) * e};
+    if (residual) in[n_in++] = {residual, bytes};
+    if (y) out[n_out++] = {y, bytes};
+    if (sum) {
+        in_place = n_out;
+        out[n_out++] = {sum, bytes};
+    }
+    const int st = validate_extents(in, n_in, out, n_out, in_place);
+    if (st != SPLITK_OK || M == 0) return st;
+    return cuda_status(splitk::launch_rows_fp8({x, residual, weight, sum, y, q, scales, M, K, eps, dtype},
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+using splitk::GroupedForm;
+
+// Every grouped entry point.  `offsets` is nullptr for the plain product.
+int grouped(GroupedForm form, const void *A, const float *sa, const void *B, const float *sb, const int *offsets,
+            void *out, int64_t T, int64_t G, int64_t N, int64_t K, int dtype, int out_dtype, bool plain, void *stream)
+{
+    const bool fp8 = form == GroupedForm::kFp8, dw = form == GroupedForm::kDw;
+    // TMA reads rows in steps of 16 bytes: every row a step long, or a multiple
+    const int64_t step = fp8 ? 16 : 8;
+    if (T < 0 || T > SPLITK_MAX_DIM || G <= 0 || G > SPLITK_MAX_GROUPS || N <= 0 || N > SPLITK_MAX_DIM || K <= 0 ||
+        K > SPLITK_MAX_DIM || K % step)
+        return SPLITK_ERR_SHAPE;
+    if ((form == GroupedForm::kKn || dw) && N % step) return SPLITK_ERR_SHAPE;
+    if (!fp8 && dtype != SPLITK_BF16 && dtype != SPLITK_F16) return SPLITK_ERR_DTYPE;
+    const int oe = elem_bytes(out_dtype);
+    if (oe == 0) return SPLITK_ERR_DTYPE;
+    const splitk::GroupedProblem p = {form, A, B, sa, sb, offsets, out, T, G, N, K, out_dtype, dtype == SPLITK_BF16};
+    // tile counts are 32-bit
+    if (splitk::grouped_tiles(p, 32) > INT32_MAX) return SPLITK_ERR_SHAPE;
+    const int64_t e = fp8 ? 1 : 2;
+    const int64_t kb = blocks_of(K);
+    Extent in[5] = {{A, static_cast<uint64_t>(T * K * e)},
+                    {B, static_cast<uint64_t>(dw ? T * N : G * N * K) * e}};
+    int n_in = 2;
+    if (fp8) {
+        in[n_in++] = {sa, static_cast<uint64_t>(T * kb) * 4};
+        in[n_in++] = {sb, static_cast<uint64_t>(G * blocks_of(N) * kb) * 4};
+    }
+    const Extent o[1] = {{out, static_cast<uint64_t>(dw ? G * N * K : T * N) * oe}};
+    int st = validate_extents(in, n_in, o, 1);
+    if (st != SPLITK_OK) return st;
+    if (!plain) {
+        if (!offsets) return SPLITK_ERR_NULL;
+        if (reinterpret_cast<uintptr_t>(offsets) & 3u) return SPLITK_ERR_ALIGN;
+        if (overlap(range_of(offsets, static_cast<uint64_t>(G + 1) * 4), range_of(out, o[0].bytes)))
+            return SPLITK_ERR_ALIAS;
+    }
+    if (T == 0 && !dw) return SPLITK_OK;
+    return cuda_status(splitk::launch_grouped(p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+int rmsnorm_fp8(const void *x, const void *residual, const void *weight, void *sum, void *y, void *q, float *scales,
+                int64_t M, int64_t K, float eps, int dtype, void *stream)
+{
+    if (!weight) return SPLITK_ERR_NULL;
+    if (!(eps >= 0.f)) return SPLITK_ERR_CONFIG;
+    return rows_fp8(x, residual, weight, sum, y, q, scales, M, K, eps, dtype, stream);
+}
+
+int fp8_quantize(const void *x, void *q, float *scales, int64_t M, int64_t K, int dtype, void *stream)
+{
+    return rows_fp8(x, nullptr, nullptr, nullptr, nullptr, q, scales, M, K, 0.f, dtype, stream);
+}
+
+int fp8_prepare_bt(const void *B, void *Bq, float *scales, int64_t G, int64_t N, int64_t K, int dtype, void *stream)
+{
+    if (G <= 0 || G > SPLITK_MAX_GROUPS || N <= 0 || N > SPLITK_MAX_DIM || K <= 0 || K > SPLITK_MAX_DIM || K % 16)
+        return SPLITK_ERR_SHAPE;
+    const int64_t blocks = G * blocks_of(N) * blocks_of(K);
+    if (blocks > INT32_MAX) return SPLITK_ERR_SHAPE;
+    const int e = elem_bytes(dtype);
+    if (e == 0) return SPLITK_ERR_DTYPE;
+    const Extent in[1] = {{B, static_cast<uint64_t>(G * N * K) * e}};
+    const Extent out[2] = {{Bq, static_cast<uint64_t>(G * N * K)}, {scales, static_cast<uint64_t>(blocks) * 4}};
+    const int st = validate_extents(in, 1, out, 2);
+    if (st != SPLITK_OK) return st;
+    return cuda_status(splitk::launch_prepare_fp8(B, Bq, scales, G, N, K, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int gemm_fp8_bt(const void *A, const float *a_scales, const void *B, const float *b_scales, void *out, int64_t M,
+                int64_t N, int64_t K, int out_dtype, void *stream)
+{
+    return grouped(GroupedForm::kFp8, A, a_scales, B, b_scales, nullptr, out, M, 1, N, K, 0, out_dtype, true, stream);
+}
+
+int gemm_grouped_fp8_bt(const void *A, const float *a_scales, const void *B, const float *b_scales,
+                        const int32_t *offsets, void *out, int64_t T, int64_t G, int64_t N, int64_t K, int out_dtype,
+                        void *stream)
+{
+    return grouped(GroupedForm::kFp8, A, a_scales, B, b_scales, offsets, out, T, G, N, K, 0, out_dtype, false, stream);
+}
+
+int gemm_grouped_bt(const void *A, const void *B, const int32_t *offsets, void *out, int64_t T, int64_t G, int64_t N,
+                    int64_t K, int dtype, int out_dtype, void *stream)
+{
+    return grouped(GroupedForm::kNk, A, nullptr, B, nullptr, offsets, out, T, G, N, K, dtype, out_dtype, false, stream);
+}
+
+int gemm_grouped_kn(const void *A, const void *W, const int32_t *offsets, void *out, int64_t T, int64_t G, int64_t N,
+                    int64_t K, int dtype, int out_dtype, void *stream)
+{
+    return grouped(GroupedForm::kKn, A, nullptr, W, nullptr, offsets, out, T, G, N, K, dtype, out_dtype, false, stream);
+}
+
+int gemm_grouped_dw(const void *A, const void *D, const int32_t *offsets, void *dB, int64_t T, int64_t G, int64_t N,
+                    int64_t K, int dtype, int out_dtype, void *stream)
+{
+    return grouped(GroupedForm::kDw, A, nullptr, D, nullptr, offsets, dB, T, G, N, K, dtype, out_dtype, false, stream);
+}
+
 const char *splitk_last_error(void) { return splitk::last_error_message(); }
 
 int splitk_get_device_status(void *stream)
@@ -443,6 +606,9 @@ int splitk_get_device_status(void *stream)
         splitk::note_error(e, "reading the device status word");
         return SPLITK_ERR_CUDA;
     }
+    unsigned grouped_status = 0;
+    if (splitk::read_and_clear_grouped_status(&grouped_status) != cudaSuccess) return SPLITK_ERR_CUDA;
+    status |= grouped_status;
     return status ? SPLITK_ERR_DEVICE_TIMEOUT : SPLITK_OK;
 }
 

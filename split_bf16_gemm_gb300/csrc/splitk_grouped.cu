@@ -1,0 +1,801 @@
+// splitk_grouped.cu -- 8-bit products with a scale for each block of 128, and
+// products grouped by expert, on the 5th-generation tensor cores.
+//
+// One kernel computes, for ragged runs of rows (run g is rows offsets[g] ..
+// offsets[g+1]-1; one run of all rows for the plain product):
+//   kFp8   out[t,n]  = sum_kb sa[t,kb] sb[g,n/128,kb] sum_{k in kb} A[t,k] B[g,n,k]
+//   kNk    out[t,n]  = sum_k A[t,k] B[g,n,k]
+//   kKn    out[t,n]  = sum_k A[t,k] W[g,k,n]
+//   kDw    dB[g,n,k] = sum_{t in run g} D[t,n] A[t,k]
+//
+// Every tile is 128 tensor-memory lanes by up to TC columns.  The lanes are
+// the weight's rows n (kDw: the columns k of A) and the columns are tokens
+// (kDw: the columns n of D), because the token count of a run is the ragged
+// and often small extent: the MMA's N can be any multiple of 16, so a run of
+// 5 tokens costs 16 columns and not a 128-row tile.  A run's columns are
+// split evenly over its tiles.  Output rows are contiguous along the lanes.
+//
+// 384 threads:
+//   warp 0     TMA producer (one lane): k-blocks of 128 bytes (128 8-bit or
+//              64 16-bit values) of 128 lanes and of the tile's columns;
+//   warp 1     MMA issuer (one lane);
+//   warp 2     kFp8: the products sa * sb of each k-block's columns, into a
+//              ring in shared memory; kDw: zeroes the rows past the run's end
+//              in the last k-block (they belong to the next run);
+//   warps 4-11 tensor memory -> registers -> output: lane quarter w % 4,
+//              column half w / 4 - 1.
+// kFp8: F32 scales cannot be applied inside the MMA, so each k-block's product
+// goes to an accumulator of its own (a ring of them in tensor memory), and the
+// last eight warps add it, times the scale, to F32 sums in registers while
+// the next block multiplies.
+//
+// Long K with few tiles: the S blocks of a cluster each take 1/S of the
+// k-blocks and add their F32 sums through distributed shared memory in rank
+// order, so the result does not depend on timing.
+//
+// Every wait has a time limit.  A wait that runs out sets the device status
+// word and a flag that ends the block's other waits; the loads in flight are
+// awaited, the MMAs too, before tensor memory is freed.
+
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "ptx.cuh"
+#include "splitk_internal.h"
+
+namespace splitk {
+namespace {
+
+__device__ unsigned g_grouped_status;
+
+constexpr uint64_t kWaitLimitNs = 1000000000ull;   // 1 s
+constexpr int kThreads = 384;
+constexpr int kEpilogueWarps = 8;
+constexpr int kLanes = 128;
+constexpr uint32_t kLaneBytes = kLanes * 128;       // one k-block of the lane operand
+constexpr int kMaxRing = 12;
+constexpr int kScaleRing = 8;
+constexpr int kUnit = 8;   // k-blocks (512 values of K) between additions in registers
+
+enum Form { kFp8, kNk, kKn, kDw };
+
+template <int TC>
+struct Shape {
+    static constexpr int kAcc = TC <= 32 ? 4 : 2;                 // accumulators in tensor memory
+    static constexpr int kTmemCols = kAcc * TC;
+    static constexpr uint32_t kColBytes = TC * 128;
+    static constexpr uint32_t kStage = kLaneBytes + kColBytes;
+};
+
+struct GroupedArgs {
+    const int *offsets;        // [G+1] on the device, or nullptr: one run of T rows
+    const float *sa, *sb;      // kFp8
+    void *out;
+    int T, G;
+    int lanes, cols;           // extent of the lanes; of the columns for kDw (else the run's length)
+    int K, kblocks;            // contracted extent and its k-blocks (not kDw)
+    int out_type;              // splitk_dtype
+    int bf16;
+    int splits;                // cluster size along K
+    int stages;
+    uint32_t sum_off, scale_off, table_off;   // byte offsets in shared memory after the stage ring
+};
+
+struct Maps {
+    CUtensorMap lane, col, col_part;   // col_part: TC / 4 rows instead of TC
+};
+
+struct Tile {
+    int g, row0;               // first output row
+    int lane0, cols, width;    // first lane; live columns, and rounded up to the MMA's N
+    int col0;                  // first column: a token, or a column of D
+    int kb0, nkb;              // this block's k-blocks
+    int tok0, tok_n;           // kDw: the run
+};
+
+__device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, volatile unsigned *abort)
+{
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if ((i & 63u) == 0 && (*abort || ptx::globaltimer_ns() - t0 > kWaitLimitNs)) {
+            *abort = 1u;
+            atomicOr(&g_grouped_status, 1u);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ void store_out(void *out, int type, size_t i, float v)
+{
+    if (type == 0)
+        static_cast<float *>(out)[i] = v;
+    else if (type == 1)
+        static_cast<__half *>(out)[i] = __float2half_rn(v);
+    else
+        static_cast<__nv_bfloat16 *>(out)[i] = __float2bfloat16_rn(v);
+}
+
+template <int FORM, int TC, bool SUMS>
+__global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_constant__ Maps maps, const GroupedArgs args)
+{
+    static_assert(SUMS || FORM != kFp8, "8-bit operands need the F32 sums in registers");
+    using Sh = Shape<TC>;
+    constexpr bool FP8 = FORM == kFp8, DW = FORM == kDw;
+    constexpr bool LMN = FORM == kKn || FORM == kDw;   // lane operand contiguous along its lanes
+    constexpr int KB = FP8 ? 128 : 64;
+    constexpr int UNIT = FP8 ? 1 : SUMS ? kUnit : 1 << 30;   // k-blocks summed in one accumulator
+    constexpr int HALF = TC / 2;                       // columns of an epilogue warp
+    constexpr int CHUNK = HALF < 32 ? HALF : 32;       // columns of one tensor-memory load
+    static_assert(!DW || TC % 64 == 0, "the columns of kDw come in boxes of 64");
+
+    extern __shared__ uint8_t dsmem[];
+    __shared__ __align__(8) uint64_t bars[3 * kMaxRing + 2 * Sh::kAcc + 2 * kScaleRing + 1];
+    __shared__ uint32_t tmem_slot;
+    __shared__ unsigned abort_s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t raw = ptx::smem_addr(dsmem);
+    const uint32_t ring = (raw + 1023u) & ~1023u;
+    uint8_t *const base = dsmem + (ring - raw);
+    float *const sum_buf = reinterpret_cast<float *>(base + args.sum_off);       // [TC][128], splits > 1
+    float *const scale_buf = reinterpret_cast<float *>(base + args.scale_off);   // [kScaleRing][TC]
+    int *const offs = reinterpret_cast<int *>(base + args.table_off);            // [G+1]
+    int *const pref = offs + args.G + 1;                                         // [G+1]: tiles before run g
+    const uint32_t bar0 = ptx::smem_addr(&bars[0]);
+    auto full_bar = [&](int i) { return bar0 + 8u * i; };
+    auto empty_bar = [&](int i) { return bar0 + 8u * (kMaxRing + i); };
+    auto acc_full = [&](int i) { return bar0 + 8u * (2 * kMaxRing + i); };
+    auto acc_empty = [&](int i) { return bar0 + 8u * (2 * kMaxRing + Sh::kAcc + i); };
+    auto scale_full = [&](int i) { return bar0 + 8u * (2 * kMaxRing + 2 * Sh::kAcc + i); };
+    auto scale_empty = [&](int i) { return bar0 + 8u * (2 * kMaxRing + 2 * Sh::kAcc + kScaleRing + i); };
+    auto fix_bar = [&](int i) { return bar0 + 8u * (2 * kMaxRing + 2 * Sh::kAcc + 2 * kScaleRing + i); };   // kDw
+    const uint32_t drain_bar = fix_bar(kMaxRing);
+    const int stages = args.stages, S = args.splits;
+
+    if (tid == 0) {
+        ptx::prefetch_tensormap(&maps.lane);
+        ptx::prefetch_tensormap(&maps.col);
+        for (int i = 0; i < stages; ++i) {
+            ptx::mbar_init(full_bar(i), 1);
+            ptx::mbar_init(empty_bar(i), DW ? 2 : 1);
+            ptx::mbar_init(fix_bar(i), 1);
+        }
+        for (int i = 0; i < Sh::kAcc; ++i) {
+            ptx::mbar_init(acc_full(i), 1);
+            ptx::mbar_init(acc_empty(i), kEpilogueWarps);
+        }
+        for (int i = 0; i < kScaleRing; ++i) {
+            ptx::mbar_init(scale_full(i), 1);
+            ptx::mbar_init(scale_empty(i), kEpilogueWarps);
+        }
+        ptx::mbar_init(drain_bar, 1);
+        abort_s = 0;
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_addr(&tmem_slot), Sh::kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    // the next launch's blocks may set up now (every block here holds its
+    // tensor memory); they wait for this grid before they read anything
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+
+    // ---- the runs, made monotone and within [0, T] whatever the offsets
+    // hold, and the number of tiles before each
+    const int lane_tiles = (args.lanes + kLanes - 1) / kLanes;
+    if (args.offsets == nullptr) {
+        if (tid < 2) offs[tid] = tid ? args.T : 0;
+    } else {
+        for (int i = tid; i <= args.G; i += kThreads) offs[i] = min(max(args.offsets[i], 0), args.T);
+    }
+    __syncthreads();
+    if (warp == 3) {
+        int most = offs[0], tiles = 0;
+        if (lane == 0) pref[0] = 0;
+        for (int b = 0; b < args.G; b += 32) {
+            const int g = b + lane;
+            int end = g < args.G ? offs[g + 1] : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, end, d);
+                if (lane >= d) end = max(end, o);
+            }
+            end = max(end, most);
+            int begin = __shfl_up_sync(0xffffffffu, end, 1);
+            if (lane == 0) begin = most;
+            const int ext = DW ? args.cols : end - begin;
+            int n = g < args.G ? lane_tiles * ((ext + TC - 1) / TC) : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, n, d);
+                if (lane >= d) n += o;
+            }
+            __syncwarp();
+            if (g < args.G) {
+                offs[g + 1] = end;
+                pref[g + 1] = tiles + n;
+            }
+            most = __shfl_sync(0xffffffffu, end, 31);
+            tiles += __shfl_sync(0xffffffffu, n, 31);
+        }
+    }
+    __syncthreads();
+    const int total = pref[args.G];
+    const int rank = S > 1 ? static_cast<int>(blockIdx.x) % S : 0;
+    const int first = static_cast<int>(blockIdx.x) / S, step = static_cast<int>(gridDim.x) / S;
+
+    // Tile w of run g.  Within a run, bands of up to 16 column tiles are
+    // walked column tile first, so that the blocks at work at one time share
+    // both operands' rows in L2.
+    auto locate = [&](int w, int &g, Tile &t) {
+        while (w >= pref[g + 1]) ++g;
+        const int begin = offs[g], run = offs[g + 1] - begin;
+        const int ext = DW ? args.cols : run;
+        const int ct = (ext + TC - 1) / TC;
+        constexpr int kBand = 16;
+        const int r = w - pref[g];
+        const int band = r / (kBand * lane_tiles);
+        const int rb = r - band * kBand * lane_tiles;
+        const int bw = min(kBand, ct - band * kBand);
+        const int li = rb / bw, ci = band * kBand + rb - li * bw;
+        constexpr int kRound = DW ? 64 : 16;
+        const int each = ((ext + ct - 1) / ct + kRound - 1) / kRound * kRound;
+        t.g = g;
+        t.lane0 = li * kLanes;
+        t.cols = min(each, ext - ci * each);
+        t.width = (t.cols + kRound - 1) / kRound * kRound;
+        t.tok0 = begin;
+        t.tok_n = run;
+        if constexpr (DW) {
+            t.col0 = ci * each;
+            t.kb0 = 0;
+            t.nkb = (run + KB - 1) / KB;
+        } else {
+            t.col0 = begin + ci * each;
+            const int lo = rank * args.kblocks / S, hi = (rank + 1) * args.kblocks / S;
+            t.kb0 = lo;
+            t.nkb = hi - lo;
+        }
+    };
+
+    auto cluster_sync = [&]() {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        ptx::cluster_wait();
+    };
+
+    if (warp == 0) {
+        // ---- producer
+        int g = 0, slot = 0;
+        uint32_t ph = 0;
+        int issued = 0;
+        bool dead = false;
+        for (int w = first; w < total; w += step) {
+            Tile t;
+            locate(w, g, t);
+            if (lane == 0 && !dead) {
+                constexpr int kPart = TC / 4;
+                const int parts = (t.width + kPart - 1) / kPart;
+                const bool whole = parts > 2;
+                const uint32_t col_bytes = DW ? static_cast<uint32_t>(t.width / 64) * 8192u
+                                              : (whole ? Sh::kColBytes : static_cast<uint32_t>(parts) * kPart * 128u);
+                for (int i = 0; i < t.nkb; ++i) {
+                    if (!bounded_wait(empty_bar(slot), ph ^ 1u, &abort_s)) {
+                        dead = true;
+                        break;
+                    }
+                    const uint32_t sl = ring + slot * Sh::kStage, sc = sl + kLaneBytes, bar = full_bar(slot);
+                    const int kx = (t.kb0 + i) * KB;
+                    ptx::mbar_arrive_expect_tx(bar, kLaneBytes + col_bytes);
+                    if constexpr (DW) {
+                        const int y = t.tok0 + kx;
+                        ptx::tma_load_2d(sl, &maps.lane, bar, t.lane0, y, ptx::l2_policy_evict_normal());
+                        ptx::tma_load_2d(sl + 8192u, &maps.lane, bar, t.lane0 + 64, y, ptx::l2_policy_evict_normal());
+                        for (int j = 0; j < t.width / 64; ++j)
+                            ptx::tma_load_2d(sc + j * 8192u, &maps.col, bar, t.col0 + 64 * j, y,
+                                             ptx::l2_policy_evict_normal());
+                    } else {
+                        if constexpr (LMN) {
+                            ptx::tma_load_3d(sl, &maps.lane, bar, t.lane0, kx, t.g, ptx::l2_policy_evict_normal());
+                            ptx::tma_load_3d(sl + 8192u, &maps.lane, bar, t.lane0 + 64, kx, t.g,
+                                             ptx::l2_policy_evict_normal());
+                        } else {
+                            ptx::tma_load_3d(sl, &maps.lane, bar, kx, t.lane0, t.g, ptx::l2_policy_evict_normal());
+                        }
+                        if (whole) {
+                            ptx::tma_load_2d(sc, &maps.col, bar, kx, t.col0, ptx::l2_policy_evict_last());
+                        } else {
+                            for (int j = 0; j < parts; ++j)
+                                ptx::tma_load_2d(sc + j * kPart * 128u, &maps.col_part, bar, kx, t.col0 + j * kPart,
+                                                 ptx::l2_policy_evict_last());
+                        }
+                    }
+                    ++issued;
+                    if (++slot == stages) {
+                        slot = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (S > 1) {
+                __syncwarp();
+                cluster_sync();
+                cluster_sync();
+            }
+        }
+        if (lane == 0) {
+            // every load has landed before the block may leave
+            for (int i = 0; i < min(stages, issued); ++i) {
+                if (--slot < 0) {
+                    slot = stages - 1;
+                    ph ^= 1u;
+                }
+                ptx::mbar_wait_bounded(full_bar(slot), ph, kWaitLimitNs);
+            }
+        }
+    } else if (warp == 1) {
+        // ---- MMA issuer
+        int g = 0, slot = 0, buf = 0;
+        uint32_t ph = 0, aph = 0, fixes = 0;
+        bool dead = false;
+        for (int w = first; w < total; w += step) {
+            Tile t;
+            locate(w, g, t);
+            if (lane == 0 && !dead) {
+                uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(t.width >> 3) << 17) | ((kLanes >> 4) << 24);
+                if (!FP8 && args.bf16) idesc |= (1u << 7) | (1u << 10);
+                if (LMN) idesc |= 1u << 15;
+                if (DW) idesc |= 1u << 16;
+                for (int i = 0; i < t.nkb && !dead; ++i) {
+                    const bool unit_start = i % UNIT == 0, unit_end = i % UNIT == UNIT - 1 || i == t.nkb - 1;
+                    if (unit_start && !bounded_wait(acc_empty(buf), aph ^ 1u, &abort_s)) dead = true;
+                    if (dead || !bounded_wait(full_bar(slot), ph, &abort_s)) {
+                        dead = true;
+                        break;
+                    }
+                    int steps = 4;
+                    if constexpr (DW) {
+                        const int rem = t.tok_n - i * KB;
+                        if (rem < KB) {
+                            steps = (rem + 15) / 16;
+                            if (rem % 16) {
+                                if (!bounded_wait(fix_bar(slot), (fixes >> slot) & 1u, &abort_s)) {
+                                    dead = true;
+                                    break;
+                                }
+                                fixes ^= 1u << slot;   // the slot's next repair is its next phase
+                            }
+                        }
+                    }
+                    ptx::tc_fence_after_sync();
+                    const uint32_t sl = ring + slot * Sh::kStage, sc = sl + kLaneBytes;
+                    const uint64_t a0 = LMN ? ptx::sdesc_mnmajor_sw128(sl, 8192u) : ptx::sdesc_kmajor_sw128(sl);
+                    const uint64_t b0 = DW ? ptx::sdesc_mnmajor_sw128(sc, 8192u) : ptx::sdesc_kmajor_sw128(sc);
+                    const uint32_t d = tmem + static_cast<uint32_t>(buf * TC);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (DW && k >= steps) break;
+                        const uint32_t accumulate = unit_start && k == 0 ? 0u : 1u;
+                        const uint64_t a = a0 + static_cast<uint64_t>((LMN ? 128u : 2u) * k);
+                        const uint64_t b = b0 + static_cast<uint64_t>((DW ? 128u : 2u) * k);
+                        if constexpr (FP8)
+                            ptx::mma_f8(d, a, b, idesc, accumulate);
+                        else
+                            ptx::mma_f16(d, a, b, idesc, accumulate);
+                    }
+                    ptx::mma_commit(empty_bar(slot));
+                    if (unit_end) {
+                        ptx::mma_commit(acc_full(buf));
+                        if (++buf == Sh::kAcc) {
+                            buf = 0;
+                            aph ^= 1u;
+                        }
+                    }
+                    if (++slot == stages) {
+                        slot = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (S > 1) {
+                __syncwarp();
+                cluster_sync();
+                cluster_sync();
+            }
+        }
+        if (lane == 0) {
+            ptx::mma_commit(drain_bar);
+            ptx::mbar_wait_bounded(drain_bar, 0, kWaitLimitNs);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ---- kFp8: scales; kDw: the run's last rows
+        int g = 0, slot = 0;
+        uint32_t ph = 0;
+        bool dead = false;
+        for (int w = first; w < total; w += step) {
+            Tile t;
+            locate(w, g, t);
+            if constexpr (FP8) {
+                constexpr int PER = TC / 32, BATCH = 4;
+                const float *const sb = args.sb + (static_cast<size_t>(t.g) * lane_tiles + t.lane0 / kLanes) * args.kblocks + t.kb0;
+                const float *sa[PER];
+#pragma unroll
+                for (int p = 0; p < PER; ++p) {
+                    const int c = min(p * 32 + lane, t.cols - 1);   // columns past the tile's repeat its last
+                    sa[p] = args.sa + static_cast<size_t>(t.col0 + c) * args.kblocks + t.kb0;
+                }
+                float next[PER][BATCH];
+                auto fetch = [&](int b) {
+#pragma unroll
+                    for (int j = 0; j < BATCH; ++j) {
+                        const int kb = min(b + j, t.nkb - 1);
+                        const float f = __ldg(sb + kb);
+#pragma unroll
+                        for (int p = 0; p < PER; ++p) next[p][j] = __ldg(sa[p] + kb) * f;
+                    }
+                };
+                fetch(0);
+                for (int b = 0; b < t.nkb && !dead; b += BATCH) {
+                    float now[PER][BATCH];
+#pragma unroll
+                    for (int j = 0; j < BATCH; ++j)
+#pragma unroll
+                        for (int p = 0; p < PER; ++p) now[p][j] = next[p][j];
+                    if (b + BATCH < t.nkb) fetch(b + BATCH);
+#pragma unroll
+                    for (int j = 0; j < BATCH; ++j) {
+                        if (b + j >= t.nkb || dead) break;
+                        if (!__all_sync(0xffffffffu, bounded_wait(scale_empty(slot), ph ^ 1u, &abort_s))) {
+                            dead = true;
+                            break;
+                        }
+#pragma unroll
+                        for (int p = 0; p < PER; ++p) scale_buf[slot * TC + p * 32 + lane] = now[p][j];
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(scale_full(slot));
+                        if (++slot == kScaleRing) {
+                            slot = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+            } else if constexpr (DW) {
+                // every k-block in turn: a barrier's parity tells only
+                // neighbouring phases apart, so this warp is one of the two
+                // that free a slot
+                for (int i = 0; i < t.nkb && !dead; ++i) {
+                    if (!__all_sync(0xffffffffu, bounded_wait(full_bar(slot), ph, &abort_s))) {
+                        dead = true;
+                        break;
+                    }
+                    const int rem = t.tok_n - i * KB;
+                    if (rem < KB && rem % 16) {
+                        const int rows = 16 - rem % 16;       // up to the MMA's step of 16
+                        const int boxes = 2 + t.width / 64;   // each [64 rows][128 bytes], lanes' then columns'
+                        const uint32_t sl = ring + slot * Sh::kStage;
+                        for (int j = lane; j < boxes * rows * 8; j += 32) {
+                            const int box = j / (rows * 8), in = j - box * rows * 8;
+                            ptx::st_shared_v4(sl + box * 8192u + rem * 128u + in * 16u, 0u, 0u, 0u, 0u);
+                        }
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(fix_bar(slot));
+                    }
+                    if (lane == 0) ptx::mbar_arrive(empty_bar(slot));
+                    if (++slot == stages) {
+                        slot = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (S > 1) {
+                __syncwarp();
+                cluster_sync();
+                cluster_sync();
+            }
+        }
+    } else if (warp == 3) {
+        if (S > 1) {
+            for (int w = first; w < total; w += step) {
+                cluster_sync();
+                cluster_sync();
+            }
+        }
+    } else {
+        // ---- epilogue
+        const int quarter = warp & 3, half = (warp >> 2) - 1;
+        const int c_lo = half * HALF;
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(c_lo);
+        const int my = quarter * 32 + lane;             // the thread's lane of the tile
+        int g = 0, buf = 0, slot = 0;
+        uint32_t aph = 0, ph = 0;
+        bool dead = false;
+        for (int w = first; w < total; w += step) {
+            Tile t;
+            locate(w, g, t);
+            const size_t pitch = static_cast<size_t>(args.lanes);
+            const size_t out0 = (DW ? static_cast<size_t>(t.g) * args.cols + t.col0 : static_cast<size_t>(t.col0)) * pitch +
+                                t.lane0 + my;
+            const bool live = t.lane0 + my < args.lanes;
+            auto emit = [&](int c, float v) {
+                if (S > 1)
+                    sum_buf[c * kLanes + my] = v;
+                else if (live && c < t.cols)
+                    store_out(args.out, args.out_type, out0 + static_cast<size_t>(c) * pitch, v);
+            };
+            if constexpr (SUMS) {
+                float acc[HALF];
+#pragma unroll
+                for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
+                for (int i = 0; i < t.nkb && !dead; i += UNIT) {
+                    bool ok = bounded_wait(acc_full(buf), aph, &abort_s);
+                    if (FP8) ok = ok && bounded_wait(scale_full(slot), ph, &abort_s);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        dead = true;
+                        break;
+                    }
+                    ptx::tc_fence_after_sync();
+#pragma unroll
+                    for (int c = 0; c < HALF; c += CHUNK) {
+                        if (c_lo + c < t.width) {
+                            uint32_t v[CHUNK];
+                            if constexpr (CHUNK == 32)
+                                ptx::tmem_ld_32x32b_x32(lane_addr + static_cast<uint32_t>(buf * TC + c), v);
+                            else
+                                ptx::tmem_ld_32x32b_x16(lane_addr + static_cast<uint32_t>(buf * TC + c), v);
+                            const float4 *const s4 = reinterpret_cast<const float4 *>(scale_buf + slot * TC + c_lo + c);
+#pragma unroll
+                            for (int j = 0; j < CHUNK / 4; ++j) {
+                                const float4 s = FP8 ? s4[j] : make_float4(1.f, 1.f, 1.f, 1.f);
+                                acc[c + 4 * j] = fmaf(__uint_as_float(v[4 * j]), s.x, acc[c + 4 * j]);
+                                acc[c + 4 * j + 1] = fmaf(__uint_as_float(v[4 * j + 1]), s.y, acc[c + 4 * j + 1]);
+                                acc[c + 4 * j + 2] = fmaf(__uint_as_float(v[4 * j + 2]), s.z, acc[c + 4 * j + 2]);
+                                acc[c + 4 * j + 3] = fmaf(__uint_as_float(v[4 * j + 3]), s.w, acc[c + 4 * j + 3]);
+                            }
+                        }
+                    }
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::mbar_arrive(acc_empty(buf));
+                        if (FP8) ptx::mbar_arrive(scale_empty(slot));
+                    }
+                    if (++buf == Sh::kAcc) {
+                        buf = 0;
+                        aph ^= 1u;
+                    }
+                    if (FP8 && ++slot == kScaleRing) {
+                        slot = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (!dead) {
+#pragma unroll
+                    for (int j = 0; j < HALF; ++j) emit(c_lo + j, acc[j]);
+                }
+            } else {
+                const bool any = t.nkb > 0;             // kDw: a run without rows has zero gradients
+                if (any && !dead && !__all_sync(0xffffffffu, bounded_wait(acc_full(buf), aph, &abort_s))) dead = true;
+                if (!dead) {
+                    ptx::tc_fence_after_sync();
+#pragma unroll 1
+                    for (int c = 0; c < HALF; c += CHUNK) {
+                        if (c_lo + c >= t.width) break;
+                        uint32_t v[CHUNK];
+                        if (any) {
+                            if constexpr (CHUNK == 32)
+                                ptx::tmem_ld_32x32b_x32(lane_addr + static_cast<uint32_t>(buf * TC + c), v);
+                            else
+                                ptx::tmem_ld_32x32b_x16(lane_addr + static_cast<uint32_t>(buf * TC + c), v);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < CHUNK; ++j) v[j] = 0u;
+                        }
+#pragma unroll
+                        for (int j = 0; j < CHUNK; ++j) emit(c_lo + c + j, __uint_as_float(v[j]));
+                    }
+                    if (any) {
+                        ptx::tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(acc_empty(buf));
+                        if (++buf == Sh::kAcc) {
+                            buf = 0;
+                            aph ^= 1u;
+                        }
+                    }
+                }
+            }
+            if (S > 1) {
+                __syncwarp();
+                cluster_sync();                        // every rank's sums stand in its shared memory
+                for (int c = rank + S * half; c < t.cols; c += 2 * S) {
+                    const uint32_t at = ptx::smem_addr(sum_buf + c * kLanes + my);
+                    float v = 0.f;
+                    for (int r = 0; r < S; ++r) {
+                        float x;
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(ptx::mapa(at, r)) : "memory");
+                        v = r == 0 ? x : v + x;
+                    }
+                    if (live) store_out(args.out, args.out_type, out0 + static_cast<size_t>(c) * pitch, v);
+                }
+                cluster_sync();                        // and may be overwritten
+            }
+        }
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc(tmem, Sh::kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+bool encode(CUtensorMap *map, CUtensorMapDataType type, int elem, int rank, const void *ptr, const uint64_t *dims,
+            const uint32_t *box)
+{
+    auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+    if (!fn) {
+        note_message("cuTensorMapEncodeTiled is not available from the driver", 0);
+        return false;
+    }
+    cuuint64_t d[3], strides[2];
+    cuuint32_t b[3], estr[3] = {1, 1, 1};
+    uint64_t s = elem;
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        s *= dims[i];
+        if (i + 1 < rank) strides[i] = s;
+    }
+    const CUresult r = fn(map, type, rank, const_cast<void *>(ptr), d, strides, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) note_message("cuTensorMapEncodeTiled (grouped operands) failed", static_cast<int>(r));
+    return r == CUDA_SUCCESS;
+}
+
+template <int FORM, int TC, bool SUMS>
+cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int sms, cudaStream_t stream)
+{
+    using Sh = Shape<TC>;
+    constexpr bool FP8 = FORM == kFp8, DW = FORM == kDw;
+    constexpr int KB = FP8 ? 128 : 64, elem = FP8 ? 1 : 2;
+    const CUtensorMapDataType type = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                         : p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    Maps maps;
+    const uint64_t T = static_cast<uint64_t>(std::max<int64_t>(p.T, 1)), G = p.G, N = p.N, K = p.K;
+    bool ok;
+    if (DW) {
+        const uint64_t da[2] = {K, T}, dd[2] = {N, T};
+        const uint32_t box[2] = {64, 64};
+        ok = encode(&maps.lane, type, elem, 2, p.A, da, box) && encode(&maps.col, type, elem, 2, p.B, dd, box);
+        maps.col_part = maps.col;
+    } else {
+        const uint64_t da[2] = {K, T};
+        const uint64_t dn[3] = {K, N, G}, dk[3] = {N, K, G};
+        const uint32_t ba[2] = {KB, TC}, bp[2] = {KB, TC / 4}, bn[3] = {KB, kLanes, 1}, bk[3] = {64, 64, 1};
+        ok = (FORM == kKn ? encode(&maps.lane, type, elem, 3, p.B, dk, bk)
+                          : encode(&maps.lane, type, elem, 3, p.B, dn, bn)) &&
+             encode(&maps.col, type, elem, 2, p.A, da, ba) && encode(&maps.col_part, type, elem, 2, p.A, da, bp);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    GroupedArgs a = {};
+    a.offsets = p.offsets;
+    a.sa = p.sa;
+    a.sb = p.sb;
+    a.out = p.out;
+    a.T = static_cast<int>(p.T);
+    a.G = static_cast<int>(p.G);
+    a.lanes = static_cast<int>(DW ? p.K : p.N);
+    a.cols = static_cast<int>(p.N);
+    a.K = static_cast<int>(p.K);
+    a.kblocks = static_cast<int>((p.K + KB - 1) / KB);
+    a.out_type = p.out_type;
+    a.bf16 = p.bf16;
+    a.splits = splits;
+    const uint32_t sums = splits > 1 ? TC * kLanes * 4 : 0, scales = FP8 ? kScaleRing * TC * 4 : 0;
+    const uint32_t tables = (static_cast<uint32_t>(2 * (p.G + 1)) * 4 + 127) / 128 * 128;
+    const uint32_t rest = sums + scales + tables;
+    const uint32_t room = static_cast<uint32_t>(kSmemLimit) - 1024 - rest;
+    a.stages = static_cast<int>(std::min<uint32_t>(kMaxRing, room / Sh::kStage));
+    a.sum_off = a.stages * Sh::kStage;
+    a.scale_off = a.sum_off + sums;
+    a.table_off = a.scale_off + scales;
+    // enough shared memory that the blocks sharing an SM never ask for more
+    // than its 512 tensor-memory columns (tmem_fits)
+    const size_t smem = kSmemLimit;
+    const void *fn = reinterpret_cast<const void *>(grouped_kernel<FORM, TC, SUMS>);
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return note_error(e, "cudaFuncSetAttribute(grouped_kernel)");
+    cudaLaunchConfig_t cfg = {};
+    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(tiles, sms / splits));
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * splits), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = splits > 1 ? 2 : 1;
+    return note_error(cudaLaunchKernelEx(&cfg, grouped_kernel<FORM, TC, SUMS>, maps, a), "cudaLaunchKernelEx(grouped_kernel)");
+}
+
+template <int FORM, int TC>
+cudaError_t launch_form(const GroupedProblem &p, int splits, int64_t tiles, int sms, cudaStream_t stream)
+{
+    if constexpr (FORM != kFp8)
+        if (p.out_type != 0) return launch_tiles<FORM, TC, false>(p, splits, tiles, sms, stream);
+    return launch_tiles<FORM, TC, true>(p, splits, tiles, sms, stream);
+}
+
+}  // namespace
+
+int64_t grouped_tiles(const GroupedProblem &p, int tc)
+{
+    if (p.form == GroupedForm::kDw) return p.G * ((p.K + kLanes - 1) / kLanes) * ((p.N + tc - 1) / tc);
+    // a run of c rows has ceil(c / tc) column tiles: at most T / tc of them full, and one more each
+    const int64_t runs = std::min<int64_t>(p.G, p.T);
+    return ((p.N + kLanes - 1) / kLanes) * (p.G == 1 ? (p.T + tc - 1) / tc : p.T / tc + runs);
+}
+
+GroupedPlan plan_grouped(const GroupedProblem &p, int sms)
+{
+    GroupedPlan plan = {128, 1};
+    if (p.form != GroupedForm::kDw && p.T <= 32 * p.G) {
+        plan.tc = 32;
+        const int64_t tiles = grouped_tiles(p, 32);
+        const int64_t kb = (p.K + (p.form == GroupedForm::kFp8 ? 127 : 63)) / (p.form == GroupedForm::kFp8 ? 128 : 64);
+        while (plan.splits < 8 && tiles * plan.splits * 2 <= sms && kb >= plan.splits * 4) plan.splits *= 2;
+    }
+    return plan;
+}
+
+cudaError_t launch_grouped(const GroupedProblem &p, cudaStream_t stream)
+{
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return note_error(e, "cudaDeviceGetAttribute(MultiProcessorCount)");
+    const GroupedPlan plan = plan_grouped(p, sms);
+    const int64_t tiles = grouped_tiles(p, plan.tc);
+    const bool small = plan.tc == 32;
+    switch (p.form) {
+    case GroupedForm::kFp8:
+        return small ? launch_form<kFp8, 32>(p, plan.splits, tiles, sms, stream)
+                     : launch_form<kFp8, 128>(p, plan.splits, tiles, sms, stream);
+    case GroupedForm::kNk:
+        return small ? launch_form<kNk, 32>(p, plan.splits, tiles, sms, stream)
+                     : launch_form<kNk, 128>(p, plan.splits, tiles, sms, stream);
+    case GroupedForm::kKn:
+        return small ? launch_form<kKn, 32>(p, plan.splits, tiles, sms, stream)
+                     : launch_form<kKn, 128>(p, plan.splits, tiles, sms, stream);
+    default: return launch_form<kDw, 128>(p, plan.splits, tiles, sms, stream);
+    }
+}
+
+cudaError_t read_and_clear_grouped_status(unsigned *status)
+{
+    const unsigned zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(status, g_grouped_status, sizeof *status);
+    if (e == cudaSuccess && *status) e = cudaMemcpyToSymbol(g_grouped_status, &zero, sizeof zero);
+    return note_error(e, "reading the grouped kernels' status word");
+}
+
+}  // namespace splitk

@@ -108,6 +108,54 @@ cudaError_t launch_reduce(const float *P, float *out, int64_t S, int64_t count, 
                           cudaStream_t stream);
 cudaError_t launch_prepare(const void *W, void *B, int64_t K, int64_t N, int elem_bytes, cudaStream_t stream);
 
+
+// The operators on 8-bit operands and on rows grouped by expert.
+enum class GroupedForm { kFp8, kNk, kKn, kDw };
+
+// out = A B^T per run of rows (splitk_grouped.cu says which product each form
+// is).  A [T,K]; B [G,N,K], kKn [G,K,N], kDw the output's gradient [T,N];
+// out [T,N], kDw [G,N,K].
+struct GroupedProblem {
+    GroupedForm form;
+    const void *A, *B;
+    const float *sa, *sb;      // kFp8: [T,ceil(K/128)] and [G,ceil(N/128),ceil(K/128)]
+    const int *offsets;        // device, [G+1]; nullptr: one run of T rows (G == 1)
+    void *out;
+    int64_t T, G, N, K;
+    int out_type;              // splitk_dtype
+    bool bf16;                 // 16-bit operands: BF16 (else F16)
+};
+struct GroupedPlan {
+    int tc;                    // columns of a tile
+    int splits;                // thread blocks of a cluster, along K
+};
+GroupedPlan plan_grouped(const GroupedProblem &p, int sms);
+// Tiles of the problem at `tc` columns each: exact for one run and for kDw, an
+// upper bound for ragged runs.
+int64_t grouped_tiles(const GroupedProblem &p, int tc);
+cudaError_t launch_grouped(const GroupedProblem &p, cudaStream_t stream);
+// (the stream has been synchronised)
+cudaError_t read_and_clear_grouped_status(unsigned *status);
+
+// Rows of [M,K] to 8 bits with a scale for each 128 values, after the
+// residual's addition and the root-mean-square norm (weight != nullptr) or as
+// they are.  residual, sum and y may be nullptr.
+struct RowsProblem {
+    const void *x, *residual, *weight;
+    void *sum, *y, *q;
+    float *scales;
+    int64_t M, K;
+    float eps;
+    int dtype;
+};
+cudaError_t launch_rows_fp8(const RowsProblem &p, cudaStream_t stream);
+// Weights [G,N,K] to 8 bits with a scale for each 128 x 128 block.
+cudaError_t launch_prepare_fp8(const void *B, void *q, float *scales, int64_t G, int64_t N, int64_t K, int dtype,
+                               cudaStream_t stream);
+
+// The driver's cuTensorMapEncodeTiled (PFN_cuTensorMapEncodeTiled_v12000), or nullptr.
+void *tensor_map_encoder();
+
 // A byte range [lo, hi) of device memory that a launch reads or writes.
 struct Span {
     uintptr_t lo, hi;
