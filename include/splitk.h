@@ -365,7 +365,8 @@ int splitk_autotune_splits(const void *A, const void *B, float *out,
  * Every tensor is dense and row-major; rows follow one another without
  * padding.  K is a positive multiple of 16 with 8-bit operands and of 8 with
  * 16-bit ones, whatever N and M (or T) are, unless said otherwise.  M (or T)
- * may be 0: nothing is written then, except by gemm_grouped_dw.  M, T, N, K <=
+ * may be 0: nothing is written then, except by gemm_grouped_dw, and the
+ * tensors without elements may be NULL.  M, T, N, K <=
  * SPLITK_MAX_DIM, G <= SPLITK_MAX_GROUPS (else SPLITK_ERR_SHAPE).  Pointers are
  * 16-byte aligned (`offsets`: 4-byte), outputs overlap nothing (exceptions are
  * named), and out_dtype is SPLITK_F32, _F16 or _BF16, rounded once from the

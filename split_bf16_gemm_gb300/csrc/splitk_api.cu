@@ -444,15 +444,16 @@ struct Extent {
     uint64_t bytes;
 };
 
-// NULL and alignment of every pointer, then each output against the inputs and
-// the other outputs.  `in_place` (may be -1): the one output that may be
-// exactly one of the inputs (same address; the extents are equal).
+// NULL and alignment of every pointer (a tensor without elements may be NULL),
+// then each output against the inputs and the other outputs.  `in_place` (may
+// be -1): the one output that may be exactly one of the inputs (same address
+// and extent).
 int validate_extents(const Extent *in, int n_in, const Extent *out, int n_out, int in_place = -1)
 {
     for (int i = 0; i < n_in; ++i)
-        if (!in[i].p) return SPLITK_ERR_NULL;
+        if (!in[i].p && in[i].bytes) return SPLITK_ERR_NULL;
     for (int i = 0; i < n_out; ++i)
-        if (!out[i].p) return SPLITK_ERR_NULL;
+        if (!out[i].p && out[i].bytes) return SPLITK_ERR_NULL;
     for (int i = 0; i < n_in; ++i)
         if (!aligned16(in[i].p)) return SPLITK_ERR_ALIGN;
     for (int i = 0; i < n_out; ++i)

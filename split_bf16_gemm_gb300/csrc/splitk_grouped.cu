@@ -675,12 +675,15 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
     const CUtensorMapDataType type = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                          : p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     Maps maps;
+    // without rows (kDw writes its zeros all the same) nothing is loaded; the
+    // maps describe memory that exists
+    const void *const A = p.T ? p.A : p.out, *const D = p.T ? p.B : p.out;
     const uint64_t T = static_cast<uint64_t>(std::max<int64_t>(p.T, 1)), G = p.G, N = p.N, K = p.K;
     bool ok;
     if (DW) {
         const uint64_t da[2] = {K, T}, dd[2] = {N, T};
         const uint32_t box[2] = {64, 64};
-        ok = encode(&maps.lane, type, elem, 2, p.A, da, box) && encode(&maps.col, type, elem, 2, p.B, dd, box);
+        ok = encode(&maps.lane, type, elem, 2, A, da, box) && encode(&maps.col, type, elem, 2, D, dd, box);
         maps.col_part = maps.col;
     } else {
         const uint64_t da[2] = {K, T};
