@@ -62,12 +62,20 @@ constexpr int kUnit = 8;   // k-blocks (512 values of K) between additions in re
 
 enum Form { kFp8, kNk, kKn, kDw };
 
+// TC: columns of a tile.  256 is a pair of blocks (cta_group::2) whose tile is
+// 256 lanes, 128 to a block, by 256 columns, half of whose operand each block
+// loads: 32 KB a k-block and block for four times the products of the 32 KB
+// that a 128 x 128 tile takes.
 template <int TC>
 struct Shape {
+    static constexpr bool kPair = TC == 256;
+    static constexpr int kBlocks = kPair ? 2 : 1;
     static constexpr int kAcc = TC <= 32 ? 4 : 2;                 // accumulators in tensor memory
     static constexpr int kTmemCols = kAcc * TC;
-    static constexpr uint32_t kColBytes = TC * 128;
+    static constexpr int kLoadCols = TC / kBlocks;                // columns a block loads
+    static constexpr uint32_t kColBytes = kLoadCols * 128;
     static constexpr uint32_t kStage = kLaneBytes + kColBytes;
+    static constexpr int kTileLanes = kLanes * kBlocks;
 };
 
 struct GroupedArgs {
@@ -85,7 +93,7 @@ struct GroupedArgs {
 };
 
 struct Maps {
-    CUtensorMap lane, col, col_part;   // col_part: TC / 4 rows instead of TC
+    CUtensorMap lane, col, col_part;   // col_part: a quarter of col's rows
 };
 
 struct Tile {
@@ -96,16 +104,23 @@ struct Tile {
     int tok0, tok_n;           // kDw: the run
 };
 
+// RELAXED: a barrier that guards tensor memory and that the other block of a
+// pair arrives on
+template <bool RELAXED = false>
 __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, volatile unsigned *abort)
 {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = ptx::globaltimer_ns();
+    auto ready = [&] { return RELAXED ? ptx::mbar_try_wait_cluster_relaxed(bar, parity) : ptx::mbar_try_wait(bar, parity); };
+    uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
-        if (ptx::mbar_try_wait(bar, parity)) return true;
-        if ((i & 63u) == 0 && (*abort || ptx::globaltimer_ns() - t0 > kWaitLimitNs)) {
-            *abort = 1u;
-            atomicOr(&g_grouped_status, 1u);
-            return false;
+        if (ready()) return true;
+        if ((i & 63u) == 0) {              // the timer is slow to read: not on short waits
+            const uint64_t now = ptx::globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (*abort || now - t0 > kWaitLimitNs) {
+                *abort = 1u;
+                atomicOr(&g_grouped_status, 1u);
+                return false;
+            }
         }
     }
 }
@@ -127,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     using Sh = Shape<TC>;
     constexpr bool FP8 = FORM == kFp8, DW = FORM == kDw;
     constexpr bool LMN = FORM == kKn || FORM == kDw;   // lane operand contiguous along its lanes
+    constexpr bool PAIR = Sh::kPair;
     constexpr int KB = FP8 ? 128 : 64;
     constexpr int UNIT = FP8 ? 1 : SUMS ? kUnit : 1 << 30;   // k-blocks summed in one accumulator
     constexpr int HALF = TC / 2;                       // columns of an epilogue warp
@@ -152,21 +168,34 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     auto acc_empty = [&](int i) { return bar0 + 8u * (2 * kMaxRing + Sh::kAcc + i); };
     auto scale_full = [&](int i) { return bar0 + 8u * (2 * kMaxRing + 2 * Sh::kAcc + i); };
     auto scale_empty = [&](int i) { return bar0 + 8u * (2 * kMaxRing + 2 * Sh::kAcc + kScaleRing + i); };
-    auto fix_bar = [&](int i) { return bar0 + 8u * (2 * kMaxRing + 2 * Sh::kAcc + 2 * kScaleRing + i); };   // kDw
-    const uint32_t drain_bar = fix_bar(kMaxRing);
+    auto tail_bar = [&](int i) { return bar0 + 8u * (2 * kMaxRing + 2 * Sh::kAcc + 2 * kScaleRing + i); };   // kDw
+    const uint32_t drain_bar = tail_bar(kMaxRing);
+    const int peer = PAIR ? static_cast<int>(blockIdx.x) & 1 : 0;   // 0: the block that issues the pair's MMAs
+    auto release_acc = [&](uint32_t bar) {
+        if constexpr (PAIR)
+            ptx::mbar_arrive_cluster_relaxed(ptx::mapa(bar, 0));
+        else
+            ptx::mbar_arrive(bar);
+    };
+    auto cluster_sync = [&]() {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        ptx::cluster_wait();
+    };
     const int stages = args.stages, S = args.splits;
 
     if (tid == 0) {
         ptx::prefetch_tensormap(&maps.lane);
         ptx::prefetch_tensormap(&maps.col);
         for (int i = 0; i < stages; ++i) {
-            ptx::mbar_init(full_bar(i), 1);
-            ptx::mbar_init(empty_bar(i), DW ? 2 : 1);
-            ptx::mbar_init(fix_bar(i), 1);
+            // kDw: one arrival a block, by its producer or, where it repairs
+            // the stage first, by its warp 2
+            ptx::mbar_init(full_bar(i), DW ? Sh::kBlocks : 1);
+            ptx::mbar_init(empty_bar(i), 1);
+            ptx::mbar_init(tail_bar(i), 1);
         }
         for (int i = 0; i < Sh::kAcc; ++i) {
             ptx::mbar_init(acc_full(i), 1);
-            ptx::mbar_init(acc_empty(i), kEpilogueWarps);
+            ptx::mbar_init(acc_empty(i), kEpilogueWarps * Sh::kBlocks);
         }
         for (int i = 0; i < kScaleRing; ++i) {
             ptx::mbar_init(scale_full(i), 1);
@@ -178,11 +207,17 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         ptx::fence_proxy_async_smem();
     }
     if (warp == 1) {
-        ptx::tmem_alloc(ptx::smem_addr(&tmem_slot), Sh::kTmemCols);
-        ptx::tmem_relinquish();
+        if constexpr (PAIR) {
+            ptx::tmem_alloc_pair(ptx::smem_addr(&tmem_slot), Sh::kTmemCols);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(ptx::smem_addr(&tmem_slot), Sh::kTmemCols);
+            ptx::tmem_relinquish();
+        }
     }
     ptx::tc_fence_before_sync();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync();   // the other block's barriers are set up
     ptx::tc_fence_after_sync();
     const uint32_t tmem = tmem_slot;
     // the next launch's blocks may set up now (every block here holds its
@@ -192,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
 
     // ---- the runs, made monotone and within [0, T] whatever the offsets
     // hold, and the number of tiles before each
-    const int lane_tiles = (args.lanes + kLanes - 1) / kLanes;
+    const int lane_tiles = (args.lanes + Sh::kTileLanes - 1) / Sh::kTileLanes;
     if (args.offsets == nullptr) {
         if (tid < 2) offs[tid] = tid ? args.T : 0;
     } else {
@@ -232,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     __syncthreads();
     const int total = pref[args.G];
     const int rank = S > 1 ? static_cast<int>(blockIdx.x) % S : 0;
-    const int first = static_cast<int>(blockIdx.x) / S, step = static_cast<int>(gridDim.x) / S;
+    const int group = PAIR ? 2 : S;                   // blocks at work on a tile
+    const int first = static_cast<int>(blockIdx.x) / group, step = static_cast<int>(gridDim.x) / group;
 
     // Tile w of run g.  Within a run, bands of up to 16 column tiles are
     // walked column tile first, so that the blocks at work at one time share
@@ -248,10 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         const int rb = r - band * kBand * lane_tiles;
         const int bw = min(kBand, ct - band * kBand);
         const int li = rb / bw, ci = band * kBand + rb - li * bw;
-        constexpr int kRound = DW ? 64 : 16;
+        constexpr int kRound = (DW ? 64 : 16) * Sh::kBlocks;
         const int each = ((ext + ct - 1) / ct + kRound - 1) / kRound * kRound;
         t.g = g;
-        t.lane0 = li * kLanes;
+        t.lane0 = li * Sh::kTileLanes + peer * kLanes;
         t.cols = min(each, ext - ci * each);
         t.width = (t.cols + kRound - 1) / kRound * kRound;
         t.tok0 = begin;
@@ -268,57 +304,85 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         }
     };
 
-    auto cluster_sync = [&]() {
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        ptx::cluster_wait();
-    };
-
+    // 384 threads start with 168 registers each; TC = 256 sums need more than
+    // that in warps 4-11: 4 * 32 * 80 + 8 * 32 * 208 <= 384 * 168
+    constexpr bool kMoveRegs = SUMS && TC == 256;
+    if (kMoveRegs && warp < 4) ptx::regs_down<80>();
     if (warp == 0) {
         // ---- producer
         int g = 0, slot = 0;
         uint32_t ph = 0;
         int issued = 0;
         bool dead = false;
+        const uint64_t once = ptx::l2_policy_evict_normal(), again = ptx::l2_policy_evict_last();
+        const uint32_t full0 = PAIR ? ptx::mapa(full_bar(0), 0) : full_bar(0);   // the issuing block's
         for (int w = first; w < total; w += step) {
             Tile t;
             locate(w, g, t);
-            if (lane == 0 && !dead) {
-                constexpr int kPart = TC / 4;
-                const int parts = (t.width + kPart - 1) / kPart;
-                const bool whole = parts > 2;
-                const uint32_t col_bytes = DW ? static_cast<uint32_t>(t.width / 64) * 8192u
-                                              : (whole ? Sh::kColBytes : static_cast<uint32_t>(parts) * kPart * 128u);
+            if (!dead) {
+                constexpr int kPart = Sh::kLoadCols / 4;
+                const int load_cols = t.width / Sh::kBlocks;             // this block's part of the columns
+                const int col = t.col0 + peer * load_cols;
+                const int parts = DW ? load_cols / 64 : (load_cols + kPart - 1) / kPart;
+                const bool whole = !DW && parts > 2;
+                const uint32_t bytes = kLaneBytes + (DW ? static_cast<uint32_t>(parts) * 8192u
+                                                     : whole ? Sh::kColBytes
+                                                             : static_cast<uint32_t>(parts) * kPart * 128u);
+                auto load2 = [&](uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, uint64_t policy) {
+                    if constexpr (PAIR)
+                        ptx::tma_load_2d_pair(dst, map, bar, x, y, policy);
+                    else
+                        ptx::tma_load_2d(dst, map, bar, x, y, policy);
+                };
+                auto load3 = [&](uint32_t dst, uint32_t bar, int x, int y) {
+                    if constexpr (PAIR)
+                        ptx::tma_load_3d_pair(dst, &maps.lane, bar, x, y, t.g, once);
+                    else
+                        ptx::tma_load_3d(dst, &maps.lane, bar, x, y, t.g, once);
+                };
                 for (int i = 0; i < t.nkb; ++i) {
                     if (!bounded_wait(empty_bar(slot), ph ^ 1u, &abort_s)) {
                         dead = true;
                         break;
                     }
-                    const uint32_t sl = ring + slot * Sh::kStage, sc = sl + kLaneBytes, bar = full_bar(slot);
+                    // one lane issues; the whole warp walks the loop, so that
+                    // slots and coordinates stay in uniform registers
+                    if (ptx::elect_one()) {
+                    const uint32_t sl = ring + slot * Sh::kStage, sc = sl + kLaneBytes;
                     const int kx = (t.kb0 + i) * KB;
-                    ptx::mbar_arrive_expect_tx(bar, kLaneBytes + col_bytes);
+                    uint32_t bar = full0 + 8u * slot;
+                    const bool tail = DW && t.tok_n - kx < KB && (t.tok_n - kx) % 16 != 0;
+                    if (tail) {                              // to this block's warp 2 first
+                        bar = tail_bar(slot);
+                        ptx::mbar_arrive_expect_tx(bar, bytes);
+                        if constexpr (PAIR) bar = ptx::mapa(bar, peer);
+                    } else if (peer == 0) {
+                        ptx::mbar_arrive_expect_tx(full_bar(slot), bytes * Sh::kBlocks);
+                        if (DW && PAIR) ptx::mbar_arrive(full_bar(slot));
+                    }
                     if constexpr (DW) {
                         const int y = t.tok0 + kx;
-                        ptx::tma_load_2d(sl, &maps.lane, bar, t.lane0, y, ptx::l2_policy_evict_normal());
-                        ptx::tma_load_2d(sl + 8192u, &maps.lane, bar, t.lane0 + 64, y, ptx::l2_policy_evict_normal());
-                        for (int j = 0; j < t.width / 64; ++j)
-                            ptx::tma_load_2d(sc + j * 8192u, &maps.col, bar, t.col0 + 64 * j, y,
-                                             ptx::l2_policy_evict_normal());
+                        load2(sl, &maps.lane, bar, t.lane0, y, once);
+                        load2(sl + 8192u, &maps.lane, bar, t.lane0 + 64, y, once);
+                        for (int j = 0; j < parts; ++j)
+                            load2(sc + j * 8192u, &maps.col, bar, col + 64 * j, y, once);
                     } else {
                         if constexpr (LMN) {
-                            ptx::tma_load_3d(sl, &maps.lane, bar, t.lane0, kx, t.g, ptx::l2_policy_evict_normal());
-                            ptx::tma_load_3d(sl + 8192u, &maps.lane, bar, t.lane0 + 64, kx, t.g,
-                                             ptx::l2_policy_evict_normal());
+                            load3(sl, bar, t.lane0, kx);
+                            load3(sl + 8192u, bar, t.lane0 + 64, kx);
                         } else {
-                            ptx::tma_load_3d(sl, &maps.lane, bar, kx, t.lane0, t.g, ptx::l2_policy_evict_normal());
+                            load3(sl, bar, kx, t.lane0);
                         }
                         if (whole) {
-                            ptx::tma_load_2d(sc, &maps.col, bar, kx, t.col0, ptx::l2_policy_evict_last());
+                            load2(sc, &maps.col, bar, kx, col, again);
                         } else {
                             for (int j = 0; j < parts; ++j)
-                                ptx::tma_load_2d(sc + j * kPart * 128u, &maps.col_part, bar, kx, t.col0 + j * kPart,
-                                                 ptx::l2_policy_evict_last());
+                                load2(sc + j * kPart * 128u, &maps.col_part, bar, kx, col + j * kPart,
+                                      again);
                         }
                     }
+                    }
+                    __syncwarp();
                     ++issued;
                     if (++slot == stages) {
                         slot = 0;
@@ -332,8 +396,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                 cluster_sync();
             }
         }
-        if (lane == 0) {
-            // every load has landed before the block may leave
+        if (peer == 0) {
+            // every load has landed before the block may leave (the issuing
+            // block's barriers count the pair's)
             for (int i = 0; i < min(stages, issued); ++i) {
                 if (--slot < 0) {
                     slot = stages - 1;
@@ -345,19 +410,27 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     } else if (warp == 1) {
         // ---- MMA issuer
         int g = 0, slot = 0, buf = 0;
-        uint32_t ph = 0, aph = 0, fixes = 0;
+        uint32_t ph = 0, aph = 0;
         bool dead = false;
+        // One thread issues every MMA with no other to hide its latency: the
+        // descriptors are built once, and a slot or a K step is an addition to
+        // the low word, whose address field (bytes >> 4) never carries out.
+        const uint64_t a0 = LMN ? ptx::sdesc_mnmajor_sw128(ring, 8192u) : ptx::sdesc_kmajor_sw128(ring);
+        const uint64_t b0 = DW ? ptx::sdesc_mnmajor_sw128(ring + kLaneBytes, 8192u)
+                               : ptx::sdesc_kmajor_sw128(ring + kLaneBytes);
+        const uint32_t a_lo = static_cast<uint32_t>(a0), a_hi = static_cast<uint32_t>(a0 >> 32);
+        const uint32_t b_lo = static_cast<uint32_t>(b0), b_hi = static_cast<uint32_t>(b0 >> 32);
         for (int w = first; w < total; w += step) {
             Tile t;
             locate(w, g, t);
-            if (lane == 0 && !dead) {
-                uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(t.width >> 3) << 17) | ((kLanes >> 4) << 24);
+            if (!dead && peer == 0) {
+                uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(t.width >> 3) << 17) | ((Sh::kTileLanes >> 4) << 24);
                 if (!FP8 && args.bf16) idesc |= (1u << 7) | (1u << 10);
                 if (LMN) idesc |= 1u << 15;
                 if (DW) idesc |= 1u << 16;
                 for (int i = 0; i < t.nkb && !dead; ++i) {
                     const bool unit_start = i % UNIT == 0, unit_end = i % UNIT == UNIT - 1 || i == t.nkb - 1;
-                    if (unit_start && !bounded_wait(acc_empty(buf), aph ^ 1u, &abort_s)) dead = true;
+                    if (unit_start && !bounded_wait<PAIR>(acc_empty(buf), aph ^ 1u, &abort_s)) dead = true;
                     if (dead || !bounded_wait(full_bar(slot), ph, &abort_s)) {
                         dead = true;
                         break;
@@ -367,38 +440,41 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                         const int rem = t.tok_n - i * KB;
                         if (rem < KB) {
                             steps = (rem + 15) / 16;
-                            if (rem % 16) {
-                                if (!bounded_wait(fix_bar(slot), (fixes >> slot) & 1u, &abort_s)) {
-                                    dead = true;
-                                    break;
-                                }
-                                fixes ^= 1u << slot;   // the slot's next repair is its next phase
-                            }
+                            if (PAIR && rem % 16) ptx::fence_acquire_cluster();   // the other block's zeroed rows
                         }
                     }
                     ptx::tc_fence_after_sync();
-                    const uint32_t sl = ring + slot * Sh::kStage, sc = sl + kLaneBytes;
-                    const uint64_t a0 = LMN ? ptx::sdesc_mnmajor_sw128(sl, 8192u) : ptx::sdesc_kmajor_sw128(sl);
-                    const uint64_t b0 = DW ? ptx::sdesc_mnmajor_sw128(sc, 8192u) : ptx::sdesc_kmajor_sw128(sc);
+                    if (ptx::elect_one()) {
+                    const uint32_t at = static_cast<uint32_t>(slot) * (Sh::kStage >> 4);
                     const uint32_t d = tmem + static_cast<uint32_t>(buf * TC);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (DW && k >= steps) break;
                         const uint32_t accumulate = unit_start && k == 0 ? 0u : 1u;
-                        const uint64_t a = a0 + static_cast<uint64_t>((LMN ? 128u : 2u) * k);
-                        const uint64_t b = b0 + static_cast<uint64_t>((DW ? 128u : 2u) * k);
-                        if constexpr (FP8)
+                        const uint64_t a = ptx::desc64(a_lo + at + (LMN ? 128u : 2u) * k, a_hi);
+                        const uint64_t b = ptx::desc64(b_lo + at + (DW ? 128u : 2u) * k, b_hi);
+                        if constexpr (PAIR)
+                            ptx::mma_pair<FP8>(d, a, b, idesc, accumulate);
+                        else if constexpr (FP8)
                             ptx::mma_f8(d, a, b, idesc, accumulate);
                         else
                             ptx::mma_f16(d, a, b, idesc, accumulate);
                     }
-                    ptx::mma_commit(empty_bar(slot));
+                    if constexpr (PAIR)
+                        ptx::mma_commit_pair(empty_bar(slot));
+                    else
+                        ptx::mma_commit(empty_bar(slot));
                     if (unit_end) {
-                        ptx::mma_commit(acc_full(buf));
-                        if (++buf == Sh::kAcc) {
-                            buf = 0;
-                            aph ^= 1u;
-                        }
+                        if constexpr (PAIR)
+                            ptx::mma_commit_pair(acc_full(buf));
+                        else
+                            ptx::mma_commit(acc_full(buf));
+                    }
+                    }
+                    __syncwarp();
+                    if (unit_end && ++buf == Sh::kAcc) {
+                        buf = 0;
+                        aph ^= 1u;
                     }
                     if (++slot == stages) {
                         slot = 0;
@@ -412,22 +488,27 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                 cluster_sync();
             }
         }
-        if (lane == 0) {
-            ptx::mma_commit(drain_bar);
+        if (lane == 0 && peer == 0) {
+            if constexpr (PAIR)
+                ptx::mma_commit_pair(drain_bar);
+            else
+                ptx::mma_commit(drain_bar);
             ptx::mbar_wait_bounded(drain_bar, 0, kWaitLimitNs);
         }
         __syncwarp();
     } else if (warp == 2) {
         // ---- kFp8: scales; kDw: the run's last rows
         int g = 0, slot = 0;
-        uint32_t ph = 0;
+        uint32_t ph = 0;                                 // kDw: the phase of each slot's tail barrier, a bit each
         bool dead = false;
         for (int w = first; w < total; w += step) {
             Tile t;
             locate(w, g, t);
             if constexpr (FP8) {
-                constexpr int PER = TC / 32, BATCH = 4;
-                const float *const sb = args.sb + (static_cast<size_t>(t.g) * lane_tiles + t.lane0 / kLanes) * args.kblocks + t.kb0;
+                constexpr int PER = TC / 32, BATCH = PER > 4 ? 2 : 4;
+                const int lane_blocks = (args.lanes + kLanes - 1) / kLanes;
+                const int lb = min(t.lane0 / kLanes, lane_blocks - 1);   // a pair's second half may lie past the end
+                const float *const sb = args.sb + (static_cast<size_t>(t.g) * lane_blocks + lb) * args.kblocks + t.kb0;
                 const float *sa[PER];
 #pragma unroll
                 for (int p = 0; p < PER; ++p) {
@@ -470,33 +551,32 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                     }
                 }
             } else if constexpr (DW) {
-                // every k-block in turn: a barrier's parity tells only
-                // neighbouring phases apart, so this warp is one of the two
-                // that free a slot
-                for (int i = 0; i < t.nkb && !dead; ++i) {
-                    if (!__all_sync(0xffffffffu, bounded_wait(full_bar(slot), ph, &abort_s))) {
+                // a run's last k-block, where its rows end inside a step of 16
+                const int rem = t.tok_n - (t.nkb - 1) * KB;
+                if (t.nkb > 0 && rem % 16 && !dead) {
+                    const int at = (slot + t.nkb - 1) % stages;
+                    if (!__all_sync(0xffffffffu, bounded_wait(tail_bar(at), (ph >> at) & 1u, &abort_s))) {
                         dead = true;
-                        break;
-                    }
-                    const int rem = t.tok_n - i * KB;
-                    if (rem < KB && rem % 16) {
-                        const int rows = 16 - rem % 16;       // up to the MMA's step of 16
-                        const int boxes = 2 + t.width / 64;   // each [64 rows][128 bytes], lanes' then columns'
-                        const uint32_t sl = ring + slot * Sh::kStage;
+                    } else {
+                        ph ^= 1u << at;
+                        const int rows = 16 - rem % 16;
+                        const int boxes = 2 + t.width / Sh::kBlocks / 64;   // [64 rows][128 bytes], lanes' then columns'
+                        const uint32_t sl = ring + at * Sh::kStage;
                         for (int j = lane; j < boxes * rows * 8; j += 32) {
                             const int box = j / (rows * 8), in = j - box * rows * 8;
                             ptx::st_shared_v4(sl + box * 8192u + rem * 128u + in * 16u, 0u, 0u, 0u, 0u);
                         }
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(fix_bar(slot));
-                    }
-                    if (lane == 0) ptx::mbar_arrive(empty_bar(slot));
-                    if (++slot == stages) {
-                        slot = 0;
-                        ph ^= 1u;
+                        if (lane == 0) {
+                            if constexpr (PAIR)
+                                ptx::mbar_arrive_cluster(ptx::mapa(full_bar(at), 0));
+                            else
+                                ptx::mbar_arrive(full_bar(at));
+                        }
                     }
                 }
+                slot = (slot + t.nkb) % stages;
             }
             if (S > 1) {
                 __syncwarp();
@@ -513,6 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         }
     } else {
         // ---- epilogue
+        if constexpr (kMoveRegs) ptx::regs_up<208>();
         const int quarter = warp & 3, half = (warp >> 2) - 1;
         const int c_lo = half * HALF;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(c_lo);
@@ -534,9 +615,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                     store_out(args.out, args.out_type, out0 + static_cast<size_t>(c) * pitch, v);
             };
             if constexpr (SUMS) {
-                float acc[HALF];
+                // F32 sums, two to a 64-bit register (fma.rn.f32x2)
+                uint64_t acc[HALF / 2];
 #pragma unroll
-                for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
+                for (int j = 0; j < HALF / 2; ++j) acc[j] = 0;
+                const int chunks = min(HALF, max(0, t.width - c_lo)) / 16;
                 for (int i = 0; i < t.nkb && !dead; i += UNIT) {
                     bool ok = bounded_wait(acc_full(buf), aph, &abort_s);
                     if (FP8) ok = ok && bounded_wait(scale_full(slot), ph, &abort_s);
@@ -545,29 +628,33 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                         break;
                     }
                     ptx::tc_fence_after_sync();
+                    // 16 columns are loaded while the 16 before are added
+                    uint32_t v[2][16];
+                    const uint32_t from = lane_addr + static_cast<uint32_t>(buf * TC);
+                    if (chunks > 0) ptx::tmem_ld_start_x16(from, v[0]);
 #pragma unroll
-                    for (int c = 0; c < HALF; c += CHUNK) {
-                        if (c_lo + c < t.width) {
-                            uint32_t v[CHUNK];
-                            if constexpr (CHUNK == 32)
-                                ptx::tmem_ld_32x32b_x32(lane_addr + static_cast<uint32_t>(buf * TC + c), v);
-                            else
-                                ptx::tmem_ld_32x32b_x16(lane_addr + static_cast<uint32_t>(buf * TC + c), v);
-                            const float4 *const s4 = reinterpret_cast<const float4 *>(scale_buf + slot * TC + c_lo + c);
+                    for (int c = 0; c < HALF / 16; ++c) {
+                        if (c < chunks) {
+                            ulonglong2 s2[4];
 #pragma unroll
-                            for (int j = 0; j < CHUNK / 4; ++j) {
-                                const float4 s = FP8 ? s4[j] : make_float4(1.f, 1.f, 1.f, 1.f);
-                                acc[c + 4 * j] = fmaf(__uint_as_float(v[4 * j]), s.x, acc[c + 4 * j]);
-                                acc[c + 4 * j + 1] = fmaf(__uint_as_float(v[4 * j + 1]), s.y, acc[c + 4 * j + 1]);
-                                acc[c + 4 * j + 2] = fmaf(__uint_as_float(v[4 * j + 2]), s.z, acc[c + 4 * j + 2]);
-                                acc[c + 4 * j + 3] = fmaf(__uint_as_float(v[4 * j + 3]), s.w, acc[c + 4 * j + 3]);
+                            for (int j = 0; j < 4; ++j)
+                                s2[j] = FP8 ? reinterpret_cast<const ulonglong2 *>(scale_buf + slot * TC + c_lo + c * 16)[j]
+                                            : make_ulonglong2(0x3F8000003F800000ull, 0x3F8000003F800000ull);
+                            uint32_t(&now)[16] = v[c & 1];
+                            ptx::tmem_wait_x16(now);
+                            if (c + 1 < chunks) ptx::tmem_ld_start_x16(from + (c + 1) * 16, v[(c + 1) & 1]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint64_t &a0 = acc[c * 8 + 2 * j], &a1 = acc[c * 8 + 2 * j + 1];
+                                a0 = ptx::fma_f32x2(ptx::pack_b32x2(now[4 * j], now[4 * j + 1]), s2[j].x, a0);
+                                a1 = ptx::fma_f32x2(ptx::pack_b32x2(now[4 * j + 2], now[4 * j + 3]), s2[j].y, a1);
                             }
                         }
                     }
                     ptx::tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) {
-                        ptx::mbar_arrive(acc_empty(buf));
+                        release_acc(acc_empty(buf));
                         if (FP8) ptx::mbar_arrive(scale_empty(slot));
                     }
                     if (++buf == Sh::kAcc) {
@@ -581,7 +668,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                 }
                 if (!dead) {
 #pragma unroll
-                    for (int j = 0; j < HALF; ++j) emit(c_lo + j, acc[j]);
+                    for (int j = 0; j < HALF / 2; ++j) {
+                        emit(c_lo + 2 * j, __uint_as_float(static_cast<uint32_t>(acc[j])));
+                        emit(c_lo + 2 * j + 1, __uint_as_float(static_cast<uint32_t>(acc[j] >> 32)));
+                    }
                 }
             } else {
                 const bool any = t.nkb > 0;             // kDw: a run without rows has zero gradients
@@ -607,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                     if (any) {
                         ptx::tc_fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(acc_empty(buf));
+                        if (lane == 0) release_acc(acc_empty(buf));
                         if (++buf == Sh::kAcc) {
                             buf = 0;
                             aph ^= 1u;
@@ -634,9 +724,13 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     }
     ptx::tc_fence_before_sync();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync();   // neither block's memory is in use by the other any more
     if (warp == 1) {
         ptx::tc_fence_after_sync();
-        ptx::tmem_dealloc(tmem, Sh::kTmemCols);
+        if constexpr (PAIR)
+            ptx::tmem_dealloc_pair(tmem, Sh::kTmemCols);
+        else
+            ptx::tmem_dealloc(tmem, Sh::kTmemCols);
     }
 }
 
@@ -688,7 +782,7 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
     } else {
         const uint64_t da[2] = {K, T};
         const uint64_t dn[3] = {K, N, G}, dk[3] = {N, K, G};
-        const uint32_t ba[2] = {KB, TC}, bp[2] = {KB, TC / 4}, bn[3] = {KB, kLanes, 1}, bk[3] = {64, 64, 1};
+        const uint32_t ba[2] = {KB, Sh::kLoadCols}, bp[2] = {KB, Sh::kLoadCols / 4}, bn[3] = {KB, kLanes, 1}, bk[3] = {64, 64, 1};
         ok = (FORM == kKn ? encode(&maps.lane, type, elem, 3, p.B, dk, bk)
                           : encode(&maps.lane, type, elem, 3, p.B, dn, bn)) &&
              encode(&maps.col, type, elem, 2, p.A, da, ba) && encode(&maps.col_part, type, elem, 2, p.A, da, bp);
@@ -723,8 +817,9 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return note_error(e, "cudaFuncSetAttribute(grouped_kernel)");
     cudaLaunchConfig_t cfg = {};
-    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(tiles, sms / splits));
-    cfg.gridDim = dim3(static_cast<unsigned>(clusters * splits), 1, 1);
+    const int cluster = Sh::kPair ? 2 : splits;
+    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(tiles, sms / cluster));
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -732,11 +827,11 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = splits;
+    attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = splits > 1 ? 2 : 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return note_error(cudaLaunchKernelEx(&cfg, grouped_kernel<FORM, TC, SUMS>, maps, a), "cudaLaunchKernelEx(grouped_kernel)");
 }
 
@@ -752,22 +847,38 @@ cudaError_t launch_form(const GroupedProblem &p, int splits, int64_t tiles, int 
 
 int64_t grouped_tiles(const GroupedProblem &p, int tc)
 {
-    if (p.form == GroupedForm::kDw) return p.G * ((p.K + kLanes - 1) / kLanes) * ((p.N + tc - 1) / tc);
+    const int64_t lanes = p.form == GroupedForm::kDw ? p.K : p.N, tl = tc == 256 ? 2 * kLanes : kLanes;
+    const int64_t lane_tiles = (lanes + tl - 1) / tl;
+    if (p.form == GroupedForm::kDw) return p.G * lane_tiles * ((p.N + tc - 1) / tc);
     // a run of c rows has ceil(c / tc) column tiles: at most T / tc of them full, and one more each
-    const int64_t runs = std::min<int64_t>(p.G, p.T);
-    return ((p.N + kLanes - 1) / kLanes) * (p.G == 1 ? (p.T + tc - 1) / tc : p.T / tc + runs);
+    return lane_tiles * (p.G == 1 ? (p.T + tc - 1) / tc : p.T / tc + std::min<int64_t>(p.G, p.T));
 }
 
 GroupedPlan plan_grouped(const GroupedProblem &p, int sms)
 {
     GroupedPlan plan = {128, 1};
-    if (p.form != GroupedForm::kDw && p.T <= 32 * p.G) {
+    const bool dw = p.form == GroupedForm::kDw;
+    if (!dw && p.T <= 32 * p.G) {
         plan.tc = 32;
         const int64_t tiles = grouped_tiles(p, 32);
         const int64_t kb = (p.K + (p.form == GroupedForm::kFp8 ? 127 : 63)) / (p.form == GroupedForm::kFp8 ? 128 : 64);
         while (plan.splits < 8 && tiles * plan.splits * 2 <= sms && kb >= plan.splits * 4) plan.splits *= 2;
+    } else if (grouped_tiles(p, 256) >= sms / 2 && (dw ? p.N : p.T) >= 192 * (dw ? 1 : p.G)) {
+        plan.tc = 256;
     }
     return plan;
+}
+
+template <int FORM>
+cudaError_t launch_plan(const GroupedProblem &p, const GroupedPlan &plan, int64_t tiles, int sms, cudaStream_t stream)
+{
+    switch (plan.tc) {
+    case 256: return launch_form<FORM, 256>(p, plan.splits, tiles, sms, stream);
+    case 128: return launch_form<FORM, 128>(p, plan.splits, tiles, sms, stream);
+    default:
+        if constexpr (FORM != kDw) return launch_form<FORM, 32>(p, plan.splits, tiles, sms, stream);
+        return note_error(cudaErrorInvalidConfiguration, "columns of a tile");
+    }
 }
 
 cudaError_t launch_grouped(const GroupedProblem &p, cudaStream_t stream)
@@ -778,18 +889,11 @@ cudaError_t launch_grouped(const GroupedProblem &p, cudaStream_t stream)
     if (e != cudaSuccess) return note_error(e, "cudaDeviceGetAttribute(MultiProcessorCount)");
     const GroupedPlan plan = plan_grouped(p, sms);
     const int64_t tiles = grouped_tiles(p, plan.tc);
-    const bool small = plan.tc == 32;
     switch (p.form) {
-    case GroupedForm::kFp8:
-        return small ? launch_form<kFp8, 32>(p, plan.splits, tiles, sms, stream)
-                     : launch_form<kFp8, 128>(p, plan.splits, tiles, sms, stream);
-    case GroupedForm::kNk:
-        return small ? launch_form<kNk, 32>(p, plan.splits, tiles, sms, stream)
-                     : launch_form<kNk, 128>(p, plan.splits, tiles, sms, stream);
-    case GroupedForm::kKn:
-        return small ? launch_form<kKn, 32>(p, plan.splits, tiles, sms, stream)
-                     : launch_form<kKn, 128>(p, plan.splits, tiles, sms, stream);
-    default: return launch_form<kDw, 128>(p, plan.splits, tiles, sms, stream);
+    case GroupedForm::kFp8: return launch_plan<kFp8>(p, plan, tiles, sms, stream);
+    case GroupedForm::kNk: return launch_plan<kNk>(p, plan, tiles, sms, stream);
+    case GroupedForm::kKn: return launch_plan<kKn>(p, plan, tiles, sms, stream);
+    default: return launch_plan<kDw>(p, plan, tiles, sms, stream);
     }
 }
 

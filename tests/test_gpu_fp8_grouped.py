@@ -113,7 +113,7 @@ def c_16(K, out):
 FP8_SHAPES = [(1, 1, 16), (1, 64, 128), (1, 1024, 2048), (3, 129, 144), (16, 130, 272), (17, 257, 400), (31, 64, 16),
               (33, 200, 1040), (64, 512, 2048), (65, 127, 640), (127, 384, 160), (128, 128, 128), (129, 129, 129 * 16),
               (200, 1000, 528), (257, 255, 1024), (300, 640, 7168), (513, 1025, 272), (1000, 2112, 5136),
-              (2049, 520, 656)]
+              (2049, 520, 656), (2049, 2600, 656), (4100, 1300, 144), (1300, 4105, 1040)]
 
 
 @pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
@@ -174,6 +174,8 @@ GROUPED = [  # counts, N, K, rows before the first run and after the last
     ([700, 1, 0, 40, 513], 392, 648, 1, 2),
     ([129] * 9, 512, 1032, 0, 0),
     ([1500, 600], 1160, 2056, 0, 0),
+    ([1500, 0, 700, 257, 1, 640], 1800, 264, 4, 3),
+    ([500, 900, 333], 2600, 2056, 0, 0),
     ([0] * 500 + [7] + [0] * 300 + [50] + [2] * 222, 72, 136, 0, 0),
 ]
 GROUPED_IDS = [f"G{len(c)}T{sum(c)}N{n}K{k}" for c, n, k, _, _ in GROUPED]
