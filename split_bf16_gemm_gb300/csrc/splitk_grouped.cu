@@ -42,6 +42,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "splitk_internal.h"
@@ -125,14 +126,42 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
     }
 }
 
-__device__ __forceinline__ void store_out(void *out, int type, size_t i, float v)
+template <typename T>
+__device__ __forceinline__ T rounded(float v);
+template <>
+__device__ __forceinline__ float rounded<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// The first `live` of N values to rows `pitch` elements apart.  No branch
+// inside: with two warps to a scheduler a branch's latency is not hidden (the
+// stores of a 256 x 256 tile took 17,500 cycles with the type and the bound
+// tested for each value).
+template <typename T, int N, typename Value>
+__device__ __forceinline__ void store_column(T *p, size_t pitch, int live, Value value)
 {
+    if (live >= N) {
+#pragma unroll
+        for (int j = 0; j < N; ++j, p += pitch) *p = rounded<T>(value(j));
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j, p += pitch)
+            if (j < live) *p = rounded<T>(value(j));
+    }
+}
+
+template <int N, typename Value>
+__device__ __forceinline__ void store_values(void *out, int type, size_t at, size_t pitch, int live, Value value)
+{
+    if (live <= 0) return;
     if (type == 0)
-        static_cast<float *>(out)[i] = v;
+        store_column<float, N>(static_cast<float *>(out) + at, pitch, live, value);
     else if (type == 1)
-        static_cast<__half *>(out)[i] = __float2half_rn(v);
+        store_column<__half, N>(static_cast<__half *>(out) + at, pitch, live, value);
     else
-        static_cast<__nv_bfloat16 *>(out)[i] = __float2bfloat16_rn(v);
+        store_column<__nv_bfloat16, N>(static_cast<__nv_bfloat16 *>(out) + at, pitch, live, value);
 }
 
 template <int FORM, int TC, bool SUMS>
@@ -608,13 +637,19 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
             const size_t out0 = (DW ? static_cast<size_t>(t.g) * args.cols + t.col0 : static_cast<size_t>(t.col0)) * pitch +
                                 t.lane0 + my;
             const bool live = t.lane0 + my < args.lanes;
-            auto emit = [&](int c, float v) {
-                if (S > 1)
-                    sum_buf[c * kLanes + my] = v;
-                else if (live && c < t.cols)
-                    store_out(args.out, args.out_type, out0 + static_cast<size_t>(c) * pitch, v);
+            // N finished values of the thread's lane, from column c on
+            auto emit = [&](auto n, int c, auto value) {
+                constexpr int N = decltype(n)::value;
+                if (S > 1) {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) sum_buf[(c + j) * kLanes + my] = value(j);
+                } else {
+                    store_values<N>(args.out, args.out_type, out0 + static_cast<size_t>(c) * pitch, pitch,
+                                    live ? t.cols - c : 0, value);
+                }
             };
             if constexpr (SUMS) {
+                constexpr uint64_t kOnes = 0x3F8000003F800000ull;   // 1.f twice
                 // F32 sums, two to a 64-bit register (fma.rn.f32x2)
                 uint64_t acc[HALF / 2];
 #pragma unroll
@@ -628,26 +663,35 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                         break;
                     }
                     ptx::tc_fence_after_sync();
-                    // 16 columns are loaded while the 16 before are added
+                    // 16 columns load while the 16 before are added
                     uint32_t v[2][16];
                     const uint32_t from = lane_addr + static_cast<uint32_t>(buf * TC);
-                    if (chunks > 0) ptx::tmem_ld_start_x16(from, v[0]);
+                    const ulonglong2 *const s2 = reinterpret_cast<const ulonglong2 *>(scale_buf + slot * TC + c_lo);
+                    auto add = [&](int c) {
+                        uint32_t(&now)[16] = v[c & 1];
 #pragma unroll
-                    for (int c = 0; c < HALF / 16; ++c) {
-                        if (c < chunks) {
-                            ulonglong2 s2[4];
+                        for (int j = 0; j < 4; ++j) {
+                            const ulonglong2 f = FP8 ? s2[4 * c + j] : make_ulonglong2(kOnes, kOnes);
+                            uint64_t &a0 = acc[c * 8 + 2 * j], &a1 = acc[c * 8 + 2 * j + 1];
+                            a0 = ptx::fma_f32x2(ptx::pack_b32x2(now[4 * j], now[4 * j + 1]), f.x, a0);
+                            a1 = ptx::fma_f32x2(ptx::pack_b32x2(now[4 * j + 2], now[4 * j + 3]), f.y, a1);
+                        }
+                    };
+                    if (chunks == HALF / 16) {                 // every column in use: no branch a chunk
+                        ptx::tmem_ld_start_x16(from, v[0]);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                s2[j] = FP8 ? reinterpret_cast<const ulonglong2 *>(scale_buf + slot * TC + c_lo + c * 16)[j]
-                                            : make_ulonglong2(0x3F8000003F800000ull, 0x3F8000003F800000ull);
-                            uint32_t(&now)[16] = v[c & 1];
-                            ptx::tmem_wait_x16(now);
-                            if (c + 1 < chunks) ptx::tmem_ld_start_x16(from + (c + 1) * 16, v[(c + 1) & 1]);
+                        for (int c = 0; c < HALF / 16; ++c) {
+                            ptx::tmem_wait_x16(v[c & 1]);
+                            if (c + 1 < HALF / 16) ptx::tmem_ld_start_x16(from + (c + 1) * 16, v[(c + 1) & 1]);
+                            add(c);
+                        }
+                    } else {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint64_t &a0 = acc[c * 8 + 2 * j], &a1 = acc[c * 8 + 2 * j + 1];
-                                a0 = ptx::fma_f32x2(ptx::pack_b32x2(now[4 * j], now[4 * j + 1]), s2[j].x, a0);
-                                a1 = ptx::fma_f32x2(ptx::pack_b32x2(now[4 * j + 2], now[4 * j + 3]), s2[j].y, a1);
+                        for (int c = 0; c < HALF / 16; ++c) {
+                            if (c < chunks) {
+                                ptx::tmem_ld_start_x16(from + c * 16, v[c & 1]);
+                                ptx::tmem_wait_x16(v[c & 1]);
+                                add(c);
                             }
                         }
                     }
@@ -667,11 +711,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                     }
                 }
                 if (!dead) {
-#pragma unroll
-                    for (int j = 0; j < HALF / 2; ++j) {
-                        emit(c_lo + 2 * j, __uint_as_float(static_cast<uint32_t>(acc[j])));
-                        emit(c_lo + 2 * j + 1, __uint_as_float(static_cast<uint32_t>(acc[j] >> 32)));
-                    }
+                    emit(std::integral_constant<int, HALF>(), c_lo, [&](int j) {
+                        return __uint_as_float(static_cast<uint32_t>(j & 1 ? acc[j / 2] >> 32 : acc[j / 2]));
+                    });
                 }
             } else {
                 const bool any = t.nkb > 0;             // kDw: a run without rows has zero gradients
@@ -691,8 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
 #pragma unroll
                             for (int j = 0; j < CHUNK; ++j) v[j] = 0u;
                         }
-#pragma unroll
-                        for (int j = 0; j < CHUNK; ++j) emit(c_lo + c + j, __uint_as_float(v[j]));
+                        emit(std::integral_constant<int, CHUNK>(), c_lo + c, [&](int j) { return __uint_as_float(v[j]); });
                     }
                     if (any) {
                         ptx::tc_fence_before_sync();
@@ -716,7 +757,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                         asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(ptx::mapa(at, r)) : "memory");
                         v = r == 0 ? x : v + x;
                     }
-                    if (live) store_out(args.out, args.out_type, out0 + static_cast<size_t>(c) * pitch, v);
+                    store_values<1>(args.out, args.out_type, out0 + static_cast<size_t>(c) * pitch, pitch, live,
+                                    [&](int) { return v; });
                 }
                 cluster_sync();                        // and may be overwritten
             }
