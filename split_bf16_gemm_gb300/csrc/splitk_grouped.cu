@@ -24,6 +24,8 @@
 //              in the last k-block (they belong to the next run);
 //   warps 4-11 tensor memory -> registers -> output: lane quarter w % 4,
 //              column half w / 4 - 1.
+// kFp8 on large problems (ROWS) exchanges the roles: the lanes are tokens and
+// the columns weights, 256 by 256 to a pair of blocks.
 // kFp8: F32 scales cannot be applied inside the MMA, so each k-block's product
 // goes to an accumulator of its own (a ring of them in tensor memory), and the
 // last eight warps add it, times the scale, to F32 sums in registers while
@@ -42,6 +44,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "ptx.cuh"
@@ -54,6 +57,7 @@ __device__ unsigned g_grouped_status;
 
 constexpr uint64_t kWaitLimitNs = 1000000000ull;   // 1 s
 constexpr int kThreads = 384;
+constexpr int kRoleWarps = 4;                       // of which the last is idle: registers move by four warps
 constexpr int kEpilogueWarps = 8;
 constexpr int kLanes = 128;
 constexpr uint32_t kLaneBytes = kLanes * 128;       // one k-block of the lane operand
@@ -71,12 +75,23 @@ template <int TC>
 struct Shape {
     static constexpr bool kPair = TC == 256;
     static constexpr int kBlocks = kPair ? 2 : 1;
-    static constexpr int kAcc = TC <= 32 ? 4 : 2;                 // accumulators in tensor memory
+    static constexpr int kAcc = TC <= 64 ? 4 : 2;                 // accumulators in tensor memory
     static constexpr int kTmemCols = kAcc * TC;
     static constexpr int kLoadCols = TC / kBlocks;                // columns a block loads
     static constexpr uint32_t kColBytes = kLoadCols * 128;
     static constexpr uint32_t kStage = kLaneBytes + kColBytes;
     static constexpr int kTileLanes = kLanes * kBlocks;
+    // kFp8, a warp's part of the columns (half the tile's): read as fragments
+    // of 8 columns, of which a thread holds two.  The scales of thread t % 4 =
+    // p stand together, p's 4 words further round the banks than the last's.
+    static constexpr int kHalf = TC / 2;
+    static constexpr int kScalePitch = kHalf / 4 + 4;
+    static constexpr int kScaleSlot = 2 * 4 * kScalePitch;
+    static constexpr int kFragCols = kHalf < 32 ? kHalf : 32;     // columns of one tensor-memory load
+    // staged rows of 16-bit outputs, padded by 16 bytes: 32 lanes a column, or
+    // (TC = 256) the warp's 128 columns of a lane
+    static constexpr uint32_t kStageRow = kPair ? 2 * kHalf + 16 : 80;
+    static constexpr uint32_t kStageWarp = (kPair ? 32 : kFragCols) * kStageRow;
 };
 
 struct GroupedArgs {
@@ -90,7 +105,7 @@ struct GroupedArgs {
     int bf16;
     int splits;                // cluster size along K
     int stages;
-    uint32_t sum_off, scale_off, table_off;   // byte offsets in shared memory after the stage ring
+    uint32_t sum_off, scale_off, stage_off, table_off;   // byte offsets in shared memory after the stage ring
 };
 
 struct Maps {
@@ -103,6 +118,7 @@ struct Tile {
     int col0;                  // first column: a token, or a column of D
     int kb0, nkb;              // this block's k-blocks
     int tok0, tok_n;           // kDw: the run
+    int rows;                  // ROWS: live lanes of this block
 };
 
 // RELAXED: a barrier that guards tensor memory and that the other block of a
@@ -172,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     constexpr bool FP8 = FORM == kFp8, DW = FORM == kDw;
     constexpr bool LMN = FORM == kKn || FORM == kDw;   // lane operand contiguous along its lanes
     constexpr bool PAIR = Sh::kPair;
+    constexpr bool ROWS = FP8 && PAIR;                 // lanes are tokens, columns weights
     constexpr int KB = FP8 ? 128 : 64;
     constexpr int UNIT = FP8 ? 1 : SUMS ? kUnit : 1 << 30;   // k-blocks summed in one accumulator
     constexpr int HALF = TC / 2;                       // columns of an epilogue warp
@@ -187,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     const uint32_t ring = (raw + 1023u) & ~1023u;
     uint8_t *const base = dsmem + (ring - raw);
     float *const sum_buf = reinterpret_cast<float *>(base + args.sum_off);       // [TC][128], splits > 1
-    float *const scale_buf = reinterpret_cast<float *>(base + args.scale_off);   // [kScaleRing][TC]
+    float *const scale_buf = reinterpret_cast<float *>(base + args.scale_off);   // [kScaleRing][kScaleSlot]
     int *const offs = reinterpret_cast<int *>(base + args.table_off);            // [G+1]
     int *const pref = offs + args.G + 1;                                         // [G+1]: tiles before run g
     const uint32_t bar0 = ptx::smem_addr(&bars[0]);
@@ -263,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         for (int i = tid; i <= args.G; i += kThreads) offs[i] = min(max(args.offsets[i], 0), args.T);
     }
     __syncthreads();
-    if (warp == 3) {
+    if (warp == 2) {
         int most = offs[0], tiles = 0;
         if (lane == 0) pref[0] = 0;
         for (int b = 0; b < args.G; b += 32) {
@@ -327,16 +344,23 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
             t.nkb = (run + KB - 1) / KB;
         } else {
             t.col0 = begin + ci * each;
+            if constexpr (ROWS) {
+                t.col0 = li * TC;                      // whole blocks of 128: a scale for each warp's columns
+                t.cols = min(TC, args.lanes - t.col0);
+                t.width = (t.cols + 31) / 32 * 32;
+                t.lane0 = begin + ci * Sh::kTileLanes + peer * kLanes;
+                t.rows = min(kLanes, begin + run - t.lane0);
+            }
             const int lo = rank * args.kblocks / S, hi = (rank + 1) * args.kblocks / S;
             t.kb0 = lo;
             t.nkb = hi - lo;
         }
     };
 
-    // 384 threads start with 168 registers each; TC = 256 sums need more than
-    // that in warps 4-11: 4 * 32 * 80 + 8 * 32 * 208 <= 384 * 168
+    // 384 threads start with 168 registers each.  The sums of a 256-column tile
+    // need more in warps 4-11: 4 * 32 * 72 + 8 * 32 * 216 = 384 * 168.
     constexpr bool kMoveRegs = SUMS && TC == 256;
-    if (kMoveRegs && warp < 4) ptx::regs_down<80>();
+    if (kMoveRegs && warp < kRoleWarps) ptx::regs_down<72>();
     if (warp == 0) {
         // ---- producer
         int g = 0, slot = 0;
@@ -363,11 +387,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                     else
                         ptx::tma_load_2d(dst, map, bar, x, y, policy);
                 };
-                auto load3 = [&](uint32_t dst, uint32_t bar, int x, int y) {
+                auto load3 = [&](uint32_t dst, uint32_t bar, int x, int y, const CUtensorMap *map) {
                     if constexpr (PAIR)
-                        ptx::tma_load_3d_pair(dst, &maps.lane, bar, x, y, t.g, once);
+                        ptx::tma_load_3d_pair(dst, map, bar, x, y, t.g, once);
                     else
-                        ptx::tma_load_3d(dst, &maps.lane, bar, x, y, t.g, once);
+                        ptx::tma_load_3d(dst, map, bar, x, y, t.g, once);
                 };
                 for (int i = 0; i < t.nkb; ++i) {
                     if (!bounded_wait(empty_bar(slot), ph ^ 1u, &abort_s)) {
@@ -397,12 +421,20 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                             load2(sc + j * 8192u, &maps.col, bar, col + 64 * j, y, once);
                     } else {
                         if constexpr (LMN) {
-                            load3(sl, bar, t.lane0, kx);
-                            load3(sl + 8192u, bar, t.lane0 + 64, kx);
+                            load3(sl, bar, t.lane0, kx, &maps.lane);
+                            load3(sl + 8192u, bar, t.lane0 + 64, kx, &maps.lane);
+                        } else if constexpr (ROWS) {
+                            load2(sl, &maps.col, bar, kx, t.lane0, again);
                         } else {
-                            load3(sl, bar, kx, t.lane0);
+                            load3(sl, bar, kx, t.lane0, &maps.lane);
                         }
-                        if (whole) {
+                        if constexpr (ROWS) {
+                            if (whole)
+                                load3(sc, bar, kx, col, &maps.lane);
+                            else
+                                for (int j = 0; j < parts; ++j)
+                                    load3(sc + j * kPart * 128u, bar, kx, col + j * kPart, &maps.col_part);
+                        } else if (whole) {
                             load2(sc, &maps.col, bar, kx, col, again);
                         } else {
                             for (int j = 0; j < parts; ++j)
@@ -533,11 +565,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         for (int w = first; w < total; w += step) {
             Tile t;
             locate(w, g, t);
-            if constexpr (FP8) {
-                constexpr int PER = TC / 32, BATCH = PER > 4 ? 2 : 4;
+            if constexpr (FP8 && !ROWS) {
+                constexpr int PER = TC / 32, BATCH = 4;
                 const int lane_blocks = (args.lanes + kLanes - 1) / kLanes;
-                const int lb = min(t.lane0 / kLanes, lane_blocks - 1);   // a pair's second half may lie past the end
-                const float *const sb = args.sb + (static_cast<size_t>(t.g) * lane_blocks + lb) * args.kblocks + t.kb0;
+                const float *const sb =
+                    args.sb + (static_cast<size_t>(t.g) * lane_blocks + t.lane0 / kLanes) * args.kblocks + t.kb0;
                 const float *sa[PER];
 #pragma unroll
                 for (int p = 0; p < PER; ++p) {
@@ -570,7 +602,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                             break;
                         }
 #pragma unroll
-                        for (int p = 0; p < PER; ++p) scale_buf[slot * TC + p * 32 + lane] = now[p][j];
+                        for (int p = 0; p < PER; ++p) {
+                            const int c = p * 32 + lane, in = c % HALF;
+                            scale_buf[slot * Sh::kScaleSlot + (c / HALF * 4 + in % 8 / 2) * Sh::kScalePitch + in / 8 * 2 +
+                                      in % 2] = now[p][j];
+                        }
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(scale_full(slot));
                         if (++slot == kScaleRing) {
@@ -613,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                 cluster_sync();
             }
         }
-    } else if (warp == 3) {
+    } else if (warp < kRoleWarps) {
         if (S > 1) {
             for (int w = first; w < total; w += step) {
                 cluster_sync();
@@ -622,8 +658,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         }
     } else {
         // ---- epilogue
-        if constexpr (kMoveRegs) ptx::regs_up<208>();
-        const int quarter = warp & 3, half = (warp >> 2) - 1;
+        if constexpr (kMoveRegs) ptx::regs_up<216>();
+        const int quarter = warp & 3, half = (warp - kRoleWarps) >> 2;
         const int c_lo = half * HALF;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(c_lo);
         const int my = quarter * 32 + lane;             // the thread's lane of the tile
@@ -648,7 +684,316 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                                     live ? t.cols - c : 0, value);
                 }
             };
-            if constexpr (SUMS) {
+            if constexpr (ROWS) {
+                // A token to a thread: its scale times the weight block's is one
+                // factor for the warp's 128 columns, and the sums of two columns
+                // share a 64-bit register (fma.rn.f32x2).  Reading 128 columns
+                // and adding them takes 8 warps 310 cycles, against 512 for the
+                // k-block's MMAs; as fragments with a scale for each column it
+                // takes 850.
+                constexpr int AHEAD = 4;                       // k-blocks whose factors are fetched together
+                const int nbs = (args.lanes + kLanes - 1) / kLanes;
+                const int nb = min((t.col0 + c_lo) / kLanes, nbs - 1);   // columns past N: any block's
+                const float *const sb = args.sb + (static_cast<size_t>(t.g) * nbs + nb) * args.kblocks;
+                const float *const sa = args.sa + static_cast<size_t>(t.lane0 + min(my, max(t.rows, 1) - 1)) * args.kblocks;
+                float next[AHEAD];
+                auto fetch = [&](int b) {
+#pragma unroll
+                    for (int j = 0; j < AHEAD; ++j) {
+                        const int kb = min(b + j, t.nkb - 1);
+                        next[j] = t.rows > 0 ? __ldg(sa + kb) * __ldg(sb + kb) : 0.f;
+                    }
+                };
+                uint64_t acc[HALF / 2];
+#pragma unroll
+                for (int j = 0; j < HALF / 2; ++j) acc[j] = 0;
+                const int chunks = (min(HALF, max(0, t.width - c_lo)) + 15) / 16;
+                fetch(0);
+                for (int b = 0; b < t.nkb && !dead; b += AHEAD) {
+                    float now[AHEAD];
+#pragma unroll
+                    for (int j = 0; j < AHEAD; ++j) now[j] = next[j];
+                    if (b + AHEAD < t.nkb) fetch(b + AHEAD);
+#pragma unroll 1
+                    for (int j = 0; j < AHEAD && b + j < t.nkb; ++j) {
+                        const float factor = now[0];
+#pragma unroll
+                        for (int i = 0; i + 1 < AHEAD; ++i) now[i] = now[i + 1];
+                        bool ok = ptx::mbar_try_wait(acc_full(buf), aph);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = bounded_wait(acc_full(buf), aph, &abort_s);
+                            if (!__all_sync(0xffffffffu, ok)) {
+                                dead = true;
+                                break;
+                            }
+                        }
+                        ptx::tc_fence_after_sync();
+                        const uint64_t f2 = ptx::pack_b32x2(__float_as_uint(factor), __float_as_uint(factor));
+                        const uint32_t from = lane_addr + static_cast<uint32_t>(buf * TC);
+                        uint32_t v[2][16];
+                        auto add = [&](int c) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                acc[c * 8 + i] = ptx::fma_f32x2(ptx::pack_b32x2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), f2,
+                                                                acc[c * 8 + i]);
+                        };
+                        auto release = [&]() {
+                            ptx::tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) release_acc(acc_empty(buf));
+                        };
+                        if (chunks == HALF / 16) {
+                            ptx::tmem_ld_start_x16(from, v[0]);
+#pragma unroll
+                            for (int c = 0; c < HALF / 16; ++c) {
+                                ptx::tmem_wait_x16(v[c & 1]);
+                                if (c + 1 < HALF / 16)
+                                    ptx::tmem_ld_start_x16(from + (c + 1) * 16, v[(c + 1) & 1]);
+                                else
+                                    release();
+                                add(c);
+                            }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < HALF / 16; ++c) {
+                                if (c < chunks) {
+                                    ptx::tmem_ld_start_x16(from + c * 16, v[c & 1]);
+                                    ptx::tmem_wait_x16(v[c & 1]);
+                                    add(c);
+                                }
+                            }
+                            release();
+                        }
+                        if (++buf == Sh::kAcc) {
+                            buf = 0;
+                            aph ^= 1u;
+                        }
+                    }
+                }
+                auto value = [&](int j) {
+                    return __uint_as_float(static_cast<uint32_t>(j & 1 ? acc[j / 2] >> 32 : acc[j / 2]));
+                };
+                const int cols = min(HALF, t.cols - c_lo);      // of the warp
+                const size_t at = static_cast<size_t>(t.lane0 + my) * pitch + t.col0 + c_lo;
+                if (dead || cols <= 0) {
+                } else if (args.out_type != 0 && args.lanes % 8 == 0) {
+                    // each thread stages its row and copies it out; the copy goes
+                    // on beside the next tile's sums
+                    const uint32_t mine = ptx::smem_addr(base + args.stage_off) +
+                                          static_cast<uint32_t>((warp - kRoleWarps) * 32 + lane) * Sh::kStageRow;
+                    ptx::bulk_wait_read();
+#pragma unroll
+                    for (int c = 0; c < HALF; c += 8) {
+                        uint32_t x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float lo = value(c + 2 * i), hi = value(c + 2 * i + 1);
+                            if (args.out_type == 1) {
+                                const __half2 y = __floats2half2_rn(lo, hi);
+                                x[i] = *reinterpret_cast<const uint32_t *>(&y);
+                            } else {
+                                const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
+                                x[i] = *reinterpret_cast<const uint32_t *>(&y);
+                            }
+                        }
+                        ptx::st_shared_v4(mine + static_cast<uint32_t>(c) * 2u, x[0], x[1], x[2], x[3]);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    if (my < t.rows)
+                        ptx::bulk_store(static_cast<uint16_t *>(args.out) + at, mine, static_cast<uint32_t>(cols) * 2u);
+                    ptx::bulk_commit();
+                } else if (my < t.rows) {
+                    // F32, or rows whose 16-bit length is no multiple of 16 bytes
+                    auto direct = [&](auto *out) {
+                        using T = std::remove_pointer_t<decltype(out)>;
+                        if constexpr (sizeof(T) == 4) {
+                            if (args.lanes % 4 == 0) {
+#pragma unroll
+                                for (int c = 0; c < HALF; c += 4)
+                                    if (c < cols)
+                                        *reinterpret_cast<float4 *>(out + c) =
+                                            make_float4(value(c), value(c + 1), value(c + 2), value(c + 3));
+                                return;
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < HALF; ++c)
+                            if (c < cols) out[c] = rounded<T>(value(c));
+                    };
+                    if (args.out_type == 0)
+                        direct(static_cast<float *>(args.out) + at);
+                    else if (args.out_type == 1)
+                        direct(static_cast<__half *>(args.out) + at);
+                    else
+                        direct(static_cast<__nv_bfloat16 *>(args.out) + at);
+                }
+            } else if constexpr (FP8) {
+                // F32 sums in fragments, two columns to a 64-bit register
+                // (fma.rn.f32x2).  A thread of a fragment needs the scales of a
+                // quarter of the columns, a quarter of the shared-memory reads of
+                // a thread that holds a whole lane.
+                constexpr int GC = Sh::kFragCols, GROUPS = HALF / GC, R = GC / 2;   // R registers a load
+                const int p = lane & 3, r8 = lane >> 2;
+                uint64_t acc[GROUPS][2][R / 2];
+#pragma unroll
+                for (int c = 0; c < GROUPS; ++c)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < R / 2; ++j) acc[c][h][j] = 0;
+                const int groups = (min(HALF, max(0, t.width - c_lo)) + GC - 1) / GC;
+                for (int i = 0; i < t.nkb && !dead; ++i) {
+                    bool ok = ptx::mbar_try_wait(acc_full(buf), aph) & ptx::mbar_try_wait(scale_full(slot), ph);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = bounded_wait(acc_full(buf), aph, &abort_s) && bounded_wait(scale_full(slot), ph, &abort_s);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            dead = true;
+                            break;
+                        }
+                    }
+                    ptx::tc_fence_after_sync();
+                    uint32_t v[2][R];
+                    const uint32_t from = lane_addr + static_cast<uint32_t>(buf * TC);
+                    const float *const sc = scale_buf + slot * Sh::kScaleSlot + (half * 4 + p) * Sh::kScalePitch;
+                    // load n covers columns n / 2 * GC .. and lanes 16 (n % 2) ..
+                    auto start = [&](int n) {
+                        ptx::tmem_ld_start_frag(from + static_cast<uint32_t>(n / 2 * GC) + (static_cast<uint32_t>(n % 2 * 16) << 16),
+                                                v[n % 2]);
+                    };
+                    auto add = [&](int n) {
+                        const ulonglong2 *const s2 = reinterpret_cast<const ulonglong2 *>(sc + n / 2 * (GC / 4));
+                        uint32_t(&now)[R] = v[n % 2];
+                        uint64_t(&a)[R / 2] = acc[n / 2][n % 2];
+#pragma unroll
+                        for (int j = 0; j < GC / 16; ++j) {    // two groups of 8 columns
+                            const ulonglong2 f = s2[j];
+                            a[4 * j] = ptx::fma_f32x2(ptx::pack_b32x2(now[8 * j], now[8 * j + 1]), f.x, a[4 * j]);
+                            a[4 * j + 1] = ptx::fma_f32x2(ptx::pack_b32x2(now[8 * j + 2], now[8 * j + 3]), f.x, a[4 * j + 1]);
+                            a[4 * j + 2] = ptx::fma_f32x2(ptx::pack_b32x2(now[8 * j + 4], now[8 * j + 5]), f.y, a[4 * j + 2]);
+                            a[4 * j + 3] = ptx::fma_f32x2(ptx::pack_b32x2(now[8 * j + 6], now[8 * j + 7]), f.y, a[4 * j + 3]);
+                        }
+                    };
+                    auto release = [&]() {                      // the accumulator may be overwritten
+                        ptx::tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) release_acc(acc_empty(buf));
+                    };
+                    if (groups == GROUPS) {                    // every column in use: no branch a load
+                        start(0);
+#pragma unroll
+                        for (int n = 0; n < 2 * GROUPS; ++n) {
+                            ptx::tmem_wait(v[n % 2]);
+                            if (n + 1 < 2 * GROUPS)
+                                start(n + 1);
+                            else
+                                release();
+                            add(n);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < GROUPS; ++c) {
+                            if (c < groups) {
+                                start(2 * c);
+                                start(2 * c + 1);
+                                ptx::tmem_wait(v[0]);
+                                ptx::tmem_wait(v[1]);
+                                add(2 * c);
+                                add(2 * c + 1);
+                            }
+                        }
+                        release();
+                    }
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(scale_empty(slot));
+                    if (++buf == Sh::kAcc) {
+                        buf = 0;
+                        aph ^= 1u;
+                    }
+                    if (++slot == kScaleRing) {
+                        slot = 0;
+                        ph ^= 1u;
+                    }
+                }
+                // value of group c, lane half h, 8-column group i, row pair rp, column b of the pair
+                auto value = [&](int c, int h, int i, int rp, int b) {
+                    const uint64_t x = acc[c][h][2 * i + rp];
+                    return __uint_as_float(static_cast<uint32_t>(b ? x >> 32 : x));
+                };
+                const int row = quarter * 32 + r8;              // of the tile, plus 16 h + 8 rp
+                if (dead) {
+                } else if (S > 1) {
+#pragma unroll
+                    for (int c = 0; c < GROUPS; ++c)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int e = 0; e < R; ++e)         // i = e / 4, rp = e / 2 % 2, b = e % 2
+                                sum_buf[(c_lo + c * GC + e / 4 * 8 + 2 * p + e % 2) * kLanes + row + 16 * h + e / 2 % 2 * 8] =
+                                    value(c, h, e / 4, e / 2 % 2, e % 2);
+                } else if (args.out_type != 0 && args.lanes % 8 == 0) {
+                    // 16-bit outputs: 32 lanes by GC columns through shared
+                    // memory (transposed on the way), then 64 bytes a row
+                    uint16_t *const out = static_cast<uint16_t *>(args.out) + static_cast<size_t>(t.col0) * pitch;
+                    const uint32_t mine = ptx::smem_addr(base + args.stage_off) +
+                                          static_cast<uint32_t>(warp - kRoleWarps) * Sh::kStageWarp;
+                    const int n = t.lane0 + quarter * 32 + (lane & 3) * 8;
+                    auto pair16 = [&](int c, int h, int i, int rp) {
+                        const float lo = value(c, h, i, rp, 0), hi = value(c, h, i, rp, 1);
+                        uint32_t x;
+                        if (args.out_type == 1) {
+                            const __half2 y = __floats2half2_rn(lo, hi);
+                            x = *reinterpret_cast<const uint32_t *>(&y);
+                        } else {
+                            const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
+                            x = *reinterpret_cast<const uint32_t *>(&y);
+                        }
+                        return x;
+                    };
+#pragma unroll
+                    for (int c = 0; c < GROUPS; ++c) {
+                        if (c >= groups) break;
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < GC / 8; ++i)
+                            ptx::stmatrix_x4_trans(mine + static_cast<uint32_t>(i * 8 + (lane & 7)) * Sh::kStageRow +
+                                                       static_cast<uint32_t>(lane >> 3) * 16u,
+                                                   pair16(c, 0, i, 0), pair16(c, 0, i, 1), pair16(c, 1, i, 0), pair16(c, 1, i, 1));
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < GC / 8; ++i) {
+                            const int col = c_lo + c * GC + i * 8 + (lane >> 2);
+                            const float4 x = ptx::ld_shared_v4(mine + static_cast<uint32_t>(i * 8 + (lane >> 2)) * Sh::kStageRow +
+                                                               static_cast<uint32_t>(lane & 3) * 16u);
+                            if (col < t.cols && n < args.lanes)
+                                *reinterpret_cast<float4 *>(out + static_cast<size_t>(col) * pitch + n) = x;
+                        }
+                    }
+                } else {
+                    // F32 rows in pieces of 32 bytes; rows whose 16-bit length
+                    // is no multiple of 16 bytes, value by value
+                    auto direct = [&](auto *out) {
+                        using T = std::remove_pointer_t<decltype(out)>;
+                        T *at = out + static_cast<size_t>(t.col0 + c_lo + 2 * p) * pitch + t.lane0 + row;
+                        const int cols = t.cols - c_lo - 2 * p, rows = args.lanes - t.lane0 - row;
+#pragma unroll
+                        for (int c = 0; c < GROUPS; ++c)
+#pragma unroll
+                            for (int i = 0; i < GC / 8; ++i, at += 8 * pitch)
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {   // b = e % 2, h = e / 4, rp = e / 2 % 2
+                                    const int up = e / 4 * 16 + e / 2 % 2 * 8;
+                                    if (c * GC + i * 8 + e % 2 < cols && up < rows)
+                                        at[(e % 2 ? pitch : 0) + up] = rounded<T>(value(c, e / 4, i, e / 2 % 2, e % 2));
+                                }
+                    };
+                    if (args.out_type == 0)
+                        direct(static_cast<float *>(args.out));
+                    else if (args.out_type == 1)
+                        direct(static_cast<__half *>(args.out));
+                    else
+                        direct(static_cast<__nv_bfloat16 *>(args.out));
+                }
+            } else if constexpr (SUMS) {
                 constexpr uint64_t kOnes = 0x3F8000003F800000ull;   // 1.f twice
                 // F32 sums, two to a 64-bit register (fma.rn.f32x2)
                 uint64_t acc[HALF / 2];
@@ -656,8 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                 for (int j = 0; j < HALF / 2; ++j) acc[j] = 0;
                 const int chunks = min(HALF, max(0, t.width - c_lo)) / 16;
                 for (int i = 0; i < t.nkb && !dead; i += UNIT) {
-                    bool ok = bounded_wait(acc_full(buf), aph, &abort_s);
-                    if (FP8) ok = ok && bounded_wait(scale_full(slot), ph, &abort_s);
+                    const bool ok = bounded_wait(acc_full(buf), aph, &abort_s);
                     if (!__all_sync(0xffffffffu, ok)) {
                         dead = true;
                         break;
@@ -666,16 +1010,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                     // 16 columns load while the 16 before are added
                     uint32_t v[2][16];
                     const uint32_t from = lane_addr + static_cast<uint32_t>(buf * TC);
-                    const ulonglong2 *const s2 = reinterpret_cast<const ulonglong2 *>(scale_buf + slot * TC + c_lo);
                     auto add = [&](int c) {
                         uint32_t(&now)[16] = v[c & 1];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const ulonglong2 f = FP8 ? s2[4 * c + j] : make_ulonglong2(kOnes, kOnes);
-                            uint64_t &a0 = acc[c * 8 + 2 * j], &a1 = acc[c * 8 + 2 * j + 1];
-                            a0 = ptx::fma_f32x2(ptx::pack_b32x2(now[4 * j], now[4 * j + 1]), f.x, a0);
-                            a1 = ptx::fma_f32x2(ptx::pack_b32x2(now[4 * j + 2], now[4 * j + 3]), f.y, a1);
-                        }
+                        for (int j = 0; j < 8; ++j)
+                            acc[c * 8 + j] = ptx::fma_f32x2(ptx::pack_b32x2(now[2 * j], now[2 * j + 1]), kOnes, acc[c * 8 + j]);
                     };
                     if (chunks == HALF / 16) {                 // every column in use: no branch a chunk
                         ptx::tmem_ld_start_x16(from, v[0]);
@@ -699,15 +1038,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                     __syncwarp();
                     if (lane == 0) {
                         release_acc(acc_empty(buf));
-                        if (FP8) ptx::mbar_arrive(scale_empty(slot));
                     }
                     if (++buf == Sh::kAcc) {
                         buf = 0;
                         aph ^= 1u;
-                    }
-                    if (FP8 && ++slot == kScaleRing) {
-                        slot = 0;
-                        ph ^= 1u;
                     }
                 }
                 if (!dead) {
@@ -749,21 +1083,33 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
             if (S > 1) {
                 __syncwarp();
                 cluster_sync();                        // every rank's sums stand in its shared memory
-                for (int c = rank + S * half; c < t.cols; c += 2 * S) {
-                    const uint32_t at = ptx::smem_addr(sum_buf + c * kLanes + my);
-                    float v = 0.f;
+                // this block adds columns rank, rank + S, ...; eight at a time, so
+                // that the reads of other blocks' memory overlap
+                constexpr int AT_ONCE = 8;
+                for (int c0 = rank + S * half; c0 < t.cols; c0 += 2 * S * AT_ONCE) {
+                    float sum[AT_ONCE], x[AT_ONCE];
                     for (int r = 0; r < S; ++r) {
-                        float x;
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(ptx::mapa(at, r)) : "memory");
-                        v = r == 0 ? x : v + x;
+                        const uint32_t at = ptx::mapa(ptx::smem_addr(sum_buf + my), r);
+#pragma unroll
+                        for (int j = 0; j < AT_ONCE; ++j) {
+                            const int c = min(c0 + 2 * S * j, t.cols - 1);
+                            x[j] = ptx::ld_cluster_f32(at + static_cast<uint32_t>(c * kLanes) * 4u);
+                        }
+#pragma unroll
+                        for (int j = 0; j < AT_ONCE; ++j) sum[j] = r == 0 ? x[j] : sum[j] + x[j];
                     }
-                    store_values<1>(args.out, args.out_type, out0 + static_cast<size_t>(c) * pitch, pitch, live,
-                                    [&](int) { return v; });
+#pragma unroll
+                    for (int j = 0; j < AT_ONCE; ++j) {
+                        const int c = c0 + 2 * S * j;
+                        store_values<1>(args.out, args.out_type, out0 + static_cast<size_t>(c) * pitch, pitch,
+                                        live && c < t.cols, [&](int) { return sum[j]; });
+                    }
                 }
                 cluster_sync();                        // and may be overwritten
             }
         }
     }
+    if (ROWS && warp >= kRoleWarps) ptx::bulk_wait();   // the outputs are written when the grid ends
     ptx::tc_fence_before_sync();
     __syncthreads();
     if constexpr (PAIR) cluster_sync();   // neither block's memory is in use by the other any more
@@ -777,6 +1123,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
 }
 
 // ------------------------------------------------------------------ host side
+
+constexpr int kMaxDevices = 64;
 
 bool encode(CUtensorMap *map, CUtensorMapDataType type, int elem, int rank, const void *ptr, const uint64_t *dims,
             const uint32_t *box)
@@ -803,7 +1151,7 @@ bool encode(CUtensorMap *map, CUtensorMapDataType type, int elem, int rank, cons
 }
 
 template <int FORM, int TC, bool SUMS>
-cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int sms, cudaStream_t stream)
+cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int dev, int sms, cudaStream_t stream)
 {
     using Sh = Shape<TC>;
     constexpr bool FP8 = FORM == kFp8, DW = FORM == kDw;
@@ -824,10 +1172,13 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
     } else {
         const uint64_t da[2] = {K, T};
         const uint64_t dn[3] = {K, N, G}, dk[3] = {N, K, G};
-        const uint32_t ba[2] = {KB, Sh::kLoadCols}, bp[2] = {KB, Sh::kLoadCols / 4}, bn[3] = {KB, kLanes, 1}, bk[3] = {64, 64, 1};
+        const uint32_t ba[2] = {KB, Sh::kLoadCols}, bp[2] = {KB, Sh::kLoadCols / 4}, bn[3] = {KB, kLanes, 1}, bk[3] = {64, 64, 1},
+                       bq[3] = {KB, Sh::kLoadCols / 4, 1};
         ok = (FORM == kKn ? encode(&maps.lane, type, elem, 3, p.B, dk, bk)
                           : encode(&maps.lane, type, elem, 3, p.B, dn, bn)) &&
-             encode(&maps.col, type, elem, 2, p.A, da, ba) && encode(&maps.col_part, type, elem, 2, p.A, da, bp);
+             encode(&maps.col, type, elem, 2, p.A, da, ba) &&
+             (FP8 && Sh::kPair ? encode(&maps.col_part, type, elem, 3, p.B, dn, bq)
+                               : encode(&maps.col_part, type, elem, 2, p.A, da, bp));
     }
     if (!ok) return cudaErrorInvalidValue;
     GroupedArgs a = {};
@@ -844,20 +1195,27 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
     a.out_type = p.out_type;
     a.bf16 = p.bf16;
     a.splits = splits;
-    const uint32_t sums = splits > 1 ? TC * kLanes * 4 : 0, scales = FP8 ? kScaleRing * TC * 4 : 0;
+    const uint32_t sums = splits > 1 ? TC * kLanes * 4 : 0, scales = FP8 && !Sh::kPair ? kScaleRing * Sh::kScaleSlot * 4 : 0,
+                   staging = FP8 ? kEpilogueWarps * Sh::kStageWarp : 0;
     const uint32_t tables = (static_cast<uint32_t>(2 * (p.G + 1)) * 4 + 127) / 128 * 128;
-    const uint32_t rest = sums + scales + tables;
+    const uint32_t rest = sums + scales + staging + tables;
     const uint32_t room = static_cast<uint32_t>(kSmemLimit) - 1024 - rest;
     a.stages = static_cast<int>(std::min<uint32_t>(kMaxRing, room / Sh::kStage));
     a.sum_off = a.stages * Sh::kStage;
     a.scale_off = a.sum_off + sums;
-    a.table_off = a.scale_off + scales;
+    a.stage_off = a.scale_off + scales;
+    a.table_off = a.stage_off + staging;
     // enough shared memory that the blocks sharing an SM never ask for more
     // than its 512 tensor-memory columns (tmem_fits)
     const size_t smem = kSmemLimit;
-    const void *fn = reinterpret_cast<const void *>(grouped_kernel<FORM, TC, SUMS>);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return note_error(e, "cudaFuncSetAttribute(grouped_kernel)");
+    static std::atomic<bool> ready[kMaxDevices];       // the attribute is set, per device
+    if (dev >= kMaxDevices || !ready[dev].load(std::memory_order_relaxed)) {
+        const void *fn = reinterpret_cast<const void *>(grouped_kernel<FORM, TC, SUMS>);
+        const cudaError_t e =
+            cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return note_error(e, "cudaFuncSetAttribute(grouped_kernel)");
+        if (dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg = {};
     const int cluster = Sh::kPair ? 2 : splits;
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(tiles, sms / cluster));
@@ -878,11 +1236,11 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
 }
 
 template <int FORM, int TC>
-cudaError_t launch_form(const GroupedProblem &p, int splits, int64_t tiles, int sms, cudaStream_t stream)
+cudaError_t launch_form(const GroupedProblem &p, int splits, int64_t tiles, int dev, int sms, cudaStream_t stream)
 {
     if constexpr (FORM != kFp8)
-        if (p.out_type != 0) return launch_tiles<FORM, TC, false>(p, splits, tiles, sms, stream);
-    return launch_tiles<FORM, TC, true>(p, splits, tiles, sms, stream);
+        if (p.out_type != 0) return launch_tiles<FORM, TC, false>(p, splits, tiles, dev, sms, stream);
+    return launch_tiles<FORM, TC, true>(p, splits, tiles, dev, sms, stream);
 }
 
 }  // namespace
@@ -912,30 +1270,40 @@ GroupedPlan plan_grouped(const GroupedProblem &p, int sms)
 }
 
 template <int FORM>
-cudaError_t launch_plan(const GroupedProblem &p, const GroupedPlan &plan, int64_t tiles, int sms, cudaStream_t stream)
+cudaError_t launch_plan(const GroupedProblem &p, const GroupedPlan &plan, int64_t tiles, int dev, int sms, cudaStream_t stream)
 {
     switch (plan.tc) {
-    case 256: return launch_form<FORM, 256>(p, plan.splits, tiles, sms, stream);
-    case 128: return launch_form<FORM, 128>(p, plan.splits, tiles, sms, stream);
-    default:
-        if constexpr (FORM != kDw) return launch_form<FORM, 32>(p, plan.splits, tiles, sms, stream);
-        return note_error(cudaErrorInvalidConfiguration, "columns of a tile");
+    case 256: return launch_form<FORM, 256>(p, plan.splits, tiles, dev, sms, stream);
+    case 128: return launch_form<FORM, 128>(p, plan.splits, tiles, dev, sms, stream);
+    case 64:
+        if constexpr (FORM != kDw) return launch_form<FORM, 64>(p, plan.splits, tiles, dev, sms, stream);
+        break;
+    case 32:
+        if constexpr (FORM != kDw) return launch_form<FORM, 32>(p, plan.splits, tiles, dev, sms, stream);
+        break;
     }
+    return note_error(cudaErrorInvalidConfiguration, "columns of a tile");
 }
 
 cudaError_t launch_grouped(const GroupedProblem &p, cudaStream_t stream)
 {
-    int dev = 0, sms = 0;
+    static std::atomic<int> counts[kMaxDevices];
+    int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return note_error(e, "cudaDeviceGetAttribute(MultiProcessorCount)");
+    if (e != cudaSuccess) return note_error(e, "cudaGetDevice");
+    int sms = dev < kMaxDevices ? counts[dev].load(std::memory_order_relaxed) : 0;
+    if (sms == 0) {
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return note_error(e, "cudaDeviceGetAttribute(MultiProcessorCount)");
+        if (dev < kMaxDevices) counts[dev].store(sms, std::memory_order_relaxed);
+    }
     const GroupedPlan plan = plan_grouped(p, sms);
     const int64_t tiles = grouped_tiles(p, plan.tc);
     switch (p.form) {
-    case GroupedForm::kFp8: return launch_plan<kFp8>(p, plan, tiles, sms, stream);
-    case GroupedForm::kNk: return launch_plan<kNk>(p, plan, tiles, sms, stream);
-    case GroupedForm::kKn: return launch_plan<kKn>(p, plan, tiles, sms, stream);
-    default: return launch_plan<kDw>(p, plan, tiles, sms, stream);
+    case GroupedForm::kFp8: return launch_plan<kFp8>(p, plan, tiles, dev, sms, stream);
+    case GroupedForm::kNk: return launch_plan<kNk>(p, plan, tiles, dev, sms, stream);
+    case GroupedForm::kKn: return launch_plan<kKn>(p, plan, tiles, dev, sms, stream);
+    default: return launch_plan<kDw>(p, plan, tiles, dev, sms, stream);
     }
 }
 
