@@ -389,34 +389,6 @@ __device__ __forceinline__ uint64_t pack_b32x2(uint32_t lo, uint32_t hi)
     return d;
 }
 
-// ------------------------------------------------- bulk stores
-
-// Copies `bytes` (a multiple of 16) of shared memory to global memory (both
-// 16-byte aligned), in the thread's open group.
-__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes)
-{
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
-                 "r"(src), "r"(bytes)
-                 : "memory");
-}
-
-__device__ __forceinline__ void bulk_commit()
-{
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-
-// The thread's groups have read their shared memory.
-__device__ __forceinline__ void bulk_wait_read()
-{
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-
-// The thread's groups are done: their writes are made.
-__device__ __forceinline__ void bulk_wait()
-{
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-
 // ------------------------------------------------- pairs of thread blocks
 // (cta_group::2: the two blocks of a cluster of 2 multiply one tile; the block
 // of even rank issues)

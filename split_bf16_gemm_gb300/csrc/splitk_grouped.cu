@@ -57,8 +57,8 @@ __device__ unsigned g_grouped_status;
 
 constexpr uint64_t kWaitLimitNs = 1000000000ull;   // 1 s
 constexpr int kThreads = 384;
-constexpr int kRoleWarps = 4;                       // of which the last is idle: registers move by four warps
 constexpr int kEpilogueWarps = 8;
+constexpr int kRoleWarps = 4;                       // of which the last is idle: registers move by four warps
 constexpr int kLanes = 128;
 constexpr uint32_t kLaneBytes = kLanes * 128;       // one k-block of the lane operand
 constexpr int kMaxRing = 12;
@@ -86,12 +86,12 @@ struct Shape {
     // p stand together, p's 4 words further round the banks than the last's.
     static constexpr int kHalf = TC / 2;
     static constexpr int kScalePitch = kHalf / 4 + 4;
-    static constexpr int kScaleSlot = 2 * 4 * kScalePitch;
+    static constexpr int kScaleSlot = kPair ? 2 * kLanes : 2 * 4 * kScalePitch;   // ROWS: lanes by two weight blocks
     static constexpr int kFragCols = kHalf < 32 ? kHalf : 32;     // columns of one tensor-memory load
-    // staged rows of 16-bit outputs, padded by 16 bytes: 32 lanes a column, or
-    // (TC = 256) the warp's 128 columns of a lane
-    static constexpr uint32_t kStageRow = kPair ? 2 * kHalf + 16 : 80;
-    static constexpr uint32_t kStageWarp = (kPair ? 32 : kFragCols) * kStageRow;
+    // staged rows of 16-bit outputs, padded by 16 bytes: 32 lanes of a column,
+    // or (ROWS) 32 columns of a lane
+    static constexpr uint32_t kStageRow = 80;
+    static constexpr uint32_t kStageWarp = kFragCols * kStageRow;
 };
 
 struct GroupedArgs {
@@ -150,6 +150,22 @@ template <>
 __device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Two values rounded to 16 bits, the first in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t pair16(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pair16<__half>(float lo, float hi)
+{
+    const __half2 y = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&y);
+}
+template <>
+__device__ __forceinline__ uint32_t pair16<__nv_bfloat16>(float lo, float hi)
+{
+    const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&y);
+}
 
 // The first `live` of N values to rows `pitch` elements apart.  No branch
 // inside: with two warps to a scheduler a branch's latency is not hidden (the
@@ -565,7 +581,62 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         for (int w = first; w < total; w += step) {
             Tile t;
             locate(w, g, t);
-            if constexpr (FP8 && !ROWS) {
+            if constexpr (ROWS) {
+                // Four k-blocks of 128 tokens' scales at a time.  A token's
+                // scales stand together, so that a warp's read touches 32
+                // lines: this warp makes them once, 16 bytes wide where rows
+                // allow it, for the eight that use them.
+                const int nbs = (args.lanes + kLanes - 1) / kLanes, nb = t.col0 / kLanes;
+                const float *const sb = args.sb + (static_cast<size_t>(t.g) * nbs + nb) * args.kblocks;
+                const float *const sb2 = sb + (nb + 1 < nbs ? args.kblocks : 0);
+                const bool wide = args.kblocks % 4 == 0;
+                const float *sa[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p)              // lanes without a token: any row
+                    sa[p] = args.sa + static_cast<size_t>(t.rows > 0 ? t.lane0 + min(p * 32 + lane, t.rows - 1) : 0) *
+                                          args.kblocks;
+                float4 next[4], w, w2;
+                auto read4 = [&](const float *at, int b) {
+                    if (wide) return __ldg(reinterpret_cast<const float4 *>(at + b));
+                    const int last = t.nkb - 1;
+                    return make_float4(__ldg(at + b), __ldg(at + min(b + 1, last)), __ldg(at + min(b + 2, last)),
+                                       __ldg(at + min(b + 3, last)));
+                };
+                auto fetch = [&](int b) {
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) next[p] = read4(sa[p], b);
+                    w = read4(sb, b);
+                    w2 = read4(sb2, b);
+                };
+                fetch(0);
+                for (int b = 0; b < t.nkb && !dead; b += 4) {
+                    float now[4][4], f[4], f2[4];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) now[p][0] = next[p].x, now[p][1] = next[p].y, now[p][2] = next[p].z, now[p][3] = next[p].w;
+                    f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
+                    f2[0] = w2.x, f2[1] = w2.y, f2[2] = w2.z, f2[3] = w2.w;
+                    if (b + 4 < t.nkb) fetch(b + 4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (b + j >= t.nkb || dead) break;
+                        if (!__all_sync(0xffffffffu, bounded_wait(scale_empty(slot), ph ^ 1u, &abort_s))) {
+                            dead = true;
+                            break;
+                        }
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            scale_buf[slot * Sh::kScaleSlot + p * 32 + lane] = now[p][j] * f[j];
+                            scale_buf[slot * Sh::kScaleSlot + kLanes + p * 32 + lane] = now[p][j] * f2[j];
+                        }
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(scale_full(slot));
+                        if (++slot == kScaleRing) {
+                            slot = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+            } else if constexpr (FP8) {
                 constexpr int PER = TC / 32, BATCH = 4;
                 const int lane_blocks = (args.lanes + kLanes - 1) / kLanes;
                 const float *const sb =
@@ -686,88 +757,75 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
             };
             if constexpr (ROWS) {
                 // A token to a thread: its scale times the weight block's is one
-                // factor for the warp's 128 columns, and the sums of two columns
-                // share a 64-bit register (fma.rn.f32x2).  Reading 128 columns
-                // and adding them takes 8 warps 310 cycles, against 512 for the
-                // k-block's MMAs; as fragments with a scale for each column it
-                // takes 850.
-                constexpr int AHEAD = 4;                       // k-blocks whose factors are fetched together
-                const int nbs = (args.lanes + kLanes - 1) / kLanes;
-                const int nb = min((t.col0 + c_lo) / kLanes, nbs - 1);   // columns past N: any block's
-                const float *const sb = args.sb + (static_cast<size_t>(t.g) * nbs + nb) * args.kblocks;
-                const float *const sa = args.sa + static_cast<size_t>(t.lane0 + min(my, max(t.rows, 1) - 1)) * args.kblocks;
-                float next[AHEAD];
-                auto fetch = [&](int b) {
-#pragma unroll
-                    for (int j = 0; j < AHEAD; ++j) {
-                        const int kb = min(b + j, t.nkb - 1);
-                        next[j] = t.rows > 0 ? __ldg(sa + kb) * __ldg(sb + kb) : 0.f;
-                    }
-                };
+                // factor for the warp's 128 columns (the tile's columns are
+                // whole weight blocks), and the sums of two columns share a
+                // 64-bit register (fma.rn.f32x2).  Reading and adding 128
+                // columns takes 8 warps 310 cycles by themselves and 570 beside
+                // the MMAs, which take 512 a k-block; as fragments with a
+                // scale for each column, 855 by themselves.
                 uint64_t acc[HALF / 2];
 #pragma unroll
                 for (int j = 0; j < HALF / 2; ++j) acc[j] = 0;
                 const int chunks = (min(HALF, max(0, t.width - c_lo)) + 15) / 16;
-                fetch(0);
-                for (int b = 0; b < t.nkb && !dead; b += AHEAD) {
-                    float now[AHEAD];
-#pragma unroll
-                    for (int j = 0; j < AHEAD; ++j) now[j] = next[j];
-                    if (b + AHEAD < t.nkb) fetch(b + AHEAD);
+                const float *const factors = scale_buf + c_lo / kLanes * kLanes + my;
 #pragma unroll 1
-                    for (int j = 0; j < AHEAD && b + j < t.nkb; ++j) {
-                        const float factor = now[0];
-#pragma unroll
-                        for (int i = 0; i + 1 < AHEAD; ++i) now[i] = now[i + 1];
-                        bool ok = ptx::mbar_try_wait(acc_full(buf), aph);
+                for (int i = 0; i < t.nkb; ++i) {
+                    bool ok = ptx::mbar_try_wait(acc_full(buf), aph) & ptx::mbar_try_wait(scale_full(slot), ph);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = bounded_wait(acc_full(buf), aph, &abort_s) && bounded_wait(scale_full(slot), ph, &abort_s);
                         if (!__all_sync(0xffffffffu, ok)) {
-                            ok = bounded_wait(acc_full(buf), aph, &abort_s);
-                            if (!__all_sync(0xffffffffu, ok)) {
-                                dead = true;
-                                break;
-                            }
+                            dead = true;
+                            break;
                         }
-                        ptx::tc_fence_after_sync();
-                        const uint64_t f2 = ptx::pack_b32x2(__float_as_uint(factor), __float_as_uint(factor));
-                        const uint32_t from = lane_addr + static_cast<uint32_t>(buf * TC);
-                        uint32_t v[2][16];
-                        auto add = [&](int c) {
+                    }
+                    ptx::tc_fence_after_sync();
+                    const float factor = factors[slot * Sh::kScaleSlot];
+                    const uint64_t f2 = ptx::pack_b32x2(__float_as_uint(factor), __float_as_uint(factor));
+                    const uint32_t from = lane_addr + static_cast<uint32_t>(buf * TC);
+                    auto release = [&]() {
+                        ptx::tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) {
+                            release_acc(acc_empty(buf));
+                            ptx::mbar_arrive(scale_empty(slot));
+                        }
+                    };
+                    uint32_t v[2][16];
+                    auto add = [&](int c) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                acc[c * 8 + i] = ptx::fma_f32x2(ptx::pack_b32x2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), f2,
-                                                                acc[c * 8 + i]);
-                        };
-                        auto release = [&]() {
-                            ptx::tc_fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0) release_acc(acc_empty(buf));
-                        };
-                        if (chunks == HALF / 16) {
-                            ptx::tmem_ld_start_x16(from, v[0]);
+                        for (int j = 0; j < 8; ++j)
+                            acc[c * 8 + j] = ptx::fma_f32x2(ptx::pack_b32x2(v[c & 1][2 * j], v[c & 1][2 * j + 1]), f2,
+                                                            acc[c * 8 + j]);
+                    };
+                    if (chunks == HALF / 16) {                 // every column in use: no branch a load
+                        ptx::tmem_ld_start_x16(from, v[0]);
 #pragma unroll
-                            for (int c = 0; c < HALF / 16; ++c) {
+                        for (int c = 0; c < HALF / 16; ++c) {
+                            ptx::tmem_wait_x16(v[c & 1]);
+                            if (c + 1 < HALF / 16)
+                                ptx::tmem_ld_start_x16(from + (c + 1) * 16, v[(c + 1) & 1]);
+                            else
+                                release();
+                            add(c);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < HALF / 16; ++c) {
+                            if (c < chunks) {
+                                ptx::tmem_ld_start_x16(from + c * 16, v[c & 1]);
                                 ptx::tmem_wait_x16(v[c & 1]);
-                                if (c + 1 < HALF / 16)
-                                    ptx::tmem_ld_start_x16(from + (c + 1) * 16, v[(c + 1) & 1]);
-                                else
-                                    release();
                                 add(c);
                             }
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < HALF / 16; ++c) {
-                                if (c < chunks) {
-                                    ptx::tmem_ld_start_x16(from + c * 16, v[c & 1]);
-                                    ptx::tmem_wait_x16(v[c & 1]);
-                                    add(c);
-                                }
-                            }
-                            release();
                         }
-                        if (++buf == Sh::kAcc) {
-                            buf = 0;
-                            aph ^= 1u;
-                        }
+                        release();
+                    }
+                    if (++buf == Sh::kAcc) {
+                        buf = 0;
+                        aph ^= 1u;
+                    }
+                    if (++slot == kScaleRing) {
+                        slot = 0;
+                        ph ^= 1u;
                     }
                 }
                 auto value = [&](int j) {
@@ -777,31 +835,41 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                 const size_t at = static_cast<size_t>(t.lane0 + my) * pitch + t.col0 + c_lo;
                 if (dead || cols <= 0) {
                 } else if (args.out_type != 0 && args.lanes % 8 == 0) {
-                    // each thread stages its row and copies it out; the copy goes
-                    // on beside the next tile's sums
-                    const uint32_t mine = ptx::smem_addr(base + args.stage_off) +
-                                          static_cast<uint32_t>((warp - kRoleWarps) * 32 + lane) * Sh::kStageRow;
-                    ptx::bulk_wait_read();
+                    // 32 columns at a time through shared memory, then 64 bytes
+                    // of eight rows to a store
+                    const uint32_t warp_at = ptx::smem_addr(base + args.stage_off) +
+                                             static_cast<uint32_t>(warp - kRoleWarps) * Sh::kStageWarp;
+                    const uint32_t mine = warp_at + static_cast<uint32_t>(lane) * Sh::kStageRow;
+                    auto staged = [&](auto *to) {
+                        using T = std::remove_pointer_t<decltype(to)>;
+                        T *const out = to + static_cast<size_t>(t.lane0 + quarter * 32) * pitch + t.col0 + c_lo;
 #pragma unroll
-                    for (int c = 0; c < HALF; c += 8) {
-                        uint32_t x[4];
+                        for (int c = 0; c < HALF; c += 32) {
+                            __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float lo = value(c + 2 * i), hi = value(c + 2 * i + 1);
-                            if (args.out_type == 1) {
-                                const __half2 y = __floats2half2_rn(lo, hi);
-                                x[i] = *reinterpret_cast<const uint32_t *>(&y);
-                            } else {
-                                const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
-                                x[i] = *reinterpret_cast<const uint32_t *>(&y);
+                            for (int d = 0; d < 32; d += 8)
+                                ptx::st_shared_v4(mine + static_cast<uint32_t>(d) * 2u,
+                                                  pair16<T>(value(c + d), value(c + d + 1)),
+                                                  pair16<T>(value(c + d + 2), value(c + d + 3)),
+                                                  pair16<T>(value(c + d + 4), value(c + d + 5)),
+                                                  pair16<T>(value(c + d + 6), value(c + d + 7)));
+                            __syncwarp();
+                            const int col = c + (lane & 3) * 8;
+                            const bool in = col < cols;
+#pragma unroll
+                            for (int r = 0; r < 32; r += 8) {
+                                const int row = r + (lane >> 2);
+                                const float4 x = ptx::ld_shared_v4(warp_at + static_cast<uint32_t>(row) * Sh::kStageRow +
+                                                                   static_cast<uint32_t>(lane & 3) * 16u);
+                                if (in && quarter * 32 + row < t.rows)
+                                    *reinterpret_cast<float4 *>(out + static_cast<size_t>(row) * pitch + col) = x;
                             }
                         }
-                        ptx::st_shared_v4(mine + static_cast<uint32_t>(c) * 2u, x[0], x[1], x[2], x[3]);
-                    }
-                    ptx::fence_proxy_async_smem();
-                    if (my < t.rows)
-                        ptx::bulk_store(static_cast<uint16_t *>(args.out) + at, mine, static_cast<uint32_t>(cols) * 2u);
-                    ptx::bulk_commit();
+                    };
+                    if (args.out_type == 1)
+                        staged(static_cast<__half *>(args.out));
+                    else
+                        staged(static_cast<__nv_bfloat16 *>(args.out));
                 } else if (my < t.rows) {
                     // F32, or rows whose 16-bit length is no multiple of 16 bytes
                     auto direct = [&](auto *out) {
@@ -933,41 +1001,39 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                 } else if (args.out_type != 0 && args.lanes % 8 == 0) {
                     // 16-bit outputs: 32 lanes by GC columns through shared
                     // memory (transposed on the way), then 64 bytes a row
-                    uint16_t *const out = static_cast<uint16_t *>(args.out) + static_cast<size_t>(t.col0) * pitch;
                     const uint32_t mine = ptx::smem_addr(base + args.stage_off) +
                                           static_cast<uint32_t>(warp - kRoleWarps) * Sh::kStageWarp;
                     const int n = t.lane0 + quarter * 32 + (lane & 3) * 8;
-                    auto pair16 = [&](int c, int h, int i, int rp) {
-                        const float lo = value(c, h, i, rp, 0), hi = value(c, h, i, rp, 1);
-                        uint32_t x;
-                        if (args.out_type == 1) {
-                            const __half2 y = __floats2half2_rn(lo, hi);
-                            x = *reinterpret_cast<const uint32_t *>(&y);
-                        } else {
-                            const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
-                            x = *reinterpret_cast<const uint32_t *>(&y);
+                    auto staged = [&](auto *to) {
+                        using T = std::remove_pointer_t<decltype(to)>;
+                        T *const out = to + static_cast<size_t>(t.col0) * pitch + n;
+                        auto pair = [&](int c, int h, int i, int rp) {
+                            return pair16<T>(value(c, h, i, rp, 0), value(c, h, i, rp, 1));
+                        };
+#pragma unroll
+                        for (int c = 0; c < GROUPS; ++c) {
+                            if (c >= groups) break;
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < GC / 8; ++i)
+                                ptx::stmatrix_x4_trans(mine + static_cast<uint32_t>(i * 8 + (lane & 7)) * Sh::kStageRow +
+                                                           static_cast<uint32_t>(lane >> 3) * 16u,
+                                                       pair(c, 0, i, 0), pair(c, 0, i, 1), pair(c, 1, i, 0), pair(c, 1, i, 1));
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < GC / 8; ++i) {
+                                const int col = c_lo + c * GC + i * 8 + (lane >> 2);
+                                const float4 x = ptx::ld_shared_v4(mine + static_cast<uint32_t>(i * 8 + (lane >> 2)) * Sh::kStageRow +
+                                                                   static_cast<uint32_t>(lane & 3) * 16u);
+                                if (col < t.cols && n < args.lanes)
+                                    *reinterpret_cast<float4 *>(out + static_cast<size_t>(col) * pitch) = x;
+                            }
                         }
-                        return x;
                     };
-#pragma unroll
-                    for (int c = 0; c < GROUPS; ++c) {
-                        if (c >= groups) break;
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < GC / 8; ++i)
-                            ptx::stmatrix_x4_trans(mine + static_cast<uint32_t>(i * 8 + (lane & 7)) * Sh::kStageRow +
-                                                       static_cast<uint32_t>(lane >> 3) * 16u,
-                                                   pair16(c, 0, i, 0), pair16(c, 0, i, 1), pair16(c, 1, i, 0), pair16(c, 1, i, 1));
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < GC / 8; ++i) {
-                            const int col = c_lo + c * GC + i * 8 + (lane >> 2);
-                            const float4 x = ptx::ld_shared_v4(mine + static_cast<uint32_t>(i * 8 + (lane >> 2)) * Sh::kStageRow +
-                                                               static_cast<uint32_t>(lane & 3) * 16u);
-                            if (col < t.cols && n < args.lanes)
-                                *reinterpret_cast<float4 *>(out + static_cast<size_t>(col) * pitch + n) = x;
-                        }
-                    }
+                    if (args.out_type == 1)
+                        staged(static_cast<__half *>(args.out));
+                    else
+                        staged(static_cast<__nv_bfloat16 *>(args.out));
                 } else {
                     // F32 rows in pieces of 32 bytes; rows whose 16-bit length
                     // is no multiple of 16 bytes, value by value
@@ -1109,7 +1175,6 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
             }
         }
     }
-    if (ROWS && warp >= kRoleWarps) ptx::bulk_wait();   // the outputs are written when the grid ends
     ptx::tc_fence_before_sync();
     __syncthreads();
     if constexpr (PAIR) cluster_sync();   // neither block's memory is in use by the other any more
@@ -1195,7 +1260,7 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
     a.out_type = p.out_type;
     a.bf16 = p.bf16;
     a.splits = splits;
-    const uint32_t sums = splits > 1 ? TC * kLanes * 4 : 0, scales = FP8 && !Sh::kPair ? kScaleRing * Sh::kScaleSlot * 4 : 0,
+    const uint32_t sums = splits > 1 ? TC * kLanes * 4 : 0, scales = FP8 ? kScaleRing * Sh::kScaleSlot * 4 : 0,
                    staging = FP8 ? kEpilogueWarps * Sh::kStageWarp : 0;
     const uint32_t tables = (static_cast<uint32_t>(2 * (p.G + 1)) * 4 + 127) / 128 * 128;
     const uint32_t rest = sums + scales + staging + tables;
