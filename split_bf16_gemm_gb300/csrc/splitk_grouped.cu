@@ -45,6 +45,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "ptx.cuh"
@@ -81,6 +82,10 @@ struct Shape {
     static constexpr uint32_t kColBytes = kLoadCols * 128;
     static constexpr uint32_t kStage = kLaneBytes + kColBytes;
     static constexpr int kTileLanes = kLanes * kBlocks;
+    // Thread blocks of an SM.  A tile of 32 columns keeps neither the loads nor
+    // the tensor cores busy by itself; two blocks share an SM's memory.
+    static constexpr int kPerSm = TC == 32 ? 2 : 1;
+    static constexpr size_t kSmem = kPerSm == 2 ? 112 * 1024 : kSmemLimit;
     // kFp8, a warp's part of the columns (half the tile's): read as fragments
     // of 8 columns, of which a thread holds two.  The scales of thread t % 4 =
     // p stand together, p's 4 words further round the banks than the last's.
@@ -197,7 +202,7 @@ __device__ __forceinline__ void store_values(void *out, int type, size_t at, siz
 }
 
 template <int FORM, int TC, bool SUMS>
-__global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_constant__ Maps maps, const GroupedArgs args)
+__global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(const __grid_constant__ Maps maps, const GroupedArgs args)
 {
     static_assert(SUMS || FORM != kFp8, "8-bit operands need the F32 sums in registers");
     using Sh = Shape<TC>;
@@ -245,7 +250,12 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     };
     const int stages = args.stages, S = args.splits;
 
+    const int lane_tiles = (args.lanes + Sh::kTileLanes - 1) / Sh::kTileLanes;
     if (tid == 0) {
+        if (args.offsets == nullptr) {               // one run of all rows
+            offs[0] = 0, offs[1] = args.T;
+            pref[0] = 0, pref[1] = lane_tiles * ((args.T + TC - 1) / TC);
+        }
         ptx::prefetch_tensormap(&maps.lane);
         ptx::prefetch_tensormap(&maps.col);
         for (int i = 0; i < stages; ++i) {
@@ -289,44 +299,46 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
 
     // ---- the runs, made monotone and within [0, T] whatever the offsets
     // hold, and the number of tiles before each
-    const int lane_tiles = (args.lanes + Sh::kTileLanes - 1) / Sh::kTileLanes;
-    if (args.offsets == nullptr) {
-        if (tid < 2) offs[tid] = tid ? args.T : 0;
-    } else {
-        for (int i = tid; i <= args.G; i += kThreads) offs[i] = min(max(args.offsets[i], 0), args.T);
-    }
-    __syncthreads();
-    if (warp == 2) {
-        int most = offs[0], tiles = 0;
-        if (lane == 0) pref[0] = 0;
-        for (int b = 0; b < args.G; b += 32) {
-            const int g = b + lane;
-            int end = g < args.G ? offs[g + 1] : 0;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, end, d);
-                if (lane >= d) end = max(end, o);
-            }
-            end = max(end, most);
-            int begin = __shfl_up_sync(0xffffffffu, end, 1);
-            if (lane == 0) begin = most;
-            const int ext = DW ? args.cols : end - begin;
-            int n = g < args.G ? lane_tiles * ((ext + TC - 1) / TC) : 0;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, n, d);
-                if (lane >= d) n += o;
-            }
-            __syncwarp();
-            if (g < args.G) {
-                offs[g + 1] = end;
-                pref[g + 1] = tiles + n;
-            }
-            most = __shfl_sync(0xffffffffu, end, 31);
-            tiles += __shfl_sync(0xffffffffu, n, 31);
+    if (args.offsets != nullptr) {
+        const bool staged = args.G > 32;               // more than one round of a warp: read all at once first
+        if (staged) {
+            for (int i = tid; i <= args.G; i += kThreads) offs[i] = min(max(args.offsets[i], 0), args.T);
+            __syncthreads();
         }
+        if (warp == 2) {
+            auto offset = [&](int i) { return staged ? offs[i] : min(max(args.offsets[i], 0), args.T); };
+            int most = offset(0), tiles = 0;
+            const int begin0 = most;
+            for (int b = 0; b < args.G; b += 32) {
+                const int g = b + lane;
+                int end = g < args.G ? offset(g + 1) : 0;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, end, d);
+                    if (lane >= d) end = max(end, o);
+                }
+                end = max(end, most);
+                int begin = __shfl_up_sync(0xffffffffu, end, 1);
+                if (lane == 0) begin = most;
+                const int ext = DW ? args.cols : end - begin;
+                int n = g < args.G ? lane_tiles * ((ext + TC - 1) / TC) : 0;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, n, d);
+                    if (lane >= d) n += o;
+                }
+                __syncwarp();
+                if (g < args.G) {
+                    offs[g + 1] = end;
+                    pref[g + 1] = tiles + n;
+                }
+                most = __shfl_sync(0xffffffffu, end, 31);
+                tiles += __shfl_sync(0xffffffffu, n, 31);
+            }
+            if (lane == 0) offs[0] = begin0, pref[0] = 0;
+        }
+        __syncthreads();
     }
-    __syncthreads();
     const int total = pref[args.G];
     const int rank = S > 1 ? static_cast<int>(blockIdx.x) % S : 0;
     const int group = PAIR ? 2 : S;                   // blocks at work on a tile
@@ -1149,28 +1161,39 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
             if (S > 1) {
                 __syncwarp();
                 cluster_sync();                        // every rank's sums stand in its shared memory
-                // this block adds columns rank, rank + S, ...; eight at a time, so
-                // that the reads of other blocks' memory overlap
-                constexpr int AT_ONCE = 8;
-                for (int c0 = rank + S * half; c0 < t.cols; c0 += 2 * S * AT_ONCE) {
-                    float sum[AT_ONCE], x[AT_ONCE];
-                    for (int r = 0; r < S; ++r) {
-                        const uint32_t at = ptx::mapa(ptx::smem_addr(sum_buf + my), r);
+                // This block adds columns rank, rank + S, ... in rank order, 16
+                // reads of the blocks' memory in flight at a time.
+                auto add_ranks = [&](auto splits) {
+                    constexpr int R = decltype(splits)::value, AT_ONCE = 16 / R;
+                    const uint32_t mine = ptx::smem_addr(sum_buf + my);
+                    uint32_t at[R];
+#pragma unroll
+                    for (int r = 0; r < R; ++r) at[r] = ptx::mapa(mine, r);
+                    for (int c0 = rank + R * half; c0 < t.cols; c0 += 2 * R * AT_ONCE) {
+                        float x[AT_ONCE][R];
 #pragma unroll
                         for (int j = 0; j < AT_ONCE; ++j) {
-                            const int c = min(c0 + 2 * S * j, t.cols - 1);
-                            x[j] = ptx::ld_cluster_f32(at + static_cast<uint32_t>(c * kLanes) * 4u);
+                            const uint32_t off = static_cast<uint32_t>(min(c0 + 2 * R * j, t.cols - 1) * kLanes) * 4u;
+#pragma unroll
+                            for (int r = 0; r < R; ++r) x[j][r] = ptx::ld_cluster_f32(at[r] + off);
                         }
 #pragma unroll
-                        for (int j = 0; j < AT_ONCE; ++j) sum[j] = r == 0 ? x[j] : sum[j] + x[j];
-                    }
+                        for (int j = 0; j < AT_ONCE; ++j) {
+                            float sum = x[j][0];
 #pragma unroll
-                    for (int j = 0; j < AT_ONCE; ++j) {
-                        const int c = c0 + 2 * S * j;
-                        store_values<1>(args.out, args.out_type, out0 + static_cast<size_t>(c) * pitch, pitch,
-                                        live && c < t.cols, [&](int) { return sum[j]; });
+                            for (int r = 1; r < R; ++r) sum += x[j][r];
+                            const int c = c0 + 2 * R * j;
+                            store_values<1>(args.out, args.out_type, out0 + static_cast<size_t>(c) * pitch, pitch,
+                                            live && c < t.cols, [&](int) { return sum; });
+                        }
                     }
-                }
+                };
+                if (S == 2)
+                    add_ranks(std::integral_constant<int, 2>());
+                else if (S == 4)
+                    add_ranks(std::integral_constant<int, 4>());
+                else
+                    add_ranks(std::integral_constant<int, 8>());
                 cluster_sync();                        // and may be overwritten
             }
         }
@@ -1264,7 +1287,7 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
                    staging = FP8 ? kEpilogueWarps * Sh::kStageWarp : 0;
     const uint32_t tables = (static_cast<uint32_t>(2 * (p.G + 1)) * 4 + 127) / 128 * 128;
     const uint32_t rest = sums + scales + staging + tables;
-    const uint32_t room = static_cast<uint32_t>(kSmemLimit) - 1024 - rest;
+    const uint32_t room = static_cast<uint32_t>(Sh::kSmem) - 1024 - rest;
     a.stages = static_cast<int>(std::min<uint32_t>(kMaxRing, room / Sh::kStage));
     a.sum_off = a.stages * Sh::kStage;
     a.scale_off = a.sum_off + sums;
@@ -1272,7 +1295,7 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
     a.table_off = a.stage_off + staging;
     // enough shared memory that the blocks sharing an SM never ask for more
     // than its 512 tensor-memory columns (tmem_fits)
-    const size_t smem = kSmemLimit;
+    const size_t smem = Sh::kSmem;
     static std::atomic<bool> ready[kMaxDevices];       // the attribute is set, per device
     if (dev >= kMaxDevices || !ready[dev].load(std::memory_order_relaxed)) {
         const void *fn = reinterpret_cast<const void *>(grouped_kernel<FORM, TC, SUMS>);
@@ -1283,7 +1306,7 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
     }
     cudaLaunchConfig_t cfg = {};
     const int cluster = Sh::kPair ? 2 : splits;
-    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(tiles, sms / cluster));
+    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(tiles, sms * Sh::kPerSm / cluster));
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
@@ -1319,19 +1342,47 @@ int64_t grouped_tiles(const GroupedProblem &p, int tc)
     return lane_tiles * (p.G == 1 ? (p.T + tc - 1) / tc : p.T / tc + std::min<int64_t>(p.G, p.T));
 }
 
+// The plan with the least time by a model of one launch:
+//   waves * (k-blocks / splits) * us a k-block + waves * us to join the splits
+// The microseconds are measured on GB300 with every SM at work (M 16 to 2048,
+// N 1024 to 8192, K 2048 to 8192, and 8 to 24 runs); each is bound by the loads
+// and, for 8 bits, by the sums.  Runs of unknown lengths are taken to end
+// half a tile past their last full one on average.
 GroupedPlan plan_grouped(const GroupedProblem &p, int sms)
 {
-    GroupedPlan plan = {128, 1};
-    const bool dw = p.form == GroupedForm::kDw;
-    if (!dw && p.T <= 32 * p.G) {
-        plan.tc = 32;
-        const int64_t tiles = grouped_tiles(p, 32);
-        const int64_t kb = (p.K + (p.form == GroupedForm::kFp8 ? 127 : 63)) / (p.form == GroupedForm::kFp8 ? 128 : 64);
-        while (plan.splits < 8 && tiles * plan.splits * 2 <= sms && kb >= plan.splits * 4) plan.splits *= 2;
-    } else if (grouped_tiles(p, 256) >= sms / 2 && (dw ? p.N : p.T) >= 192 * (dw ? 1 : p.G)) {
-        plan.tc = 256;
+    struct Tiling {
+        int tc;
+        double us8, us16, join;
+    };
+    static constexpr Tiling kTilings[] = {   // 32: two blocks to an SM
+        {32, 0.38, 0.30, 1.5}, {64, 0.285, 0.26, 2.}, {128, 0.42, 0.26, 3.3}, {256, 0.54, 0.31, 0.}};
+    constexpr double kAlone = 0.7;           // of those figures, for a 32-column block alone on its SM
+    const bool dw = p.form == GroupedForm::kDw, fp8 = p.form == GroupedForm::kFp8;
+    const int64_t k = dw ? std::max<int64_t>(1, p.T / p.G) : p.K, kb = (k + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64);
+    GroupedPlan best = {128, 1};
+    double least = 0;
+    for (const Tiling &t : kTilings) {
+        if (dw && t.tc < 128) continue;
+        const int64_t tl = t.tc == 256 ? 2 * kLanes : kLanes;
+        const double lane_tiles = static_cast<double>(((dw ? p.K : p.N) + tl - 1) / tl);
+        const double runs = static_cast<double>(std::min(p.G, p.T));
+        const double col_tiles = dw ? static_cast<double>(p.G) * static_cast<double>((p.N + t.tc - 1) / t.tc)
+                                 : p.G == 1 ? static_cast<double>((p.T + t.tc - 1) / t.tc)
+                                            : std::max(runs, static_cast<double>(p.T) / t.tc + runs / 2);
+        const double places = t.tc == 256 ? sms / 2 : t.tc == 32 ? sms * 2 : sms;
+        for (int splits = 1; splits <= 8; splits *= 2) {
+            // a split of fewer than two k-blocks, or more blocks than places, never pays
+            if (splits > 1 && (dw || t.tc == 256 || kb < 2 * splits || lane_tiles * col_tiles * splits > places)) break;
+            const double waves = std::ceil(lane_tiles * col_tiles * splits / places);
+            const double rate = (fp8 ? t.us8 : t.us16) * (t.tc == 32 && lane_tiles * col_tiles * splits <= sms ? kAlone : 1.);
+            const double us = waves * (static_cast<double>((kb + splits - 1) / splits) * rate + (splits > 1 ? t.join : 0.));
+            if (least == 0 || us < least) {
+                least = us;
+                best = {t.tc, splits};
+            }
+        }
     }
-    return plan;
+    return best;
 }
 
 template <int FORM>
