@@ -24,8 +24,8 @@
 //              in the last k-block (they belong to the next run);
 //   warps 4-11 tensor memory -> registers -> output: lane quarter w % 4,
 //              column half w / 4 - 1.
-// kFp8 on large problems (ROWS) exchanges the roles: the lanes are tokens and
-// the columns weights, 256 by 256 to a pair of blocks.
+// kFp8 with many rows (ROWS, TC >= 128) exchanges the roles: the lanes are
+// tokens and the columns weights, so that a thread's scale is one factor.
 // kFp8: F32 scales cannot be applied inside the MMA, so each k-block's product
 // goes to an accumulator of its own (a ring of them in tensor memory), and the
 // last eight warps add it, times the scale, to F32 sums in registers while
@@ -91,10 +91,10 @@ struct Shape {
     // p stand together, p's 4 words further round the banks than the last's.
     static constexpr int kHalf = TC / 2;
     static constexpr int kScalePitch = kHalf / 4 + 4;
-    static constexpr int kScaleSlot = kPair ? 2 * kLanes : 2 * 4 * kScalePitch;   // ROWS: lanes by two weight blocks
+    static constexpr int kScaleSlot = TC >= 128 ? TC : 2 * 4 * kScalePitch;   // ROWS: lanes by weight blocks
     static constexpr int kFragCols = kHalf < 32 ? kHalf : 32;     // columns of one tensor-memory load
-    // staged rows of 16-bit outputs, padded by 16 bytes: 32 lanes of a column,
-    // or (ROWS) 32 columns of a lane
+    // staged rows of 64 bytes, padded by 16: 32 lanes of a column in 16 bits,
+    // or (ROWS) a piece of a lane's columns
     static constexpr uint32_t kStageRow = 80;
     static constexpr uint32_t kStageWarp = kFragCols * kStageRow;
 };
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
     constexpr bool FP8 = FORM == kFp8, DW = FORM == kDw;
     constexpr bool LMN = FORM == kKn || FORM == kDw;   // lane operand contiguous along its lanes
     constexpr bool PAIR = Sh::kPair;
-    constexpr bool ROWS = FP8 && PAIR;                 // lanes are tokens, columns weights
+    constexpr bool ROWS = FP8 && TC >= 128;            // lanes are tokens, columns weights
     constexpr int KB = FP8 ? 128 : 64;
     constexpr int UNIT = FP8 ? 1 : SUMS ? kUnit : 1 << 30;   // k-blocks summed in one accumulator
     constexpr int HALF = TC / 2;                       // columns of an epilogue warp
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
     const uint32_t raw = ptx::smem_addr(dsmem);
     const uint32_t ring = (raw + 1023u) & ~1023u;
     uint8_t *const base = dsmem + (ring - raw);
-    float *const sum_buf = reinterpret_cast<float *>(base + args.sum_off);       // [TC][128], splits > 1
+    float *const sum_buf = reinterpret_cast<float *>(base + args.sum_off);       // [TC][128] (ROWS: [128][TC + 1]), splits > 1
     float *const scale_buf = reinterpret_cast<float *>(base + args.scale_off);   // [kScaleRing][kScaleSlot]
     int *const offs = reinterpret_cast<int *>(base + args.table_off);            // [G+1]
     int *const pref = offs + args.G + 1;                                         // [G+1]: tiles before run g
@@ -386,9 +386,10 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
     };
 
     // 384 threads start with 168 registers each.  The sums of a 256-column tile
-    // need more in warps 4-11: 4 * 32 * 72 + 8 * 32 * 216 = 384 * 168.
+    // need more in warps 4-11: 4 * 32 * 88 + 8 * 32 * 208 = 384 * 168
+    // (fewer in warps 0-3 spill their loops: 136 against 112 us at M4096 N8192 K4096).
     constexpr bool kMoveRegs = SUMS && TC == 256;
-    if (kMoveRegs && warp < kRoleWarps) ptx::regs_down<72>();
+    if (kMoveRegs && warp < kRoleWarps) ptx::regs_down<88>();
     if (warp == 0) {
         // ---- producer
         int g = 0, slot = 0;
@@ -599,35 +600,30 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
                 // lines: this warp makes them once, 16 bytes wide where rows
                 // allow it, for the eight that use them.
                 const int nbs = (args.lanes + kLanes - 1) / kLanes, nb = t.col0 / kLanes;
-                const float *const sb = args.sb + (static_cast<size_t>(t.g) * nbs + nb) * args.kblocks;
-                const float *const sb2 = sb + (nb + 1 < nbs ? args.kblocks : 0);
-                const bool wide = args.kblocks % 4 == 0;
+                const float *const sb = args.sb + (static_cast<size_t>(t.g) * nbs + nb) * args.kblocks + t.kb0;
+                const float *const sb2 = sb + (nb + 1 < nbs ? args.kblocks : 0);   // the second block of a pair's columns
+                const bool wide = args.kblocks % 4 == 0 && t.kb0 % 4 == 0 && t.nkb % 4 == 0;
                 const float *sa[4];
 #pragma unroll
                 for (int p = 0; p < 4; ++p)              // lanes without a token: any row
                     sa[p] = args.sa + static_cast<size_t>(t.rows > 0 ? t.lane0 + min(p * 32 + lane, t.rows - 1) : 0) *
-                                          args.kblocks;
-                float4 next[4], w, w2;
-                auto read4 = [&](const float *at, int b) {
-                    if (wide) return __ldg(reinterpret_cast<const float4 *>(at + b));
-                    const int last = t.nkb - 1;
-                    return make_float4(__ldg(at + b), __ldg(at + min(b + 1, last)), __ldg(at + min(b + 2, last)),
-                                       __ldg(at + min(b + 3, last)));
-                };
-                auto fetch = [&](int b) {
+                                          args.kblocks + t.kb0;
+                auto read4 = [&](const float *at, int b, float (&to)[4]) {
+                    if (wide) {
+                        const float4 x = __ldg(reinterpret_cast<const float4 *>(at + b));
+                        to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w;
+                    } else {
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) next[p] = read4(sa[p], b);
-                    w = read4(sb, b);
-                    w2 = read4(sb2, b);
+                        for (int j = 0; j < 4; ++j) to[j] = __ldg(at + min(b + j, t.nkb - 1));
+                    }
                 };
-                fetch(0);
                 for (int b = 0; b < t.nkb && !dead; b += 4) {
-                    float now[4][4], f[4], f2[4];
+                    // the ring holds eight k-blocks, more than these reads' latency
+                    float now[4][4], f[4], f2[4] = {};
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) now[p][0] = next[p].x, now[p][1] = next[p].y, now[p][2] = next[p].z, now[p][3] = next[p].w;
-                    f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
-                    f2[0] = w2.x, f2[1] = w2.y, f2[2] = w2.z, f2[3] = w2.w;
-                    if (b + 4 < t.nkb) fetch(b + 4);
+                    for (int p = 0; p < 4; ++p) read4(sa[p], b, now[p]);
+                    read4(sb, b, f);
+                    if (PAIR) read4(sb2, b, f2);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (b + j >= t.nkb || dead) break;
@@ -638,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
                             scale_buf[slot * Sh::kScaleSlot + p * 32 + lane] = now[p][j] * f[j];
-                            scale_buf[slot * Sh::kScaleSlot + kLanes + p * 32 + lane] = now[p][j] * f2[j];
+                            if (PAIR) scale_buf[slot * Sh::kScaleSlot + kLanes + p * 32 + lane] = now[p][j] * f2[j];
                         }
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(scale_full(slot));
@@ -741,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
         }
     } else {
         // ---- epilogue
-        if constexpr (kMoveRegs) ptx::regs_up<216>();
+        if constexpr (kMoveRegs) ptx::regs_up<208>();
         const int quarter = warp & 3, half = (warp - kRoleWarps) >> 2;
         const int c_lo = half * HALF;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(c_lo);
@@ -844,68 +840,67 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
                     return __uint_as_float(static_cast<uint32_t>(j & 1 ? acc[j / 2] >> 32 : acc[j / 2]));
                 };
                 const int cols = min(HALF, t.cols - c_lo);      // of the warp
-                const size_t at = static_cast<size_t>(t.lane0 + my) * pitch + t.col0 + c_lo;
                 if (dead || cols <= 0) {
-                } else if (args.out_type != 0 && args.lanes % 8 == 0) {
-                    // 32 columns at a time through shared memory, then 64 bytes
-                    // of eight rows to a store
+                } else if (S > 1) {
+#pragma unroll
+                    for (int j = 0; j < HALF; ++j) sum_buf[my * (TC + 1) + c_lo + j] = value(j);
+                } else {
+                    // 64 bytes of each row at a time through shared memory, so
+                    // that a store writes whole sectors
                     const uint32_t warp_at = ptx::smem_addr(base + args.stage_off) +
                                              static_cast<uint32_t>(warp - kRoleWarps) * Sh::kStageWarp;
                     const uint32_t mine = warp_at + static_cast<uint32_t>(lane) * Sh::kStageRow;
                     auto staged = [&](auto *to) {
                         using T = std::remove_pointer_t<decltype(to)>;
+                        constexpr int E = sizeof(T), V = 16 / E, PIECE = 64 / E;   // values of 16 and of 64 bytes
                         T *const out = to + static_cast<size_t>(t.lane0 + quarter * 32) * pitch + t.col0 + c_lo;
+                        const bool wide = static_cast<uint32_t>(args.lanes) % V == 0;   // rows start on 16 bytes
 #pragma unroll
-                        for (int c = 0; c < HALF; c += 32) {
+                        for (int c = 0; c < HALF; c += PIECE) {
                             __syncwarp();
 #pragma unroll
-                            for (int d = 0; d < 32; d += 8)
-                                ptx::st_shared_v4(mine + static_cast<uint32_t>(d) * 2u,
-                                                  pair16<T>(value(c + d), value(c + d + 1)),
-                                                  pair16<T>(value(c + d + 2), value(c + d + 3)),
-                                                  pair16<T>(value(c + d + 4), value(c + d + 5)),
-                                                  pair16<T>(value(c + d + 6), value(c + d + 7)));
+                            for (int d = 0; d < PIECE; d += V) {
+                                if constexpr (E == 4)
+                                    ptx::st_shared_v4(mine + d * E, __float_as_uint(value(c + d)),
+                                                      __float_as_uint(value(c + d + 1)), __float_as_uint(value(c + d + 2)),
+                                                      __float_as_uint(value(c + d + 3)));
+                                else
+                                    ptx::st_shared_v4(mine + d * E, pair16<T>(value(c + d), value(c + d + 1)),
+                                                      pair16<T>(value(c + d + 2), value(c + d + 3)),
+                                                      pair16<T>(value(c + d + 4), value(c + d + 5)),
+                                                      pair16<T>(value(c + d + 6), value(c + d + 7)));
+                            }
                             __syncwarp();
-                            const int col = c + (lane & 3) * 8;
-                            const bool in = col < cols;
+                            if (wide) {
+                                const int col = c + lane % 4 * V;
+                                const bool in = col < cols;
 #pragma unroll
-                            for (int r = 0; r < 32; r += 8) {
-                                const int row = r + (lane >> 2);
-                                const float4 x = ptx::ld_shared_v4(warp_at + static_cast<uint32_t>(row) * Sh::kStageRow +
-                                                                   static_cast<uint32_t>(lane & 3) * 16u);
-                                if (in && quarter * 32 + row < t.rows)
-                                    *reinterpret_cast<float4 *>(out + static_cast<size_t>(row) * pitch + col) = x;
+                                for (int r = 0; r < 32; r += 8) {
+                                    const int row = r + lane / 4;
+                                    const float4 x = ptx::ld_shared_v4(warp_at + static_cast<uint32_t>(row) * Sh::kStageRow +
+                                                                       static_cast<uint32_t>(lane % 4) * 16u);
+                                    if (in && quarter * 32 + row < t.rows)
+                                        *reinterpret_cast<float4 *>(out + static_cast<size_t>(row) * pitch + col) = x;
+                                }
+                            } else {
+                                constexpr int AT_ONCE = 32 / PIECE;              // rows of a store
+                                const int col = lane % PIECE, row0 = lane / PIECE;
+                                const T *const from = reinterpret_cast<const T *>(
+                                    base + args.stage_off + (warp - kRoleWarps) * Sh::kStageWarp) + col;
+                                const int live_rows = c + col < cols ? t.rows - quarter * 32 : 0;
+#pragma unroll 8
+                                for (int r = row0; r < 32; r += AT_ONCE)
+                                    if (r < live_rows)
+                                        out[static_cast<size_t>(r) * pitch + c + col] = from[r * (Sh::kStageRow / E)];
                             }
                         }
                     };
-                    if (args.out_type == 1)
+                    if (args.out_type == 0)
+                        staged(static_cast<float *>(args.out));
+                    else if (args.out_type == 1)
                         staged(static_cast<__half *>(args.out));
                     else
                         staged(static_cast<__nv_bfloat16 *>(args.out));
-                } else if (my < t.rows) {
-                    // F32, or rows whose 16-bit length is no multiple of 16 bytes
-                    auto direct = [&](auto *out) {
-                        using T = std::remove_pointer_t<decltype(out)>;
-                        if constexpr (sizeof(T) == 4) {
-                            if (args.lanes % 4 == 0) {
-#pragma unroll
-                                for (int c = 0; c < HALF; c += 4)
-                                    if (c < cols)
-                                        *reinterpret_cast<float4 *>(out + c) =
-                                            make_float4(value(c), value(c + 1), value(c + 2), value(c + 3));
-                                return;
-                            }
-                        }
-#pragma unroll
-                        for (int c = 0; c < HALF; ++c)
-                            if (c < cols) out[c] = rounded<T>(value(c));
-                    };
-                    if (args.out_type == 0)
-                        direct(static_cast<float *>(args.out) + at);
-                    else if (args.out_type == 1)
-                        direct(static_cast<__half *>(args.out) + at);
-                    else
-                        direct(static_cast<__nv_bfloat16 *>(args.out) + at);
                 }
             } else if constexpr (FP8) {
                 // F32 sums in fragments, two columns to a 64-bit register
@@ -1161,19 +1156,23 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
             if (S > 1) {
                 __syncwarp();
                 cluster_sync();                        // every rank's sums stand in its shared memory
-                // This block adds columns rank, rank + S, ... in rank order, 16
-                // reads of the blocks' memory in flight at a time.
+                // This block adds columns rank, rank + S, ... (ROWS: lanes), in
+                // rank order, 16 reads of the blocks' memory in flight at a time.
+                // A thread keeps to one place along the output's rows.
+                const int lines = ROWS ? t.rows : t.cols, line_pitch = ROWS ? TC + 1 : kLanes;
+                const bool on = ROWS ? my < t.cols : live;
+                const size_t to = ROWS ? static_cast<size_t>(t.lane0) * pitch + t.col0 + my : out0;
                 auto add_ranks = [&](auto splits) {
                     constexpr int R = decltype(splits)::value, AT_ONCE = 16 / R;
                     const uint32_t mine = ptx::smem_addr(sum_buf + my);
                     uint32_t at[R];
 #pragma unroll
                     for (int r = 0; r < R; ++r) at[r] = ptx::mapa(mine, r);
-                    for (int c0 = rank + R * half; c0 < t.cols; c0 += 2 * R * AT_ONCE) {
+                    for (int c0 = rank + R * half; c0 < lines; c0 += 2 * R * AT_ONCE) {
                         float x[AT_ONCE][R];
 #pragma unroll
                         for (int j = 0; j < AT_ONCE; ++j) {
-                            const uint32_t off = static_cast<uint32_t>(min(c0 + 2 * R * j, t.cols - 1) * kLanes) * 4u;
+                            const uint32_t off = static_cast<uint32_t>(min(c0 + 2 * R * j, lines - 1) * line_pitch) * 4u;
 #pragma unroll
                             for (int r = 0; r < R; ++r) x[j][r] = ptx::ld_cluster_f32(at[r] + off);
                         }
@@ -1183,8 +1182,8 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
 #pragma unroll
                             for (int r = 1; r < R; ++r) sum += x[j][r];
                             const int c = c0 + 2 * R * j;
-                            store_values<1>(args.out, args.out_type, out0 + static_cast<size_t>(c) * pitch, pitch,
-                                            live && c < t.cols, [&](int) { return sum; });
+                            store_values<1>(args.out, args.out_type, to + static_cast<size_t>(c) * pitch, pitch,
+                                            on && c < lines, [&](int) { return sum; });
                         }
                     }
                 };
@@ -1265,7 +1264,7 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
         ok = (FORM == kKn ? encode(&maps.lane, type, elem, 3, p.B, dk, bk)
                           : encode(&maps.lane, type, elem, 3, p.B, dn, bn)) &&
              encode(&maps.col, type, elem, 2, p.A, da, ba) &&
-             (FP8 && Sh::kPair ? encode(&maps.col_part, type, elem, 3, p.B, dn, bq)
+             (FP8 && TC >= 128 ? encode(&maps.col_part, type, elem, 3, p.B, dn, bq)
                                : encode(&maps.col_part, type, elem, 2, p.A, da, bp));
     }
     if (!ok) return cudaErrorInvalidValue;
@@ -1283,7 +1282,7 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
     a.out_type = p.out_type;
     a.bf16 = p.bf16;
     a.splits = splits;
-    const uint32_t sums = splits > 1 ? TC * kLanes * 4 : 0, scales = FP8 ? kScaleRing * Sh::kScaleSlot * 4 : 0,
+    const uint32_t sums = splits > 1 ? (TC + (FP8 && TC >= 128 ? 1 : 0)) * kLanes * 4 : 0, scales = FP8 ? kScaleRing * Sh::kScaleSlot * 4 : 0,
                    staging = FP8 ? kEpilogueWarps * Sh::kStageWarp : 0;
     const uint32_t tables = (static_cast<uint32_t>(2 * (p.G + 1)) * 4 + 127) / 128 * 128;
     const uint32_t rest = sums + scales + staging + tables;
@@ -1355,7 +1354,7 @@ GroupedPlan plan_grouped(const GroupedProblem &p, int sms)
         double us8, us16, join;
     };
     static constexpr Tiling kTilings[] = {   // 32: two blocks to an SM
-        {32, 0.38, 0.30, 1.5}, {64, 0.285, 0.26, 2.}, {128, 0.42, 0.26, 3.3}, {256, 0.54, 0.31, 0.}};
+        {32, 0.38, 0.30, 1.5}, {64, 0.285, 0.26, 2.}, {128, 0.33, 0.26, 2.5}, {256, 0.54, 0.31, 0.}};
     constexpr double kAlone = 0.7;           // of those figures, for a 32-column block alone on its SM
     const bool dw = p.form == GroupedForm::kDw, fp8 = p.form == GroupedForm::kFp8;
     const int64_t k = dw ? std::max<int64_t>(1, p.T / p.G) : p.K, kb = (k + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64);
