@@ -534,3 +534,19 @@ def test_beside_the_split_k_product(sk):
     torch.cuda.synchronize()
     assert torch.equal(e1, c1) and torch.equal(e2, c2)
     assert sk.splitk_get_device_status() == 0
+
+
+@pytest.mark.parametrize("tokens,experts", [(1, 8), (37, 16), (700, 4)])
+def test_example_block(sk, tokens, experts):
+    """The example against the same block in 32 bits.  E4M3 keeps four significant
+    bits: a value is off by at most 2^-4 of itself, 2^-4 / sqrt(3) on average, and
+    four such errors (activations and weights of two products; the gated product
+    passes its first factor's error on about twice) add to about 0.1."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_block.py")
+    spec = importlib.util.spec_from_file_location("moe_block", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.main(tokens, experts, hidden=1024, inner=512) < 0.1
