@@ -48,7 +48,7 @@
 #include <cmath>
 #include <type_traits>
 
-#include "ptx.cuh"
+#include "ptx_grouped.cuh"
 #include "splitk_internal.h"
 
 namespace splitk {
