@@ -618,7 +618,7 @@ const char *splitk_status_string(int status)
     switch (status) {
     case SPLITK_OK: return "ok";
     case SPLITK_ERR_NULL: return "a required pointer is NULL";
-    case SPLITK_ERR_SHAPE: return "M, K and k_per_split must be positive multiples of 32 and N of 64 (within limits)";
+    case SPLITK_ERR_SHAPE: return "a size breaks the call's rules (gemm_bt: M, K and k_per_split positive multiples of 32, N of 64) or limits";
     case SPLITK_ERR_SPLIT: return "splits must equal ceil(K / k_per_split): every split starts below K and they cover K";
     case SPLITK_ERR_ALIAS: return "an output range overlaps an input or another output";
     case SPLITK_ERR_ALIGN: return "pointers must be 16-byte aligned";

@@ -655,24 +655,17 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
                     const int c = min(p * 32 + lane, t.cols - 1);   // columns past the tile's repeat its last
                     sa[p] = args.sa + static_cast<size_t>(t.col0 + c) * args.kblocks + t.kb0;
                 }
-                float next[PER][BATCH];
-                auto fetch = [&](int b) {
+                for (int b = 0; b < t.nkb && !dead; b += BATCH) {
+                    // read together, multiplied when stored: the ring holds
+                    // eight k-blocks, more than these reads' latency
+                    float now[PER][BATCH], f[BATCH];
 #pragma unroll
                     for (int j = 0; j < BATCH; ++j) {
                         const int kb = min(b + j, t.nkb - 1);
-                        const float f = __ldg(sb + kb);
+                        f[j] = __ldg(sb + kb);
 #pragma unroll
-                        for (int p = 0; p < PER; ++p) next[p][j] = __ldg(sa[p] + kb) * f;
+                        for (int p = 0; p < PER; ++p) now[p][j] = __ldg(sa[p] + kb);
                     }
-                };
-                fetch(0);
-                for (int b = 0; b < t.nkb && !dead; b += BATCH) {
-                    float now[PER][BATCH];
-#pragma unroll
-                    for (int j = 0; j < BATCH; ++j)
-#pragma unroll
-                        for (int p = 0; p < PER; ++p) now[p][j] = next[p][j];
-                    if (b + BATCH < t.nkb) fetch(b + BATCH);
 #pragma unroll
                     for (int j = 0; j < BATCH; ++j) {
                         if (b + j >= t.nkb || dead) break;
@@ -684,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
                         for (int p = 0; p < PER; ++p) {
                             const int c = p * 32 + lane, in = c % HALF;
                             scale_buf[slot * Sh::kScaleSlot + (c / HALF * 4 + in % 8 / 2) * Sh::kScalePitch + in / 8 * 2 +
-                                      in % 2] = now[p][j];
+                                      in % 2] = now[p][j] * f[j];
                         }
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(scale_full(slot));
@@ -777,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
                 const int chunks = (min(HALF, max(0, t.width - c_lo)) + 15) / 16;
                 const float *const factors = scale_buf + c_lo / kLanes * kLanes + my;
 #pragma unroll 1
-                for (int i = 0; i < t.nkb; ++i) {
+                for (int i = 0; i < t.nkb && !dead; ++i) {
                     bool ok = ptx::mbar_try_wait(acc_full(buf), aph) & ptx::mbar_try_wait(scale_full(slot), ph);
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = bounded_wait(acc_full(buf), aph, &abort_s) && bounded_wait(scale_full(slot), ph, &abort_s);
