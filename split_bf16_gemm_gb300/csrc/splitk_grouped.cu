@@ -1348,7 +1348,7 @@ GroupedPlan plan_grouped(const GroupedProblem &p, int sms)
     };
     static constexpr Tiling kTilings[] = {   // 32: two blocks to an SM
         {32, 0.38, 0.30, 1.5}, {64, 0.285, 0.26, 2.}, {128, 0.33, 0.26, 2.5}, {256, 0.54, 0.31, 0.}};
-    constexpr double kAlone = 0.7;           // of those figures, for a 32-column block alone on its SM
+    constexpr double kAlone = 0.8;           // of those figures, for a 32-column block alone on its SM
     const bool dw = p.form == GroupedForm::kDw, fp8 = p.form == GroupedForm::kFp8;
     const int64_t k = dw ? std::max<int64_t>(1, p.T / p.G) : p.K, kb = (k + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64);
     GroupedPlan best = {128, 1};
@@ -1366,7 +1366,9 @@ GroupedPlan plan_grouped(const GroupedProblem &p, int sms)
             // a split of fewer than two k-blocks, or more blocks than places, never pays
             if (splits > 1 && (dw || t.tc == 256 || kb < 2 * splits || lane_tiles * col_tiles * splits > places)) break;
             const double waves = std::ceil(lane_tiles * col_tiles * splits / places);
-            const double rate = (fp8 ? t.us8 : t.us16) * (t.tc == 32 && lane_tiles * col_tiles * splits <= sms ? kAlone : 1.);
+            double rate = (fp8 ? t.us8 : t.us16) * (t.tc == 32 && lane_tiles * col_tiles * splits <= sms ? kAlone : 1.);
+            // a pair's 16-bit time goes by the rows it loads: 128 lanes and half the columns a block
+            if (t.tc == 256 && !fp8 && !dw) rate *= 0.65 + 0.35 * std::min(1., static_cast<double>(p.T) / (runs * t.tc));
             const double us = waves * (static_cast<double>((kb + splits - 1) / splits) * rate + (splits > 1 ? t.join : 0.));
             if (least == 0 || us < least) {
                 least = us;
