@@ -133,9 +133,17 @@ __device__ __forceinline__ bool mbar_try_wait_cluster_relaxed(uint32_t bar, uint
     return ok != 0;
 }
 
-__device__ __forceinline__ void fence_acquire_cluster()
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
 {
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // Arrivals on a barrier of any block of the cluster (a shared::cluster address).

@@ -126,12 +126,19 @@ struct Tile {
     int rows;                  // ROWS: live lanes of this block
 };
 
-// RELAXED: a barrier that guards tensor memory and that the other block of a
-// pair arrives on
-template <bool RELAXED = false>
+// kBlock: an arrival of this block or of its loads.  Of the other block of a
+// pair: kRelaxed, which guards tensor memory alone, and kAcquire, shared memory
+// that the other block wrote.
+enum Order { kBlock, kRelaxed, kAcquire };
+
+template <Order ORDER = kBlock>
 __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, volatile unsigned *abort)
 {
-    auto ready = [&] { return RELAXED ? ptx::mbar_try_wait_cluster_relaxed(bar, parity) : ptx::mbar_try_wait(bar, parity); };
+    auto ready = [&] {
+        return ORDER == kRelaxed   ? ptx::mbar_try_wait_cluster_relaxed(bar, parity)
+               : ORDER == kAcquire ? ptx::mbar_try_wait_cluster(bar, parity)
+                                   : ptx::mbar_try_wait(bar, parity);
+    };
     uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
         if (ready()) return true;
@@ -520,18 +527,17 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
                 if (DW) idesc |= 1u << 16;
                 for (int i = 0; i < t.nkb && !dead; ++i) {
                     const bool unit_start = i % UNIT == 0, unit_end = i % UNIT == UNIT - 1 || i == t.nkb - 1;
-                    if (unit_start && !bounded_wait<PAIR>(acc_empty(buf), aph ^ 1u, &abort_s)) dead = true;
-                    if (dead || !bounded_wait(full_bar(slot), ph, &abort_s)) {
+                    if (unit_start && !bounded_wait<PAIR ? kRelaxed : kBlock>(acc_empty(buf), aph ^ 1u, &abort_s)) dead = true;
+                    // a run's last k-block may hold rows that the other block zeroed
+                    if (dead || !(DW && PAIR && i == t.nkb - 1 ? bounded_wait<kAcquire>(full_bar(slot), ph, &abort_s)
+                                                               : bounded_wait(full_bar(slot), ph, &abort_s))) {
                         dead = true;
                         break;
                     }
                     int steps = 4;
                     if constexpr (DW) {
                         const int rem = t.tok_n - i * KB;
-                        if (rem < KB) {
-                            steps = (rem + 15) / 16;
-                            if (PAIR && rem % 16) ptx::fence_acquire_cluster();   // the other block's zeroed rows
-                        }
+                        if (rem < KB) steps = (rem + 15) / 16;
                     }
                     ptx::tc_fence_after_sync();
                     if (ptx::elect_one()) {
@@ -696,13 +702,12 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
                         dead = true;
                     } else {
                         ph ^= 1u << at;
-                        const int rows = 16 - rem % 16;
                         const int boxes = 2 + t.width / Sh::kBlocks / 64;   // [64 rows][128 bytes], lanes' then columns'
-                        const uint32_t sl = ring + at * Sh::kStage;
-                        for (int j = lane; j < boxes * rows * 8; j += 32) {
-                            const int box = j / (rows * 8), in = j - box * rows * 8;
-                            ptx::st_shared_v4(sl + box * 8192u + rem * 128u + in * 16u, 0u, 0u, 0u, 0u);
-                        }
+                        const int end = (rem + 15) / 16 * 16;               // of the MMA's step
+                        const uint32_t sl = ring + at * Sh::kStage + static_cast<uint32_t>(lane & 7) * 16u;
+                        for (int row = rem + (lane >> 3); row < end; row += 4)
+                            for (int box = 0; box < boxes; ++box)
+                                ptx::st_shared_v4(sl + box * 8192u + row * 128u, 0u, 0u, 0u, 0u);
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
