@@ -324,7 +324,8 @@ def splitk_selftest_kernel_timeout(A, B, out, M, N, K, splits, k_per_split, dtyp
 
 
 # The operators below are called once or more per layer with few microseconds
-# of device work, so their wrappers do no more than pass addresses on.
+# of device work, so their wrappers do no more than pass addresses on.  Tensors
+# are dense and row-major, as include/splitk.h says.
 
 def _here():
     """The current stream of the current device, as an integer."""
@@ -358,49 +359,55 @@ def rmsnorm_fp8(x, weight, q, scales, M, K, dtype, eps=1e-6, residual=None, sum_
     for each 128 values: q [M,K] (torch.float8_e4m3fn), scales [M, ceil(K/128)]
     F32; sum_out (x + residual; may be x or residual) and y (the norm in
     `dtype`) where given."""
-    _check((_lib or lib()).rmsnorm_fp8(_ptr(x), _ptr(residual), _ptr(weight), _ptr(sum_out), _ptr(y), _ptr(q), _ptr(scales),
-                             M, K, eps, _code(dtype), _on(stream)), "rmsnorm_fp8")
+    status = (_lib or lib()).rmsnorm_fp8(_ptr(x), _ptr(residual), _ptr(weight), _ptr(sum_out), _ptr(y), _ptr(q),
+                                         _ptr(scales), M, K, eps, _code(dtype), _on(stream))
+    _check(status, "rmsnorm_fp8")
 
 
 def fp8_quantize(x, q, scales, M, K, dtype, stream=None) -> None:
     """Activations x [M,K] to 8 bits: q [M,K], scales [M, ceil(K/128)] F32."""
-    _check((_lib or lib()).fp8_quantize(_ptr(x), _ptr(q), _ptr(scales), M, K, _code(dtype), _on(stream)),
-           "fp8_quantize")
+    status = (_lib or lib()).fp8_quantize(_ptr(x), _ptr(q), _ptr(scales), M, K, _code(dtype), _on(stream))
+    _check(status, "fp8_quantize")
 
 
 def fp8_prepare_bt(B, Bq, scales, G, N, K, dtype, stream=None) -> None:
     """Weights B [G,N,K] to 8 bits: Bq [G,N,K], scales [G, ceil(N/128), ceil(K/128)] F32."""
-    _check((_lib or lib()).fp8_prepare_bt(_ptr(B), _ptr(Bq), _ptr(scales), G, N, K, _code(dtype), _on(stream)),
-           "fp8_prepare_bt")
+    status = (_lib or lib()).fp8_prepare_bt(_ptr(B), _ptr(Bq), _ptr(scales), G, N, K, _code(dtype), _on(stream))
+    _check(status, "fp8_prepare_bt")
 
 
 def gemm_fp8_bt(A, a_scales, B, b_scales, out, M, N, K, out_dtype, stream=None) -> None:
     """out [M,N] = A B^T from 8-bit operands with their scales."""
-    _check((_lib or lib()).gemm_fp8_bt(_ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales), _ptr(out), M, N, K,
-                             _code(out_dtype), _on(stream)), "gemm_fp8_bt")
+    status = (_lib or lib()).gemm_fp8_bt(_ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales), _ptr(out), M, N, K,
+                                         _code(out_dtype), _on(stream))
+    _check(status, "gemm_fp8_bt")
 
 
 def gemm_grouped_fp8_bt(A, a_scales, B, b_scales, offsets, out, T, G, N, K, out_dtype, stream=None) -> None:
     """gemm_fp8_bt per run of rows: rows offsets[g]..offsets[g+1]-1 of A [T,K]
     meet B[g] ([G,N,K]); offsets: int32 [G+1] on the device."""
-    _check((_lib or lib()).gemm_grouped_fp8_bt(_ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales), _ptr(offsets), _ptr(out),
-                                     T, G, N, K, _code(out_dtype), _on(stream)), "gemm_grouped_fp8_bt")
+    status = (_lib or lib()).gemm_grouped_fp8_bt(_ptr(A), _ptr(a_scales), _ptr(B), _ptr(b_scales), _ptr(offsets),
+                                                 _ptr(out), T, G, N, K, _code(out_dtype), _on(stream))
+    _check(status, "gemm_grouped_fp8_bt")
 
 
 def gemm_grouped_bt(A, B, offsets, out, T, G, N, K, dtype, out_dtype, stream=None) -> None:
     """out [T,N]: rows offsets[g]..offsets[g+1]-1 of A [T,K] times B[g]^T (B [G,N,K]), 16-bit operands."""
-    _check((_lib or lib()).gemm_grouped_bt(_ptr(A), _ptr(B), _ptr(offsets), _ptr(out), T, G, N, K, _code(dtype),
-                                 _code(out_dtype), _on(stream)), "gemm_grouped_bt")
+    status = (_lib or lib()).gemm_grouped_bt(_ptr(A), _ptr(B), _ptr(offsets), _ptr(out), T, G, N, K, _code(dtype),
+                                             _code(out_dtype), _on(stream))
+    _check(status, "gemm_grouped_bt")
 
 
 def gemm_grouped_kn(A, W, offsets, out, T, G, N, K, dtype, out_dtype, stream=None) -> None:
     """gemm_grouped_bt with weights W [G,K,N]; with N and K exchanged, the
     gradient of gemm_grouped_bt's A."""
-    _check((_lib or lib()).gemm_grouped_kn(_ptr(A), _ptr(W), _ptr(offsets), _ptr(out), T, G, N, K, _code(dtype),
-                                 _code(out_dtype), _on(stream)), "gemm_grouped_kn")
+    status = (_lib or lib()).gemm_grouped_kn(_ptr(A), _ptr(W), _ptr(offsets), _ptr(out), T, G, N, K, _code(dtype),
+                                             _code(out_dtype), _on(stream))
+    _check(status, "gemm_grouped_kn")
 
 
 def gemm_grouped_dw(A, D, offsets, dB, T, G, N, K, dtype, out_dtype, stream=None) -> None:
     """The gradient of gemm_grouped_bt's B: dB[g] [N,K] = D_g^T A_g over the rows of run g."""
-    _check((_lib or lib()).gemm_grouped_dw(_ptr(A), _ptr(D), _ptr(offsets), _ptr(dB), T, G, N, K, _code(dtype),
-                                 _code(out_dtype), _on(stream)), "gemm_grouped_dw")
+    status = (_lib or lib()).gemm_grouped_dw(_ptr(A), _ptr(D), _ptr(offsets), _ptr(dB), T, G, N, K, _code(dtype),
+                                             _code(out_dtype), _on(stream))
+    _check(status, "gemm_grouped_dw")

@@ -245,8 +245,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_kernel(const RowsA
 // One block of 256 threads for each 128 x 128 block of a weight: thread t
 // takes 8 consecutive values of rows t / 16, t / 16 + 16, ...
 template <typename T>
-__global__ void __launch_bounds__(256) prepare_fp8_kernel(const T *__restrict__ B, uint8_t *__restrict__ q,
-                                                          float *__restrict__ scales, int N, int K, int n_blocks,
+__global__ void __launch_bounds__(256) prepare_fp8_kernel(const T *B, uint8_t *q, float *scales, int N, int K, int n_blocks,
                                                           int k_blocks)
 {
     __shared__ float part[8];

@@ -301,6 +301,8 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
     const uint32_t tmem = tmem_slot;
     // the next launch's blocks may set up now (every block here holds its
     // tensor memory); they wait for this grid before they read anything
+    // (with plain loads: what the grid before wrote is not constant while this
+    // one runs)
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
 
@@ -616,11 +618,11 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
                                           args.kblocks + t.kb0;
                 auto read4 = [&](const float *at, int b, float (&to)[4]) {
                     if (wide) {
-                        const float4 x = __ldg(reinterpret_cast<const float4 *>(at + b));
+                        const float4 x = *reinterpret_cast<const float4 *>(at + b);
                         to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w;
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) to[j] = __ldg(at + min(b + j, t.nkb - 1));
+                        for (int j = 0; j < 4; ++j) to[j] = at[min(b + j, t.nkb - 1)];
                     }
                 };
                 for (int b = 0; b < t.nkb && !dead; b += 4) {
@@ -668,9 +670,9 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
 #pragma unroll
                     for (int j = 0; j < BATCH; ++j) {
                         const int kb = min(b + j, t.nkb - 1);
-                        f[j] = __ldg(sb + kb);
+                        f[j] = sb[kb];
 #pragma unroll
-                        for (int p = 0; p < PER; ++p) now[p][j] = __ldg(sa[p] + kb);
+                        for (int p = 0; p < PER; ++p) now[p][j] = sa[p][kb];
                     }
 #pragma unroll
                     for (int j = 0; j < BATCH; ++j) {
