@@ -154,6 +154,13 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
     }
 }
 
+// The same for a whole warp: every lane goes one way.
+template <Order ORDER = kBlock>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile unsigned *abort)
+{
+    return __all_sync(0xffffffffu, bounded_wait<ORDER>(bar, parity, abort)) != 0;
+}
+
 template <typename T>
 __device__ __forceinline__ T rounded(float v);
 template <>
@@ -209,7 +216,8 @@ __device__ __forceinline__ void store_values(void *out, int type, size_t at, siz
 }
 
 template <int FORM, int TC, bool SUMS>
-__global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(const __grid_constant__ Maps maps, const GroupedArgs args)
+__global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm)
+    grouped_kernel(const __grid_constant__ Maps maps, const GroupedArgs args)
 {
     static_assert(SUMS || FORM != kFp8, "8-bit operands need the F32 sums in registers");
     using Sh = Shape<TC>;
@@ -231,7 +239,8 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
     const uint32_t raw = ptx::smem_addr(dsmem);
     const uint32_t ring = (raw + 1023u) & ~1023u;
     uint8_t *const base = dsmem + (ring - raw);
-    float *const sum_buf = reinterpret_cast<float *>(base + args.sum_off);       // [TC][128] (ROWS: [128][TC + 1]), splits > 1
+    // splits > 1: [TC][128], ROWS [128][TC + 1]
+    float *const sum_buf = reinterpret_cast<float *>(base + args.sum_off);
     float *const scale_buf = reinterpret_cast<float *>(base + args.scale_off);   // [kScaleRing][kScaleSlot]
     int *const offs = reinterpret_cast<int *>(base + args.table_off);            // [G+1]
     int *const pref = offs + args.G + 1;                                         // [G+1]: tiles before run g
@@ -432,54 +441,54 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
                         ptx::tma_load_3d(dst, map, bar, x, y, t.g, once);
                 };
                 for (int i = 0; i < t.nkb; ++i) {
-                    if (!bounded_wait(empty_bar(slot), ph ^ 1u, &abort_s)) {
+                    if (!warp_wait(empty_bar(slot), ph ^ 1u, &abort_s)) {
                         dead = true;
                         break;
                     }
                     // one lane issues; the whole warp walks the loop, so that
                     // slots and coordinates stay in uniform registers
                     if (ptx::elect_one()) {
-                    const uint32_t sl = ring + slot * Sh::kStage, sc = sl + kLaneBytes;
-                    const int kx = (t.kb0 + i) * KB;
-                    uint32_t bar = full0 + 8u * slot;
-                    const bool tail = DW && t.tok_n - kx < KB && (t.tok_n - kx) % 16 != 0;
-                    if (tail) {                              // to this block's warp 2 first
-                        bar = tail_bar(slot);
-                        ptx::mbar_arrive_expect_tx(bar, bytes);
-                        if constexpr (PAIR) bar = ptx::mapa(bar, peer);
-                    } else if (peer == 0) {
-                        ptx::mbar_arrive_expect_tx(full_bar(slot), bytes * Sh::kBlocks);
-                        if (DW && PAIR) ptx::mbar_arrive(full_bar(slot));
-                    }
-                    if constexpr (DW) {
-                        const int y = t.tok0 + kx;
-                        load2(sl, &maps.lane, bar, t.lane0, y, once);
-                        load2(sl + 8192u, &maps.lane, bar, t.lane0 + 64, y, once);
-                        for (int j = 0; j < parts; ++j)
-                            load2(sc + j * 8192u, &maps.col, bar, col + 64 * j, y, once);
-                    } else {
-                        if constexpr (LMN) {
-                            load3(sl, bar, t.lane0, kx, &maps.lane);
-                            load3(sl + 8192u, bar, t.lane0 + 64, kx, &maps.lane);
-                        } else if constexpr (ROWS) {
-                            load2(sl, &maps.col, bar, kx, t.lane0, again);
-                        } else {
-                            load3(sl, bar, kx, t.lane0, &maps.lane);
+                        const uint32_t sl = ring + slot * Sh::kStage, sc = sl + kLaneBytes;
+                        const int kx = (t.kb0 + i) * KB;
+                        uint32_t bar = full0 + 8u * slot;
+                        const bool tail = DW && t.tok_n - kx < KB && (t.tok_n - kx) % 16 != 0;
+                        if (tail) {                              // to this block's warp 2 first
+                            bar = tail_bar(slot);
+                            ptx::mbar_arrive_expect_tx(bar, bytes);
+                            if constexpr (PAIR) bar = ptx::mapa(bar, peer);
+                        } else if (peer == 0) {
+                            ptx::mbar_arrive_expect_tx(full_bar(slot), bytes * Sh::kBlocks);
+                            if (DW && PAIR) ptx::mbar_arrive(full_bar(slot));
                         }
-                        if constexpr (ROWS) {
-                            if (whole)
-                                load3(sc, bar, kx, col, &maps.lane);
-                            else
-                                for (int j = 0; j < parts; ++j)
-                                    load3(sc + j * kPart * 128u, bar, kx, col + j * kPart, &maps.col_part);
-                        } else if (whole) {
-                            load2(sc, &maps.col, bar, kx, col, again);
-                        } else {
+                        if constexpr (DW) {
+                            const int y = t.tok0 + kx;
+                            load2(sl, &maps.lane, bar, t.lane0, y, once);
+                            load2(sl + 8192u, &maps.lane, bar, t.lane0 + 64, y, once);
                             for (int j = 0; j < parts; ++j)
-                                load2(sc + j * kPart * 128u, &maps.col_part, bar, kx, col + j * kPart,
-                                      again);
+                                load2(sc + j * 8192u, &maps.col, bar, col + 64 * j, y, once);
+                        } else {
+                            if constexpr (LMN) {
+                                load3(sl, bar, t.lane0, kx, &maps.lane);
+                                load3(sl + 8192u, bar, t.lane0 + 64, kx, &maps.lane);
+                            } else if constexpr (ROWS) {
+                                load2(sl, &maps.col, bar, kx, t.lane0, again);
+                            } else {
+                                load3(sl, bar, kx, t.lane0, &maps.lane);
+                            }
+                            if constexpr (ROWS) {
+                                if (whole)
+                                    load3(sc, bar, kx, col, &maps.lane);
+                                else
+                                    for (int j = 0; j < parts; ++j)
+                                        load3(sc + j * kPart * 128u, bar, kx, col + j * kPart, &maps.col_part);
+                            } else if (whole) {
+                                load2(sc, &maps.col, bar, kx, col, again);
+                            } else {
+                                for (int j = 0; j < parts; ++j)
+                                    load2(sc + j * kPart * 128u, &maps.col_part, bar, kx, col + j * kPart,
+                                          again);
+                            }
                         }
-                    }
                     }
                     __syncwarp();
                     ++issued;
@@ -493,6 +502,13 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
                 __syncwarp();
                 cluster_sync();
                 cluster_sync();
+            }
+        }
+        if (PAIR && peer == 1 && dead) {
+            // after a time-out nothing here counts this block's loads in
+            // flight: long enough for them to land
+            const uint64_t t0 = ptx::globaltimer_ns();
+            while (ptx::globaltimer_ns() - t0 < 100000) {
             }
         }
         if (peer == 0) {
@@ -527,12 +543,15 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
                 if (!FP8 && args.bf16) idesc |= (1u << 7) | (1u << 10);
                 if (LMN) idesc |= 1u << 15;
                 if (DW) idesc |= 1u << 16;
-                for (int i = 0; i < t.nkb && !dead; ++i) {
+                for (int i = 0; i < t.nkb; ++i) {
                     const bool unit_start = i % UNIT == 0, unit_end = i % UNIT == UNIT - 1 || i == t.nkb - 1;
-                    if (unit_start && !bounded_wait<PAIR ? kRelaxed : kBlock>(acc_empty(buf), aph ^ 1u, &abort_s)) dead = true;
+                    if (unit_start && !warp_wait<PAIR ? kRelaxed : kBlock>(acc_empty(buf), aph ^ 1u, &abort_s)) {
+                        dead = true;
+                        break;
+                    }
                     // a run's last k-block may hold rows that the other block zeroed
-                    if (dead || !(DW && PAIR && i == t.nkb - 1 ? bounded_wait<kAcquire>(full_bar(slot), ph, &abort_s)
-                                                               : bounded_wait(full_bar(slot), ph, &abort_s))) {
+                    if (!(DW && PAIR && i == t.nkb - 1 ? warp_wait<kAcquire>(full_bar(slot), ph, &abort_s)
+                                                       : warp_wait(full_bar(slot), ph, &abort_s))) {
                         dead = true;
                         break;
                     }
@@ -543,31 +562,31 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
                     }
                     ptx::tc_fence_after_sync();
                     if (ptx::elect_one()) {
-                    const uint32_t at = static_cast<uint32_t>(slot) * (Sh::kStage >> 4);
-                    const uint32_t d = tmem + static_cast<uint32_t>(buf * TC);
+                        const uint32_t at = static_cast<uint32_t>(slot) * (Sh::kStage >> 4);
+                        const uint32_t d = tmem + static_cast<uint32_t>(buf * TC);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (DW && k >= steps) break;
-                        const uint32_t accumulate = unit_start && k == 0 ? 0u : 1u;
-                        const uint64_t a = ptx::desc64(a_lo + at + (LMN ? 128u : 2u) * k, a_hi);
-                        const uint64_t b = ptx::desc64(b_lo + at + (DW ? 128u : 2u) * k, b_hi);
+                        for (int k = 0; k < 4; ++k) {
+                            if (DW && k >= steps) break;
+                            const uint32_t accumulate = unit_start && k == 0 ? 0u : 1u;
+                            const uint64_t a = ptx::desc64(a_lo + at + (LMN ? 128u : 2u) * k, a_hi);
+                            const uint64_t b = ptx::desc64(b_lo + at + (DW ? 128u : 2u) * k, b_hi);
+                            if constexpr (PAIR)
+                                ptx::mma_pair<FP8>(d, a, b, idesc, accumulate);
+                            else if constexpr (FP8)
+                                ptx::mma_f8(d, a, b, idesc, accumulate);
+                            else
+                                ptx::mma_f16(d, a, b, idesc, accumulate);
+                        }
                         if constexpr (PAIR)
-                            ptx::mma_pair<FP8>(d, a, b, idesc, accumulate);
-                        else if constexpr (FP8)
-                            ptx::mma_f8(d, a, b, idesc, accumulate);
+                            ptx::mma_commit_pair(empty_bar(slot));
                         else
-                            ptx::mma_f16(d, a, b, idesc, accumulate);
-                    }
-                    if constexpr (PAIR)
-                        ptx::mma_commit_pair(empty_bar(slot));
-                    else
-                        ptx::mma_commit(empty_bar(slot));
-                    if (unit_end) {
-                        if constexpr (PAIR)
-                            ptx::mma_commit_pair(acc_full(buf));
-                        else
-                            ptx::mma_commit(acc_full(buf));
-                    }
+                            ptx::mma_commit(empty_bar(slot));
+                        if (unit_end) {
+                            if constexpr (PAIR)
+                                ptx::mma_commit_pair(acc_full(buf));
+                            else
+                                ptx::mma_commit(acc_full(buf));
+                        }
                     }
                     __syncwarp();
                     if (unit_end && ++buf == Sh::kAcc) {
@@ -586,11 +605,14 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
                 cluster_sync();
             }
         }
-        if (lane == 0 && peer == 0) {
-            if constexpr (PAIR)
-                ptx::mma_commit_pair(drain_bar);
-            else
-                ptx::mma_commit(drain_bar);
+        if (peer == 0) {
+            // the lane that issued: a commit is for its own operations
+            if (ptx::elect_one()) {
+                if constexpr (PAIR)
+                    ptx::mma_commit_pair(drain_bar);
+                else
+                    ptx::mma_commit(drain_bar);
+            }
             ptx::mbar_wait_bounded(drain_bar, 0, kWaitLimitNs);
         }
         __syncwarp();
@@ -635,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (b + j >= t.nkb || dead) break;
-                        if (!__all_sync(0xffffffffu, bounded_wait(scale_empty(slot), ph ^ 1u, &abort_s))) {
+                        if (!warp_wait(scale_empty(slot), ph ^ 1u, &abort_s)) {
                             dead = true;
                             break;
                         }
@@ -677,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
 #pragma unroll
                     for (int j = 0; j < BATCH; ++j) {
                         if (b + j >= t.nkb || dead) break;
-                        if (!__all_sync(0xffffffffu, bounded_wait(scale_empty(slot), ph ^ 1u, &abort_s))) {
+                        if (!warp_wait(scale_empty(slot), ph ^ 1u, &abort_s)) {
                             dead = true;
                             break;
                         }
@@ -700,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
                 const int rem = t.tok_n - (t.nkb - 1) * KB;
                 if (t.nkb > 0 && rem % 16 && !dead) {
                     const int at = (slot + t.nkb - 1) % stages;
-                    if (!__all_sync(0xffffffffu, bounded_wait(tail_bar(at), (ph >> at) & 1u, &abort_s))) {
+                    if (!warp_wait(tail_bar(at), (ph >> at) & 1u, &abort_s)) {
                         dead = true;
                     } else {
                         ph ^= 1u << at;
@@ -1124,7 +1146,7 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm) grouped_kernel(co
                 }
             } else {
                 const bool any = t.nkb > 0;             // kDw: a run without rows has zero gradients
-                if (any && !dead && !__all_sync(0xffffffffu, bounded_wait(acc_full(buf), aph, &abort_s))) dead = true;
+                if (any && !dead && !warp_wait(acc_full(buf), aph, &abort_s)) dead = true;
                 if (!dead) {
                     ptx::tc_fence_after_sync();
 #pragma unroll 1
