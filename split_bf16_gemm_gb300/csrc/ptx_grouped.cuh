@@ -228,6 +228,12 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar)
         : "memory");
 }
 
+// The same, on this block's barrier only.
+__device__ __forceinline__ void mma_commit_own(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // Moves registers between the warpgroups of a block (every warp of the
 // warpgroup calls it).
 template <int N>

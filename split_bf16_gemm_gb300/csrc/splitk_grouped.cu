@@ -105,7 +105,7 @@ struct GroupedArgs {
     void *out;
     int T, G;
     int lanes, cols;           // extent of the lanes; of the columns for kDw (else the run's length)
-    int K, kblocks;            // contracted extent and its k-blocks (not kDw)
+    int kblocks;               // of the contracted extent (not kDw)
     int out_type;              // splitk_dtype
     int bf16;
     int splits;                // cluster size along K
@@ -118,7 +118,7 @@ struct Maps {
 };
 
 struct Tile {
-    int g, row0;               // first output row
+    int g;
     int lane0, cols, width;    // first lane; live columns, and rounded up to the MMA's N
     int col0;                  // first column: a token, or a column of D
     int kb0, nkb;              // this block's k-blocks
@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm)
             // the lane that issued: a commit is for its own operations
             if (ptx::elect_one()) {
                 if constexpr (PAIR)
-                    ptx::mma_commit_pair(drain_bar);
+                    ptx::mma_commit_own(drain_bar);   // the other block may be leaving
                 else
                     ptx::mma_commit(drain_bar);
             }
@@ -1299,7 +1299,6 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
     a.G = static_cast<int>(p.G);
     a.lanes = static_cast<int>(DW ? p.K : p.N);
     a.cols = static_cast<int>(p.N);
-    a.K = static_cast<int>(p.K);
     a.kblocks = static_cast<int>((p.K + KB - 1) / KB);
     a.out_type = p.out_type;
     a.bf16 = p.bf16;
