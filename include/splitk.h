@@ -378,8 +378,7 @@ int splitk_autotune_splits(const void *A, const void *B, float *out,
  *   h = x + residual, rounded to `dtype` (h = x without a residual)
  *   y = h * weight / sqrt(mean_k h^2 + eps), in F32
  *   scales[m,b] = max(max_{k in b} |y[m,k]| / 448, 2^-126)
- *   q[m,k]      = y[m,k] / scales[m,b] to E4M3, to nearest even (the quotient
- *                 by the scale before its rounding to F32)
+ *   q[m,k]      = y[m,k] / scales[m,b] to E4M3, to nearest even
  *   x, residual  device, [M,K] of `dtype` (SPLITK_F32, _F16, _BF16); residual
  *                may be NULL
  *   weight       device, [K] of `dtype`
@@ -387,9 +386,8 @@ int splitk_autotune_splits(const void *A, const void *B, float *out,
  *                x or residual (in place)
  *   y            device, [M,K] of `dtype` or NULL: receives y, rounded once
  *   q, scales    device, as above
- * A row that holds a NaN gets NaN scales and codes; one that holds an infinity
- * NaN in the infinity's block and zeros elsewhere (its mean is infinite).
- * eps >= 0 (else SPLITK_ERR_CONFIG). */
+ * A row that holds a NaN or an infinity gets NaN scales and codes.  eps >= 0
+ * (else SPLITK_ERR_CONFIG). */
 int rmsnorm_fp8(const void *x, const void *residual, const void *weight,
                 void *sum, void *y, void *q, float *scales, int64_t M,
                 int64_t K, float eps, int dtype, void *stream);

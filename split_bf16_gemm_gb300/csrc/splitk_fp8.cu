@@ -4,11 +4,10 @@
 // Rows: h = x + residual, rounded once to the inputs' type (the `sum` that the
 // next layer adds to; the norm is of what is kept); y = h w / sqrt(mean h^2 +
 // eps) in F32; each 128 consecutive y share the scale s = max(max|y| / 448,
-// 2^-126), and q = E4M3(y / s), to nearest even (y / s for s before its own
-// rounding).  448 is E4M3's largest value; the floor keeps y / s defined for a
-// block of zeros and s out of the subnormals.  A NaN or an infinity in a block
-// gives it a NaN or infinite scale and NaN products, never finite ones (the
-// norm of a row with an infinity: zeros in its other blocks).
+// 2^-126), and q = E4M3(y / s), to nearest even.  448 is E4M3's largest value;
+// the floor keeps y / s defined for a block of zeros and s out of the
+// subnormals.  A NaN or an infinity in a block gives it a NaN or infinite
+// scale and NaN products, never finite ones.
 //
 // A row is read once: its values stay in registers (8 to a 16-byte load of
 // 16-bit inputs) between the sum of squares and the output.  Rows longer than
@@ -29,7 +28,6 @@ namespace {
 
 constexpr float kE4m3Max = 448.f;
 constexpr float kScaleFloor = 1.17549435082228751e-38f;   // 2^-126
-constexpr float kNoOverflow = 1e35f;                       // times 448 stays finite
 constexpr int kVec = 8;                                    // values a thread takes at once
 constexpr int kBlockVecs = 128 / kVec;                     // threads that share a scale
 
@@ -221,7 +219,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_kernel(const RowsA
                 float w[kVec];
                 unpack(*reinterpret_cast<const Pack<T> *>(weight + static_cast<size_t>(v) * kVec), w);
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) h[i][j] *= w[j];
+                for (int j = 0; j < kVec; ++j) h[i][j] = h[i][j] * rstd * w[j];
             }
             float m = 0.f;
 #pragma unroll
@@ -229,23 +227,14 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_kernel(const RowsA
             // the 16 threads of a scale are consecutive lanes of one warp
 #pragma unroll
             for (int d = kBlockVecs / 2; d; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-            const float unfloored = m * rstd / kE4m3Max, s = max_nan(unfloored, kScaleFloor);
+            const float s = max_nan(m / kE4m3Max, kScaleFloor);
             if (in) {
                 if (a.y) {
-                    float y[kVec];
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j) y[j] = h[i][j] * rstd;
                     Pack<T> p;
-                    pack(y, p);
+                    pack(h[i], p);
                     *reinterpret_cast<Pack<T> *>(static_cast<T *>(a.y) + at + static_cast<size_t>(v) * kVec) = p;
                 }
-                // y / s is h w 448 / max|h w|, in which 1 / sqrt(mean h^2 + eps)
-                // has gone: products of 16-bit values are exact in F32, so
-                // their codes are off by one rounding of the quotient
-                const bool exact = unfloored > kScaleFloor && m < kNoOverflow;
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) h[i][j] *= exact ? kE4m3Max : rstd;
-                divide(h[i], exact ? m : s);
+                divide(h[i], s);
                 *reinterpret_cast<uint2 *>(a.q + at + static_cast<size_t>(v) * kVec) = to_e4m3(h[i]);
                 if (v % kBlockVecs == 0) a.scales[static_cast<size_t>(row) * a.blocks + v / kBlockVecs] = s;
             }
