@@ -26,7 +26,7 @@
 namespace splitk {
 namespace {
 
-constexpr float kE4m3Max = 448.f;
+constexpr float kE4m3Max = 448.f;                          // its reciprocal times 448 2^n is 2^n exactly
 constexpr float kScaleFloor = 1.17549435082228751e-38f;   // 2^-126
 constexpr int kVec = 8;                                    // values a thread takes at once
 constexpr int kBlockVecs = 128 / kVec;                     // threads that share a scale
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_kernel(const RowsA
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) sq += part[in_block * kWarps + i];
         }
-        rstd = 1.f / sqrtf(sq / static_cast<float>(a.K) + a.eps);
+        rstd = rsqrtf(sq / static_cast<float>(a.K) + a.eps);
     }
     for (int turn = 0; turn < turns; ++turn) {
         if (LONG) load(turn, true);
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_kernel(const RowsA
             // the 16 threads of a scale are consecutive lanes of one warp
 #pragma unroll
             for (int d = kBlockVecs / 2; d; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-            const float s = max_nan(m / kE4m3Max, kScaleFloor);
+            const float s = max_nan(m * (1.f / kE4m3Max), kScaleFloor);
             if (in) {
                 if (a.y) {
                     Pack<T> p;
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(256) prepare_fp8_kernel(const T *B, uint8_t *q
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max_nan(m, part[i]);
-    const float s = max_nan(m / kE4m3Max, kScaleFloor);
+    const float s = max_nan(m * (1.f / kE4m3Max), kScaleFloor);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int r = r0 + 16 * i;
