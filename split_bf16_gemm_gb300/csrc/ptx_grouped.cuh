@@ -112,6 +112,34 @@ __device__ __forceinline__ uint64_t pack_b32x2(uint32_t lo, uint32_t hi)
     return d;
 }
 
+// Stores a box of shared memory (128-byte swizzled, 1024-byte aligned) to a
+// tensor map's matrix, in the thread's open group; what lies past the matrix's
+// end is left out.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int32_t x, int32_t y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(x), "r"(y)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bulk_commit()
+{
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// The thread's groups have read their shared memory.
+__device__ __forceinline__ void bulk_wait_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
+// The thread's groups are done.
+__device__ __forceinline__ void bulk_wait()
+{
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // ------------------------------------------------- pairs of thread blocks
 // (cta_group::2: the two blocks of a cluster of 2 multiply one tile; the block
 // of even rank issues)

@@ -94,9 +94,10 @@ struct Shape {
     static constexpr int kScaleSlot = TC >= 128 ? TC : 2 * 4 * kScalePitch;   // ROWS: lanes by weight blocks
     static constexpr int kFragCols = kHalf < 32 ? kHalf : 32;     // columns of one tensor-memory load
     // staged rows of 64 bytes, padded by 16: 32 lanes of a column in 16 bits,
-    // or (ROWS) a piece of a lane's columns
+    // or (ROWS) a piece of a lane's columns; ROWS with 16-bit outputs: boxes of
+    // 32 lanes by 64 columns, as a TMA store takes them
     static constexpr uint32_t kStageRow = 80;
-    static constexpr uint32_t kStageWarp = kFragCols * kStageRow;
+    static constexpr uint32_t kStageWarp = TC >= 128 ? kHalf / 64 * 4096 : kFragCols * kStageRow;
 };
 
 struct GroupedArgs {
@@ -110,11 +111,13 @@ struct GroupedArgs {
     int bf16;
     int splits;                // cluster size along K
     int stages;
+    int store_boxes;           // ROWS: 16-bit rows that start on 16 bytes
     uint32_t sum_off, scale_off, stage_off, table_off;   // byte offsets in shared memory after the stage ring
 };
 
 struct Maps {
     CUtensorMap lane, col, col_part;   // col_part: a quarter of col's rows
+    CUtensorMap out;                   // ROWS, with store_boxes
 };
 
 struct Tile {
@@ -877,6 +880,36 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm)
                         constexpr int E = sizeof(T), V = 16 / E, PIECE = 64 / E;   // values of 16 and of 64 bytes
                         T *const out = to + static_cast<size_t>(t.lane0 + quarter * 32) * pitch + t.col0 + c_lo;
                         const bool wide = static_cast<uint32_t>(args.lanes) % V == 0;   // rows start on 16 bytes
+                        // the last tile's boxes have been read
+                        if (lane == 0) ptx::bulk_wait_read();
+                        __syncwarp();
+                        if constexpr (E == 2) {
+                            if (args.store_boxes && quarter * 32 + 32 <= t.rows) {
+                                // every row is the run's: whole boxes, which the
+                                // TMA unit writes beside the next tile's sums
+                                // (M4096 N8192 K4096: 109 us, stores by the
+                                // warps 115; 16 runs of 8192 rows 79 and 85)
+#pragma unroll
+                                for (int c = 0; c < HALF; c += 8)
+                                    ptx::st_shared_v4(warp_at + static_cast<uint32_t>(c / 64) * 4096u +
+                                                          static_cast<uint32_t>(lane) * 128u +
+                                                          static_cast<uint32_t>((c / 8 % 8) ^ (lane & 7)) * 16u,
+                                                      pair16<T>(value(c), value(c + 1)), pair16<T>(value(c + 2), value(c + 3)),
+                                                      pair16<T>(value(c + 4), value(c + 5)),
+                                                      pair16<T>(value(c + 6), value(c + 7)));
+                                ptx::fence_proxy_async_smem();
+                                __syncwarp();
+                                if (lane == 0) {
+#pragma unroll
+                                    for (int c = 0; c < HALF; c += 64)
+                                        if (c < cols)
+                                            ptx::tma_store_2d(&maps.out, warp_at + static_cast<uint32_t>(c / 64) * 4096u,
+                                                              t.col0 + c_lo + c, t.lane0 + quarter * 32);
+                                    ptx::bulk_commit();
+                                }
+                                return;
+                            }
+                        }
 #pragma unroll
                         for (int c = 0; c < HALF; c += PIECE) {
                             __syncwarp();
@@ -1219,6 +1252,7 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm)
             }
         }
     }
+    if (ROWS && warp >= kRoleWarps && lane == 0) ptx::bulk_wait();   // the outputs are written when the grid ends
     ptx::tc_fence_before_sync();
     __syncthreads();
     if constexpr (PAIR) cluster_sync();   // neither block's memory is in use by the other any more
@@ -1289,8 +1323,16 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
              (FP8 && TC >= 128 ? encode(&maps.col_part, type, elem, 3, p.B, dn, bq)
                                : encode(&maps.col_part, type, elem, 2, p.A, da, bp));
     }
+    const bool boxes = FP8 && TC >= 128 && p.out_type != 0 && p.N % 8 == 0;
+    if (ok && boxes) {
+        const uint64_t dims[2] = {N, T};
+        const uint32_t box[2] = {64, 32};
+        ok = encode(&maps.out, p.out_type == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 2,
+                    p.out, dims, box);
+    }
     if (!ok) return cudaErrorInvalidValue;
     GroupedArgs a = {};
+    a.store_boxes = boxes;
     a.offsets = p.offsets;
     a.sa = p.sa;
     a.sb = p.sb;
@@ -1303,7 +1345,7 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
     a.out_type = p.out_type;
     a.bf16 = p.bf16;
     a.splits = splits;
-    const uint32_t sums = splits > 1 ? (TC + (FP8 && TC >= 128 ? 1 : 0)) * kLanes * 4 : 0, scales = FP8 ? kScaleRing * Sh::kScaleSlot * 4 : 0,
+    const uint32_t sums = splits > 1 ? ((TC + (FP8 && TC >= 128 ? 1 : 0)) * kLanes * 4 + 1023) / 1024 * 1024 : 0, scales = FP8 ? kScaleRing * Sh::kScaleSlot * 4 : 0,
                    staging = FP8 ? kEpilogueWarps * Sh::kStageWarp : 0;
     const uint32_t tables = (static_cast<uint32_t>(2 * (p.G + 1)) * 4 + 127) / 128 * 128;
     const uint32_t rest = sums + scales + staging + tables;
