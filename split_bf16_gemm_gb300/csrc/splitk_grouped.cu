@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm)
 
     // 384 threads start with 168 registers each.  The sums of a 256-column tile
     // need more in warps 4-11: 4 * 32 * 88 + 8 * 32 * 208 = 384 * 168
-    // (fewer in warps 0-3 spill their loops: 136 against 112 us at M4096 N8192 K4096).
+    // (fewer in warps 0-3 spill their loops: 136 against 112 us then, at M4096 N8192 K4096).
     constexpr bool kMoveRegs = SUMS && TC == 256;
     if (kMoveRegs && warp < kRoleWarps) ptx::regs_down<88>();
     if (warp == 0) {
