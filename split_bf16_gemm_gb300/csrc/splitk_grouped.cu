@@ -507,6 +507,20 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm)
                 cluster_sync();
             }
         }
+        if constexpr (PAIR) {
+            // The issuing block's commits arrive on both blocks' empty barriers,
+            // also for the stages that are not filled again: each block waits
+            // for those too, as no arrival may reach a block that has left.
+            int s = slot;
+            uint32_t p = ph;
+            for (int i = 0; i < stages && !dead; ++i) {   // (a stage never filled is free at once)
+                if (!warp_wait(empty_bar(s), p ^ 1u, &abort_s)) dead = true;
+                if (++s == stages) {
+                    s = 0;
+                    p ^= 1u;
+                }
+            }
+        }
         if (PAIR && peer == 1 && dead) {
             // after a time-out nothing here counts this block's loads in
             // flight: long enough for them to land

@@ -1,0 +1,55 @@
+"""More tests of the 8-bit and grouped operators on the GPU: pairs of thread
+blocks that leave, long contractions, rows at the ends of F32's range, every
+plan, broken offsets over many runs, streams, threads and captured chains.
+
+Tolerances are those of test_gpu_fp8_grouped.py unless a test states its own.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_fp8_grouped import DT, E4M3, Guarded, gen, offsets_of, runs, sk  # noqa: E402,F401
+
+pytestmark = pytest.mark.gpu
+
+
+def whole(g, dtype, *shape, most=3):
+    """Whole numbers of at most `most`: products and sums of fewer than 2^24 are exact."""
+    return torch.randint(-most, most + 1, shape, device="cuda", generator=g).float().to(dtype)
+
+
+# ------------------------------------------------------------------ pairs of thread blocks
+
+@pytest.mark.parametrize("kblocks", [1, 2, 3, 4, 5, 6, 7, 9])
+@pytest.mark.parametrize("form", ["fp8", "bt", "dw"])
+def test_pairs_leave_after_their_last_stages(sk, form, kblocks):
+    """Launches of pairs (this many tiles take them) with fewer k-blocks than the
+    ring has stages, as many and more, one behind the other: the next launch's
+    blocks take over the shared memory that the last one's arrivals went to."""
+    g = gen(kblocks)
+    M = N = 4096
+    outs = [Guarded((M, N), torch.float32) for _ in range(2)]
+    if form == "fp8":
+        K = 128 * kblocks - 16
+        a, b = whole(g, E4M3, M, K), whole(g, E4M3, N, K)
+        ones = [torch.ones(r, kblocks, device="cuda") for r in (M, (N + 127) // 128)]
+        for i in range(24):
+            sk.gemm_fp8_bt(a, ones[0], b, ones[1], outs[i % 2].data, M, N, K, "f32")
+        want = a.double() @ b.double().T
+    elif form == "bt":
+        K = 64 * kblocks - 8
+        a, b = whole(g, torch.bfloat16, M, K), whole(g, torch.bfloat16, N, K)
+        _, offs = offsets_of([M])
+        for i in range(24):
+            sk.gemm_grouped_bt(a, b, offs, outs[i % 2].data, M, 1, N, K, "bf16", "f32")
+        want = a.double() @ b.double().T
+    else:
+        T = 64 * kblocks - 5                      # the last k-block ends inside a step of 16
+        a, d = whole(g, torch.bfloat16, T, M), whole(g, torch.bfloat16, T, N)
+        _, offs = offsets_of([T])
+        for i in range(24):
+            sk.gemm_grouped_dw(a, d, offs, outs[i % 2].data, T, 1, N, M, "bf16", "f32")
+        want = d.double().T @ a.double()
+    assert sk.splitk_get_device_status() == 0
+    for out in outs:
+        assert torch.equal(out.data.double(), want) and out.intact()
