@@ -446,9 +446,9 @@ struct Extent {
 
 // NULL and alignment of every pointer (a tensor without elements may be NULL),
 // then each output against the inputs and the other outputs.  `in_place` (may
-// be -1): the one output that may be exactly one of the inputs (same address
-// and extent).
-int validate_extents(const Extent *in, int n_in, const Extent *out, int n_out, int in_place = -1)
+// be -1): the one output that may be exactly one of the first `in_place_of`
+// inputs (same address and extent).
+int validate_extents(const Extent *in, int n_in, const Extent *out, int n_out, int in_place = -1, int in_place_of = 0)
 {
     for (int i = 0; i < n_in; ++i)
         if (!in[i].p && in[i].bytes) return SPLITK_ERR_NULL;
@@ -462,7 +462,7 @@ int validate_extents(const Extent *in, int n_in, const Extent *out, int n_out, i
         const Range r = range_of(out[o].p, out[o].bytes);
         for (int i = 0; i < n_in; ++i)
             if (overlap(r, range_of(in[i].p, in[i].bytes)) &&
-                !(o == in_place && in[i].p == out[o].p && in[i].bytes == out[o].bytes))
+                !(o == in_place && i < in_place_of && in[i].p == out[o].p && in[i].bytes == out[o].bytes))
                 return SPLITK_ERR_ALIAS;
         for (int i = 0; i < o; ++i)
             if (overlap(r, range_of(out[i].p, out[i].bytes))) return SPLITK_ERR_ALIAS;
@@ -482,14 +482,15 @@ int rows_fp8(const void *x, const void *residual, const void *weight, void *sum,
     Extent in[3] = {{x, bytes}}, out[4] = {{q, static_cast<uint64_t>(M * K)},
                                            {scales, static_cast<uint64_t>(M * blocks_of(K)) * 4}};
     int n_in = 1, n_out = 2, in_place = -1;
-    if (weight) in[n_in++] = {weight, static_cast<uint64_t>(K) * e};
     if (residual) in[n_in++] = {residual, bytes};
+    const int rows = n_in;                             // x and the residual, which `sum` may be
+    if (weight) in[n_in++] = {weight, static_cast<uint64_t>(K) * e};
     if (y) out[n_out++] = {y, bytes};
     if (sum) {
         in_place = n_out;
         out[n_out++] = {sum, bytes};
     }
-    const int st = validate_extents(in, n_in, out, n_out, in_place);
+    const int st = validate_extents(in, n_in, out, n_out, in_place, rows);
     if (st != SPLITK_OK || M == 0) return st;
     return cuda_status(splitk::launch_rows_fp8({x, residual, weight, sum, y, q, scales, M, K, eps, dtype},
                                                static_cast<cudaStream_t>(stream)));
