@@ -367,11 +367,14 @@ int splitk_autotune_splits(const void *A, const void *B, float *out,
  * 16-bit ones, whatever N and M (or T) are, unless said otherwise.  M (or T)
  * may be 0: nothing is written then, except by gemm_grouped_dw, and the
  * tensors without elements may be NULL.  M, T, N, K <=
- * SPLITK_MAX_DIM, G <= SPLITK_MAX_GROUPS (else SPLITK_ERR_SHAPE).  Pointers are
+ * SPLITK_MAX_DIM, G <= SPLITK_MAX_GROUPS, and what a call works through must
+ * count below 2^31: ceil(N/128) * (T/32 + G) tiles of a product (M for T, G =
+ * 1 where there are no runs), G * ceil(K/128) * ceil(N/32) of gemm_grouped_dw,
+ * the scales of fp8_prepare_bt (else SPLITK_ERR_SHAPE).  Pointers are
  * 16-byte aligned (`offsets`: 4-byte), outputs overlap nothing (exceptions are
  * named), and out_dtype is SPLITK_F32, _F16 or _BF16, rounded once from the
  * F32 sum.  Checks come before any device work, in the order shape, dtype,
- * NULL, alignment, overlap.  The calls take no workspace, may be captured,
+ * NULL, alignment, overlap, eps.  The calls take no workspace, may be captured,
  * and give the same bits for the same call every time. */
 
 /* Residual addition, root-mean-square norm, 8-bit output:

@@ -442,6 +442,7 @@ constexpr int kFp8Block = 128;
 struct Extent {
     const void *p;
     uint64_t bytes;
+    uintptr_t align = 16;
 };
 
 // NULL and alignment of every pointer (a tensor without elements may be NULL),
@@ -455,9 +456,9 @@ int validate_extents(const Extent *in, int n_in, const Extent *out, int n_out, i
     for (int i = 0; i < n_out; ++i)
         if (!out[i].p && out[i].bytes) return SPLITK_ERR_NULL;
     for (int i = 0; i < n_in; ++i)
-        if (!aligned16(in[i].p)) return SPLITK_ERR_ALIGN;
+        if (reinterpret_cast<uintptr_t>(in[i].p) % in[i].align) return SPLITK_ERR_ALIGN;
     for (int i = 0; i < n_out; ++i)
-        if (!aligned16(out[i].p)) return SPLITK_ERR_ALIGN;
+        if (reinterpret_cast<uintptr_t>(out[i].p) % out[i].align) return SPLITK_ERR_ALIGN;
     for (int o = 0; o < n_out; ++o) {
         const Range r = range_of(out[o].p, out[o].bytes);
         for (int i = 0; i < n_in; ++i)
@@ -472,8 +473,8 @@ int validate_extents(const Extent *in, int n_in, const Extent *out, int n_out, i
 
 int64_t blocks_of(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
 
-int rows_fp8(const void *x, const void *residual, const void *weight, void *sum, void *y, void *q, float *scales,
-             int64_t M, int64_t K, float eps, int dtype, void *stream)
+int rows_fp8(bool norm, const void *x, const void *residual, const void *weight, void *sum, void *y, void *q,
+             float *scales, int64_t M, int64_t K, float eps, int dtype, void *stream)
 {
     if (M < 0 || M > SPLITK_MAX_DIM || K <= 0 || K > SPLITK_MAX_DIM || K % 16) return SPLITK_ERR_SHAPE;
     const int e = elem_bytes(dtype);
@@ -484,14 +485,16 @@ int rows_fp8(const void *x, const void *residual, const void *weight, void *sum,
     int n_in = 1, n_out = 2, in_place = -1;
     if (residual) in[n_in++] = {residual, bytes};
     const int rows = n_in;                             // x and the residual, which `sum` may be
-    if (weight) in[n_in++] = {weight, static_cast<uint64_t>(K) * e};
+    if (norm) in[n_in++] = {weight, static_cast<uint64_t>(K) * e};
     if (y) out[n_out++] = {y, bytes};
     if (sum) {
         in_place = n_out;
         out[n_out++] = {sum, bytes};
     }
     const int st = validate_extents(in, n_in, out, n_out, in_place, rows);
-    if (st != SPLITK_OK || M == 0) return st;
+    if (st != SPLITK_OK) return st;
+    if (!(eps >= 0.f)) return SPLITK_ERR_CONFIG;
+    if (M == 0) return SPLITK_OK;
     return cuda_status(splitk::launch_rows_fp8({x, residual, weight, sum, y, q, scales, M, K, eps, dtype},
                                                static_cast<cudaStream_t>(stream)));
 }
@@ -509,12 +512,12 @@ int grouped(GroupedForm form, const void *A, const float *sa, const void *B, con
         K > SPLITK_MAX_DIM || K % step)
         return SPLITK_ERR_SHAPE;
     if ((form == GroupedForm::kKn || dw) && N % step) return SPLITK_ERR_SHAPE;
-    if (!fp8 && dtype != SPLITK_BF16 && dtype != SPLITK_F16) return SPLITK_ERR_DTYPE;
-    const int oe = elem_bytes(out_dtype);
-    if (oe == 0) return SPLITK_ERR_DTYPE;
     const splitk::GroupedProblem p = {form, A, B, sa, sb, offsets, out, T, G, N, K, out_dtype, dtype == SPLITK_BF16};
     // tile counts are 32-bit
     if (splitk::grouped_tiles(p, 32) > INT32_MAX) return SPLITK_ERR_SHAPE;
+    if (!fp8 && dtype != SPLITK_BF16 && dtype != SPLITK_F16) return SPLITK_ERR_DTYPE;
+    const int oe = elem_bytes(out_dtype);
+    if (oe == 0) return SPLITK_ERR_DTYPE;
     const int64_t e = fp8 ? 1 : 2;
     const int64_t kb = blocks_of(K);
     Extent in[5] = {{A, static_cast<uint64_t>(T * K * e)},
@@ -524,15 +527,10 @@ int grouped(GroupedForm form, const void *A, const float *sa, const void *B, con
         in[n_in++] = {sa, static_cast<uint64_t>(T * kb) * 4};
         in[n_in++] = {sb, static_cast<uint64_t>(G * blocks_of(N) * kb) * 4};
     }
+    if (!plain) in[n_in++] = {offsets, static_cast<uint64_t>(G + 1) * 4, 4};
     const Extent o[1] = {{out, static_cast<uint64_t>(dw ? G * N * K : T * N) * oe}};
-    int st = validate_extents(in, n_in, o, 1);
+    const int st = validate_extents(in, n_in, o, 1);
     if (st != SPLITK_OK) return st;
-    if (!plain) {
-        if (!offsets) return SPLITK_ERR_NULL;
-        if (reinterpret_cast<uintptr_t>(offsets) & 3u) return SPLITK_ERR_ALIGN;
-        if (overlap(range_of(offsets, static_cast<uint64_t>(G + 1) * 4), range_of(out, o[0].bytes)))
-            return SPLITK_ERR_ALIAS;
-    }
     if (T == 0 && !dw) return SPLITK_OK;
     return cuda_status(splitk::launch_grouped(p, static_cast<cudaStream_t>(stream)));
 }
@@ -542,14 +540,12 @@ int grouped(GroupedForm form, const void *A, const float *sa, const void *B, con
 int rmsnorm_fp8(const void *x, const void *residual, const void *weight, void *sum, void *y, void *q, float *scales,
                 int64_t M, int64_t K, float eps, int dtype, void *stream)
 {
-    if (!weight) return SPLITK_ERR_NULL;
-    if (!(eps >= 0.f)) return SPLITK_ERR_CONFIG;
-    return rows_fp8(x, residual, weight, sum, y, q, scales, M, K, eps, dtype, stream);
+    return rows_fp8(true, x, residual, weight, sum, y, q, scales, M, K, eps, dtype, stream);
 }
 
 int fp8_quantize(const void *x, void *q, float *scales, int64_t M, int64_t K, int dtype, void *stream)
 {
-    return rows_fp8(x, nullptr, nullptr, nullptr, nullptr, q, scales, M, K, 0.f, dtype, stream);
+    return rows_fp8(false, x, nullptr, nullptr, nullptr, nullptr, q, scales, M, K, 0.f, dtype, stream);
 }
 
 int fp8_prepare_bt(const void *B, void *Bq, float *scales, int64_t G, int64_t N, int64_t K, int dtype, void *stream)
