@@ -1399,11 +1399,22 @@ cudaError_t launch_tiles(const GroupedProblem &p, int splits, int64_t tiles, int
     return note_error(cudaLaunchKernelEx(&cfg, grouped_kernel<FORM, TC, SUMS>, maps, a), "cudaLaunchKernelEx(grouped_kernel)");
 }
 
+// Products of a value that a 16-bit output may leave to one accumulator in
+// tensor memory.  It cuts off what a step of 16 products adds below its last
+// place: sums of one sign come out low by about 1.6 * 2^-24 a step on GB300, 8192
+// products by 5e-5 (an eighth of F16's half unit, 2^-11), 131072 by 7.8e-4.
+// Longer ones are added in registers every kUnit k-blocks, as for an F32 output
+// (131072 products: 1e-5; 8192 rows, N 8192, K 16384: 1.23 ms, in one accumulator
+// 1.17; the gradient of 8 runs of 16384 rows, N = K = 2048: 648 us and 640).
+constexpr int64_t kOneAccumulator = 8192;
+
 template <int FORM, int TC>
 cudaError_t launch_form(const GroupedProblem &p, int splits, int64_t tiles, int dev, int sms, cudaStream_t stream)
 {
+    // (kDw: no run is longer than T)
+    const int64_t products = FORM == kDw ? p.T : (p.K + splits - 1) / splits;
     if constexpr (FORM != kFp8)
-        if (p.out_type != 0) return launch_tiles<FORM, TC, false>(p, splits, tiles, dev, sms, stream);
+        if (p.out_type != 0 && products <= kOneAccumulator) return launch_tiles<FORM, TC, false>(p, splits, tiles, dev, sms, stream);
     return launch_tiles<FORM, TC, true>(p, splits, tiles, dev, sms, stream);
 }
 

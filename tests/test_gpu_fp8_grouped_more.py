@@ -8,7 +8,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_fp8_grouped import DT, E4M3, Guarded, gen, offsets_of, runs, sk  # noqa: E402,F401
+from test_gpu_fp8_grouped import DT, E4M3, Guarded, c_16, check, gen, offsets_of, runs, sk  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +53,42 @@ def test_pairs_leave_after_their_last_stages(sk, form, kblocks):
     assert sk.splitk_get_device_status() == 0
     for out in outs:
         assert torch.equal(out.data.double(), want) and out.intact()
+
+
+# ------------------------------------------------------------------ long contractions
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("form", ["bt", "kn", "dw"])
+def test_long_contraction_with_16_bit_output(sk, form, dt):
+    """131072 products of one sign a value: the output is rounded from an F32 sum,
+    so the error that goes with the length is that of its additions (every 512
+    products), not of a tensor-core accumulator (every 16, cut off): c_16 of an
+    F32 output, and half a unit of the output's last place."""
+    L = 131072
+    g = gen(21)
+
+    def positive(*shape):
+        return (torch.rand(*shape, device="cuda", generator=g) * 0.5 + 0.25).to(DT[dt])
+
+    if form == "dw":
+        counts, N, K = [L, 0, 70], 136, 72
+        T, G = sum(counts), len(counts)
+        a, d = positive(T, K), positive(T, N)
+        o, offs = offsets_of(counts)
+        res = Guarded((G, N, K), DT[dt])
+        sk.gemm_grouped_dw(a, d, offs, res.data, T, G, N, K, dt, dt)
+        got = [(res.data[e], d[r].double().T @ a[r].double()) for e, r in runs(o)]
+        assert not res.data[1].any()
+    else:
+        T, N = 1100, 1104
+        a = positive(T, L)
+        w = positive(1, *((L, N) if form == "kn" else (N, L)))
+        _, offs = offsets_of([T])
+        res = Guarded((T, N), DT[dt])
+        (sk.gemm_grouped_kn if form == "kn" else sk.gemm_grouped_bt)(a, w, offs, res.data, T, 1, N, L, dt, dt)
+        rows = torch.arange(0, T, 17, device="cuda")
+        got = [(res.data[rows], a[rows].double() @ (w[0] if form == "kn" else w[0].T).double())]
+    assert sk.splitk_get_device_status() == 0
+    for out, ref in got:
+        check(out, ref, ref, c_16(L, "f32"), dt)       # all terms are positive
+    assert res.intact()
