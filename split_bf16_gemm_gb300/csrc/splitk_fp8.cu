@@ -26,7 +26,7 @@
 namespace splitk {
 namespace {
 
-constexpr float kE4m3Max = 448.f;                          // its reciprocal times 448 2^n is 2^n exactly
+constexpr float kE4m3Max = 448.f;
 constexpr float kScaleFloor = 1.17549435082228751e-38f;   // 2^-126
 constexpr int kVec = 8;                                    // values a thread takes at once
 constexpr int kBlockVecs = 128 / kVec;                     // threads that share a scale
@@ -102,6 +102,17 @@ __device__ __forceinline__ uint2 to_e4m3(const float (&v)[kVec])
     for (int i = 0; i < 4; ++i)
         w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// The scale of a block whose largest magnitude is m: m / 448, rounded once (the
+// product with the rounded reciprocal alone is a unit off for 55% of the m), by the
+// correction that divide() takes; an infinity stays one.
+__device__ __forceinline__ float scale_of(float m)
+{
+    constexpr float kInv = 1.f / kE4m3Max;
+    const float q0 = m * kInv;
+    const float s = isinf(m) ? m : fmaf(fmaf(-kE4m3Max, q0, m), kInv, q0);
+    return max_nan(s, kScaleFloor);
 }
 
 // The quotients of a block's values and its scale s, each rounded once: q0 =
@@ -227,7 +238,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rows_kernel(const RowsA
             // the 16 threads of a scale are consecutive lanes of one warp
 #pragma unroll
             for (int d = kBlockVecs / 2; d; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-            const float s = max_nan(m * (1.f / kE4m3Max), kScaleFloor);
+            const float s = scale_of(m);
             if (in) {
                 if (a.y) {
                     Pack<T> p;
@@ -276,7 +287,7 @@ __global__ void __launch_bounds__(256) prepare_fp8_kernel(const T *B, uint8_t *q
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max_nan(m, part[i]);
-    const float s = max_nan(m * (1.f / kE4m3Max), kScaleFloor);
+    const float s = scale_of(m);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int r = r0 + 16 * i;

@@ -8,7 +8,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_fp8_grouped import DT, E4M3, Guarded, c_16, check, gen, offsets_of, runs, sk  # noqa: E402,F401
+from test_gpu_fp8_grouped import (BLOCK, DT, E4M3, Guarded, c_16, check, gen, nblk, offsets_of, randn,  # noqa: E402
+                                  runs, sk, spread)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +93,66 @@ def test_long_contraction_with_16_bit_output(sk, form, dt):
     for out, ref in got:
         check(out, ref, ref, c_16(L, "f32"), dt)       # all terms are positive
     assert res.intact()
+
+
+# ------------------------------------------------------------------ scales and codes to the last bit
+
+def scales_of(m):
+    """max(m / 448, 2^-126) in F32 from the largest magnitudes m: a quotient of F32
+    numbers in 64 bits is far enough from a tie to be rounded to F32 once more."""
+    return (m.double() / 448).clamp_min(2.0 ** -126).float()
+
+
+def largest(x):
+    M, K = x.shape
+    return torch.nn.functional.pad(x.float(), (0, nblk(K) * BLOCK - K)).view(M, -1, BLOCK).abs().amax(-1)
+
+
+def same_bits(a, b):
+    return torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M,K", [(1, 16), (300, 400), (64, 4096), (3, 30000)])
+def test_quantized_rows_to_the_last_bit(sk, M, K, dt):
+    x = (randn(gen(K + M), M, K) * 3).to(DT[dt])
+    q, s = Guarded((M, K), E4M3), Guarded((M, nblk(K)), torch.float32)
+    sk.fp8_quantize(x, q.data, s.data, M, K, dt)
+    assert torch.equal(s.data, scales_of(largest(x)))
+    assert same_bits(q.data, (x.float() / spread(s.data, K, 1)).to(E4M3))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("G,N,K", [(1, 1, 16), (3, 130, 272), (2, 500, 2064)])
+def test_prepared_weights_to_the_last_bit(sk, G, N, K, dt):
+    b = randn(gen(N + K), G, N, K).to(DT[dt])
+    q, s = Guarded((G, N, K), E4M3), Guarded((G, nblk(N), nblk(K)), torch.float32)
+    sk.fp8_prepare_bt(b, q.data, s.data, G, N, K, dt)
+    pad = torch.nn.functional.pad(b.float(), (0, nblk(K) * BLOCK - K, 0, nblk(N) * BLOCK - N))
+    assert torch.equal(s.data, scales_of(pad.view(G, nblk(N), BLOCK, nblk(K), BLOCK).abs().amax((2, 4))))
+    assert same_bits(q.data, (b.float() / spread(spread(s.data, N, 1), K, 2)).to(E4M3))
+
+
+@pytest.mark.parametrize("M,K", [(300, 400), (64, 4096), (3, 30000)])
+def test_norm_codes_follow_from_its_output(sk, M, K):
+    """With F32 inputs y is what the scales and codes are made of."""
+    g = gen(K)
+    x, w = randn(g, M, K), 1 + 0.2 * randn(g, K)
+    q, s, y = Guarded((M, K), E4M3), Guarded((M, nblk(K)), torch.float32), Guarded((M, K), torch.float32)
+    sk.rmsnorm_fp8(x, w, q.data, s.data, M, K, "f32", eps=1e-5, y=y.data)
+    assert torch.equal(s.data, scales_of(largest(y.data)))
+    assert same_bits(q.data, (y.data / spread(s.data, K, 1)).to(E4M3))
+
+
+@pytest.mark.parametrize("eps", [0.0, 0.5])
+def test_norm_root_is_one_operation(sk, eps):
+    """Rows of one value c of 10 significant bits: squares, their sum, the mean and
+    the sum with eps are exact, so y = c / sqrt(c^2 + eps) is off by what the
+    reciprocal root may be (two units, 2^-22) and the product's rounding, 2^-24."""
+    K, M = 512, 512
+    c = torch.arange(512, 512 + M, device="cuda").float() / 512
+    x = c[:, None].expand(M, K).contiguous()
+    q, s, y = Guarded((M, K), E4M3), Guarded((M, nblk(K)), torch.float32), Guarded((M, K), torch.float32)
+    sk.rmsnorm_fp8(x, torch.ones(K, device="cuda"), q.data, s.data, M, K, "f32", eps=eps, y=y.data)
+    ref = x.double() / (x.double().square() + eps).sqrt()
+    assert bool(((y.data.double() - ref).abs() <= 5 * 2.0 ** -24 * ref).all())
