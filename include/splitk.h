@@ -389,9 +389,11 @@ int splitk_autotune_splits(const void *A, const void *B, float *out,
  *                x or residual (in place)
  *   y            device, [M,K] of `dtype` or NULL: receives y, rounded once
  *   q, scales    device, as above
- * A row that holds a NaN gets NaN scales and codes; one that holds an infinity
- * NaN in the infinity's block and zeros elsewhere (its mean is infinite).
- * eps >= 0 (else SPLITK_ERR_CONFIG). */
+ * Finite rows of any size have their norm, also where the squares leave F32's
+ * range.  A row that holds a NaN gets NaN scales and codes; one that holds an
+ * infinity NaN in the infinity's block and zeros elsewhere (its mean is
+ * infinite).  eps >= 0 (else SPLITK_ERR_CONFIG); with eps = 0 a row of zeros
+ * is 0 / 0: NaN scales and codes. */
 int rmsnorm_fp8(const void *x, const void *residual, const void *weight,
                 void *sum, void *y, void *q, float *scales, int64_t M,
                 int64_t K, float eps, int dtype, void *stream);

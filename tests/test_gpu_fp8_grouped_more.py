@@ -8,8 +8,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_fp8_grouped import (BLOCK, DT, E4M3, Guarded, c_16, check, gen, nblk, offsets_of, randn,  # noqa: E402
-                                  runs, sk, spread)  # noqa: F401
+from test_gpu_fp8_grouped import (BLOCK, DT, E4M3, HALF_UNIT, Guarded, c_16, check, check_rows, gen,  # noqa: E402
+                                  nblk, offsets_of, randn, runs, sk, spread)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -156,3 +156,60 @@ def test_norm_root_is_one_operation(sk, eps):
     sk.rmsnorm_fp8(x, torch.ones(K, device="cuda"), q.data, s.data, M, K, "f32", eps=eps, y=y.data)
     ref = x.double() / (x.double().square() + eps).sqrt()
     assert bool(((y.data.double() - ref).abs() <= 5 * 2.0 ** -24 * ref).all())
+
+
+# ------------------------------------------------------------------ rows whose squares leave F32's range
+
+@pytest.mark.parametrize("eps", [0.0, 1e-36, 1e-6])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [16, 400, 1008, 2048, 4096, 8208, 20000])
+def test_norm_of_rows_at_the_ends_of_the_range(sk, K, dt, eps):
+    """Rows of one launch (several share a block) from 3e38 down to the smallest
+    numbers, beside ordinary ones, against 64 bits; the relative error of the
+    root is test_norm's, whatever the row's size."""
+    scale = [1.0, 1e30, 5e19, 3e37, 1e-18, 1e-20, 1e-25, 1e-38, 1.0, 1e-3] + ([1e-43] if dt == "f32" else [])
+    M = len(scale)
+    g = gen(K)
+    x = (randn(g, M, K).clamp(-4, 4).double() * torch.tensor(scale, device="cuda").double()[:, None]).to(DT[dt])
+    x[8, 3] = 3e38                                        # one value decides
+    w = (1 + 0.2 * randn(g, K)).to(DT[dt])
+    q, s, y = Guarded((M, K), E4M3), Guarded((M, nblk(K)), torch.float32), Guarded((M, K), DT[dt])
+    sk.rmsnorm_fp8(x, w, q.data, s.data, M, K, dt, eps=eps, y=y.data)
+    H = x.double()
+    ref = H / (H.square().mean(-1, keepdim=True) + torch.tensor(eps, dtype=torch.float32).double().item()).sqrt() * w.double()
+    rel = (8 * (K // 4096 + 1) * 4 + 10 + 6) * 2.0 ** -24
+    check_rows(ref, q.data, s.data, rel)
+    # below 2^-126 the output's step is 2^-149 (BF16: 2^-133)
+    tol = (rel + HALF_UNIT[dt]) * ref.abs() + (2.0 ** -133 if dt == "bf16" else 2.0 ** -148)
+    assert bool(((y.data.double() - ref).abs() <= tol).all())
+    assert q.intact() and s.intact() and y.intact()
+
+
+@pytest.mark.parametrize("K", [400, 1008, 2048, 20000])
+@pytest.mark.parametrize("kept", ["x", "residual", "new", "none"])
+def test_norm_of_large_sums(sk, K, kept):
+    """The same through the residual's addition, the sum kept in place, elsewhere or not at all."""
+    M = 4
+    g = gen(K + 1)
+    x, r, w = randn(g, M, K) * 1e25, randn(g, M, K) * 1e25, torch.ones(K, device="cuda")
+    h = x + r
+    q, s = Guarded((M, K), E4M3), Guarded((M, nblk(K)), torch.float32)
+    out = {"x": x, "residual": r, "new": torch.empty_like(x), "none": None}[kept]
+    sk.rmsnorm_fp8(x, w, q.data, s.data, M, K, "f32", residual=r, sum_out=out)
+    assert out is None or torch.equal(out, h)
+    ref = h.double() / h.double().square().mean(-1, keepdim=True).sqrt()
+    check_rows(ref, q.data, s.data, (8 * (K // 4096 + 1) * 4 + 10 + 6) * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("K", [400, 1008, 20000])
+def test_norm_of_zeros_without_eps_and_of_infinities(sk, K):
+    """0 / 0 is NaN; beside it an infinity's block is NaN and its row's others 0."""
+    x, w = torch.ones(3, K, device="cuda"), torch.ones(K, device="cuda")
+    x[0] = 0
+    x[1, 200] = -float("inf")
+    q, s = Guarded((3, K), E4M3), Guarded((3, nblk(K)), torch.float32)
+    sk.rmsnorm_fp8(x, w, q.data, s.data, 3, K, "f32", eps=0.0)
+    assert torch.isnan(s.data[0]).all() and torch.isnan(q.data[0].float()).all()
+    assert torch.isnan(s.data[1, 1]) and torch.isnan(q.data[1, 200].float())
+    assert not q.data[1, :128].float().any() and not q.data[1, 256:].float().any()
+    assert bool((q.data[2].float() == 448).all())
