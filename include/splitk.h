@@ -482,6 +482,15 @@ const char *splitk_status_string(int status);
  * SPLITK_OK or SPLITK_ERR_CONFIG. */
 int splitk_set_tile_override(int bn, int chunks, int kblocks_per_stage);
 
+/* The same for gemm_fp8_bt and the grouped products: every later launch takes
+ * tiles of `columns` columns (32, 64, 128 or 256, a pair of thread blocks;
+ * gemm_grouped_dw has 128 and 256 and keeps its own choice for less) and
+ * `splits` thread blocks along K (1, 2, 4 or 8; fewer where a split would have
+ * less than two k-blocks, and one with 256 columns and for gemm_grouped_dw).
+ * Zero keeps the automatic choice for that item.  Process-wide.  Returns
+ * SPLITK_OK or SPLITK_ERR_CONFIG. */
+int splitk_set_grouped_override(int columns, int splits);
+
 /* Describes the launch gemm_bt would make, without launching: info[0..25] =
  * {path (0 tensor-core, 2 tensor-core 3xTF32 for F32), bn, chunks, chunk_len, stages,
  *  cluster_size (chunks, or splits * chunks), grid_x, grid_y, grid_z,

@@ -30,7 +30,7 @@ EXPORTS = (
     "gemm_splitk_kn", "gemm_kn", "splitk_set_overlap", "splitk_last_launch", "splitk_selftest_kernel_timeout",
     "gemm_bt_batch",
     "rmsnorm_fp8", "fp8_quantize", "fp8_prepare_bt", "gemm_fp8_bt", "gemm_grouped_fp8_bt", "gemm_grouped_bt",
-    "gemm_grouped_kn", "gemm_grouped_dw",
+    "gemm_grouped_kn", "gemm_grouped_dw", "splitk_set_grouped_override",
 )
 NOALLOC_MAX_BYTES = 32 << 20   # SPLITK_NOALLOC_MAX_BYTES
 
@@ -70,6 +70,7 @@ def lib() -> ctypes.CDLL:
             L.splitk_status_string.argtypes = [i32]
             L.splitk_status_string.restype = ctypes.c_char_p
             L.splitk_set_tile_override.argtypes = [i32, i32, i32]
+            L.splitk_set_grouped_override.argtypes = [i32, i32]
             L.splitk_describe_launch.argtypes = [i64, i64, i64, i64, i64, i32, i32, vp]
             L.splitk_selftest_bounded_wait.argtypes = [i64, vp]
             L.gemm_bt_workspace_init.argtypes = [vp, sz, vp]
@@ -100,7 +101,7 @@ def lib() -> ctypes.CDLL:
                          "gemm_splitk_kn", "gemm_kn",
                          "gemm_bt_workspace_init", "gemm_bt_noalloc", "splitk_prepare_bt",
                          "gemm_bt_host_batch", "splitk_choose_splits", "splitk_autotune_splits",
-                         "splitk_get_device_status", "splitk_set_tile_override",
+                         "splitk_get_device_status", "splitk_set_tile_override", "splitk_set_grouped_override",
                          "splitk_describe_launch", "splitk_selftest_bounded_wait", "splitk_set_overlap",
                          "splitk_last_launch", "splitk_selftest_kernel_timeout"):
                 getattr(L, name).restype = i32
@@ -279,6 +280,10 @@ def splitk_get_device_status(stream=None) -> int:
 
 def splitk_set_tile_override(bn: int = 0, chunks: int = 0, kblocks_per_stage: int = 0) -> None:
     _check(lib().splitk_set_tile_override(bn, chunks, kblocks_per_stage), "splitk_set_tile_override")
+
+
+def splitk_set_grouped_override(columns: int = 0, splits: int = 0) -> None:
+    _check(lib().splitk_set_grouped_override(columns, splits), "splitk_set_grouped_override")
 
 
 def splitk_describe_launch(M, N, K, splits, k_per_split, dtype, fused=0) -> dict:

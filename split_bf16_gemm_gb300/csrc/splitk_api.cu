@@ -639,6 +639,14 @@ int splitk_set_tile_override(int bn, int chunks, int kblocks_per_stage)
     return SPLITK_OK;
 }
 
+int splitk_set_grouped_override(int columns, int splits)
+{
+    if (columns != 0 && columns != 32 && columns != 64 && columns != 128 && columns != 256) return SPLITK_ERR_CONFIG;
+    if (splits != 0 && splits != 1 && splits != 2 && splits != 4 && splits != 8) return SPLITK_ERR_CONFIG;
+    splitk::set_grouped_override(columns, splits);
+    return SPLITK_OK;
+}
+
 int splitk_describe_launch(int64_t M, int64_t N, int64_t K, int64_t splits, int64_t k_per_split, int dtype, int fused,
                            int *info)
 {

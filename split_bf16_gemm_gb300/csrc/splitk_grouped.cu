@@ -1283,6 +1283,8 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm)
 
 constexpr int kMaxDevices = 64;
 
+std::atomic<int> g_plan_override{0};   // columns of a tile << 8 | splits, 0 for either: the model's choice
+
 bool encode(CUtensorMap *map, CUtensorMapDataType type, int elem, int rank, const void *ptr, const uint64_t *dims,
             const uint32_t *box)
 {
@@ -1446,10 +1448,12 @@ GroupedPlan plan_grouped(const GroupedProblem &p, int sms)
     constexpr double kAlone = 0.8;           // of those figures, for a 32-column block alone on its SM
     const bool dw = p.form == GroupedForm::kDw, fp8 = p.form == GroupedForm::kFp8;
     const int64_t k = dw ? std::max<int64_t>(1, p.T / p.G) : p.K, kb = (k + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64);
+    const int asked = g_plan_override.load(std::memory_order_relaxed), only_tc = asked >> 8, only_splits = asked & 255;
     GroupedPlan best = {128, 1};
     double least = 0;
     for (const Tiling &t : kTilings) {
         if (dw && t.tc < 128) continue;
+        if (only_tc != 0 && t.tc != only_tc && !(dw && only_tc < 128)) continue;
         const int64_t tl = t.tc == 256 ? 2 * kLanes : kLanes;
         const double lane_tiles = static_cast<double>(((dw ? p.K : p.N) + tl - 1) / tl);
         const double runs = static_cast<double>(std::min(p.G, p.T));
@@ -1457,9 +1461,14 @@ GroupedPlan plan_grouped(const GroupedProblem &p, int sms)
                                  : p.G == 1 ? static_cast<double>((p.T + t.tc - 1) / t.tc)
                                             : std::max(runs, static_cast<double>(p.T) / t.tc + runs / 2);
         const double places = t.tc == 256 ? sms / 2 : t.tc == 32 ? sms * 2 : sms;
-        for (int splits = 1; splits <= 8; splits *= 2) {
-            // a split of fewer than two k-blocks, or more blocks than places, never pays
-            if (splits > 1 && (dw || t.tc == 256 || kb < 2 * splits || lane_tiles * col_tiles * splits > places)) break;
+        int most = 1;   // a split of fewer than two k-blocks never pays
+        while (most < 8 && !dw && t.tc != 256 && kb >= 4 * most) most *= 2;
+        for (int splits = 1; splits <= most; splits *= 2) {
+            if (only_splits != 0) {
+                if (splits != std::min(only_splits, most)) continue;
+            } else if (splits > 1 && lane_tiles * col_tiles * splits > places) {
+                break;   // more blocks than places
+            }
             const double waves = std::ceil(lane_tiles * col_tiles * splits / places);
             double rate = (fp8 ? t.us8 : t.us16) * (t.tc == 32 && lane_tiles * col_tiles * splits <= sms ? kAlone : 1.);
             // a pair's 16-bit time goes by the rows it loads: 128 lanes and half the columns a block
@@ -1473,6 +1482,8 @@ GroupedPlan plan_grouped(const GroupedProblem &p, int sms)
     }
     return best;
 }
+
+void set_grouped_override(int columns, int splits) { g_plan_override.store(columns << 8 | splits); }
 
 template <int FORM>
 cudaError_t launch_plan(const GroupedProblem &p, const GroupedPlan &plan, int64_t tiles, int dev, int sms, cudaStream_t stream)

@@ -130,6 +130,8 @@ struct GroupedPlan {
     int splits;                // thread blocks of a cluster, along K
 };
 GroupedPlan plan_grouped(const GroupedProblem &p, int sms);
+// Every later plan: 0 leaves the choice.  splits are kept to what the call allows.
+void set_grouped_override(int columns, int splits);
 // Tiles of the problem at `tc` columns each: exact for one run and for kDw, an
 // upper bound for ragged runs.
 int64_t grouped_tiles(const GroupedProblem &p, int tc);

@@ -66,3 +66,12 @@ def test_too_many_tiles_is_a_shape(L):
     for call in (gfp8, grouped16("gemm_grouped_bt")):
         assert call(L, T=1 << 22, N=1 << 22, dt=9) == bd.ERR_SHAPE
     assert grouped16("gemm_grouped_dw")(L, G=1024, N=1 << 22, K=1 << 22, dt=9) == bd.ERR_SHAPE
+
+
+def test_grouped_override_validation(L):
+    for columns, splits in [(16, 0), (96, 1), (512, 1), (-32, 0), (0, 3), (64, 16), (0, -1)]:
+        assert L.splitk_set_grouped_override(columns, splits) == bd.ERR_CONFIG
+    for columns in (0, 32, 64, 128, 256):
+        for splits in (0, 1, 2, 4, 8):
+            assert L.splitk_set_grouped_override(columns, splits) == bd.OK
+    assert L.splitk_set_grouped_override(0, 0) == bd.OK

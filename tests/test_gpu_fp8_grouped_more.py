@@ -8,8 +8,9 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_fp8_grouped import (BLOCK, DT, E4M3, HALF_UNIT, Guarded, c_16, check, check_rows, gen,  # noqa: E402
-                                  nblk, offsets_of, randn, runs, sk, spread)  # noqa: F401
+from test_gpu_fp8_grouped import (BLOCK, DT, E4M3, HALF_UNIT, Guarded, c_16, c_fp8, check, check_rows,  # noqa: E402
+                                  fp8_rows, fp8_weights, gen, nblk, offsets_of, randn, real_rows,
+                                  real_weights, runs, sk, spread)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -213,3 +214,146 @@ def test_norm_of_zeros_without_eps_and_of_infinities(sk, K):
     assert torch.isnan(s.data[1, 1]) and torch.isnan(q.data[1, 200].float())
     assert not q.data[1, :128].float().any() and not q.data[1, 256:].float().any()
     assert bool((q.data[2].float() == 448).all())
+
+
+# ------------------------------------------------------------------ every plan
+
+PLANS = [(c, s) for c in (32, 64, 128) for s in (1, 2, 4, 8)] + [(256, 1)]
+PLAN_IDS = [f"{c}x{s}" for c, s in PLANS]
+# counts, N, rows before the first run and after the last: rows that are whole boxes
+# of the outputs' stores and not, whole 16 bytes and not, runs that end inside a
+# tile, and more tiles than an SM or a pair of them takes at once
+PLAN_SETS = {
+    "ragged": ([130, 0, 1, 255, 64, 129], 264, 2, 3),
+    "rows8": ([700], 1000, 0, 0),
+    "odd": ([333, 31, 0, 512], 1001, 1, 0),
+    "few": ([0, 3, 1, 0, 16, 33], 520, 0, 1),
+    "many": ([2500, 0, 300], 5200, 0, 0),
+    "wide": ([4, 60], 5188, 0, 0),
+}
+
+
+@pytest.fixture
+def planned(sk):
+    yield sk.splitk_set_grouped_override
+    sk.splitk_set_grouped_override(0, 0)
+
+
+_operands = {}
+
+
+def operands(form, name):
+    """Operands of a set and their products in 64 bits, kept while the same set is asked for."""
+    if (form, name) not in _operands:
+        _operands.clear()
+        counts, N, before, after = PLAN_SETS[name]
+        if form in ("kn", "dw"):
+            N = N // 8 * 8
+        K = {"fp8": 2064, "dw": 392}.get(form, 1032)          # 17 k-blocks, the last a short one
+        G, T = len(counts), sum(counts) + before + after
+        g = gen(T + N)
+        o, offs = offsets_of(counts, before)
+        if form == "fp8":
+            a, b = fp8_rows(g, T, K), fp8_weights(g, G, N, K)
+            A, B = real_rows(*a), real_weights(*b)
+            refs = [(r, A[r] @ B[e].T, A[r].abs() @ B[e].abs().T) for e, r in runs(o)]
+        else:
+            a = randn(g, T, K).bfloat16()
+            b = randn(g, *{"bt": (G, N, K), "kn": (G, K, N), "dw": (T, N)}[form]).bfloat16()
+            A, B = a.double(), b.double()
+            if form == "dw":
+                refs = [(e, B[r].T @ A[r], B[r].abs().T @ A[r].abs()) for e, r in runs(o)]
+            else:
+                W = B if form == "kn" else B.mT
+                refs = [(r, A[r] @ W[e], A[r].abs() @ W[e].abs()) for e, r in runs(o)]
+        _operands[form, name] = (a, b, o, offs, T, G, N, K, refs)
+    return _operands[form, name]
+
+
+def planned_product(sk, form, name, out):
+    a, b, o, offs, T, G, N, K, refs = operands(form, name)
+    res = Guarded((G, N, K) if form == "dw" else (T, N), DT[out])
+    if form == "fp8":
+        sk.gemm_grouped_fp8_bt(*a, *b, offs, res.data, T, G, N, K, out)
+    else:
+        call = {"bt": sk.gemm_grouped_bt, "kn": sk.gemm_grouped_kn, "dw": sk.gemm_grouped_dw}[form]
+        call(a, b, offs, res.data, T, G, N, K, "bf16", out)
+    return res
+
+
+def check_planned(sk, form, name, out, plan):
+    a, b, o, offs, T, G, N, K, refs = operands(form, name)
+    # the same call twice, with another plan's between
+    first = planned_product(sk, form, name, out)
+    sk.splitk_set_grouped_override(256 if plan[0] == 128 else 128, 1)
+    planned_product(sk, form, name, out)
+    sk.splitk_set_grouped_override(*plan)
+    res = planned_product(sk, form, name, out)
+    assert sk.splitk_get_device_status() == 0
+    assert torch.equal(first.raw, res.raw)
+    # a sum over splits adds one rounding a split
+    L = max(o[e + 1] - o[e] for e in range(G)) if form == "dw" else K
+    c = (c_fp8(K) if form == "fp8" else c_16(L, out)) + plan[1]
+    for at, ref, mag in refs:
+        check(res.data[at], ref, mag, c, out)
+    if form == "dw":
+        for e in range(G):
+            assert o[e + 1] > o[e] or not res.data[e].any()
+    else:
+        assert torch.isnan(res.data[:o[0]].float()).all() and torch.isnan(res.data[o[-1]:].float()).all()
+    assert res.intact()
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("plan", PLANS, ids=PLAN_IDS)
+@pytest.mark.parametrize("name", PLAN_SETS)
+@pytest.mark.parametrize("form", ["fp8", "bt", "kn"])
+def test_every_plan(sk, planned, form, name, plan, out):
+    planned(*plan)
+    check_planned(sk, form, name, out, plan)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("columns", [128, 256])
+@pytest.mark.parametrize("name", PLAN_SETS)
+def test_every_plan_of_the_weight_gradient(sk, planned, name, columns, out):
+    planned(columns, 1)
+    check_planned(sk, "dw", name, out, (columns, 1))
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("plan", PLANS, ids=PLAN_IDS)
+@pytest.mark.parametrize("M,N", [(1, 64), (33, 1160), (300, 136), (2000, 2600)])
+def test_every_plan_of_the_plain_product(sk, planned, M, N, plan, out):
+    K = 2064
+    g = gen(M)
+    a, b = fp8_rows(g, M, K), fp8_weights(g, 1, N, K)
+    res = Guarded((M, N), DT[out])
+    planned(*plan)
+    sk.gemm_fp8_bt(*a, b[0][0], b[1][0], res.data, M, N, K, out)
+    assert sk.splitk_get_device_status() == 0
+    A, B = real_rows(*a), real_weights(*b)[0]
+    check(res.data, A @ B.T, A.abs() @ B.abs().T, c_fp8(K) + plan[1], out)
+    assert res.intact()
+
+
+@pytest.mark.parametrize("plan", [(128, 1), (256, 1)], ids=["128x1", "256x1"])
+@pytest.mark.parametrize("form", ["bt", "kn", "dw"])
+def test_sums_in_registers_for_16_bit_outputs(sk, planned, form, plan):
+    """Past 8192 products 16-bit outputs take the sums in registers, in each form."""
+    L = 8200 + 56
+    g = gen(7)
+    planned(*plan)
+    T, N, K = (L - 3, 264, 136) if form == "dw" else (333, 264, L)
+    a = randn(g, T, K).bfloat16()
+    b = randn(g, *{"bt": (1, N, K), "kn": (1, K, N), "dw": (T, N)}[form]).bfloat16()
+    _, offs = offsets_of([T])
+    res = Guarded((1, N, K) if form == "dw" else (T, N), DT["f16"])
+    call = {"bt": sk.gemm_grouped_bt, "kn": sk.gemm_grouped_kn, "dw": sk.gemm_grouped_dw}[form]
+    call(a, b, offs, res.data, T, 1, N, K, "bf16", "f16")
+    assert sk.splitk_get_device_status() == 0
+    A, B = a.double(), b.double()
+    left, right = {"bt": (A, B.mT), "kn": (A, B), "dw": (B.mT, A)}[form]
+    got, right = (res.data[0], right) if form == "dw" else (res.data, right[0])
+    check(got, left @ right, left.abs() @ right.abs(), c_16(L, "f32"), "f16")
+    assert res.intact()
