@@ -360,7 +360,10 @@ int splitk_autotune_splits(const void *A, const void *B, float *out,
  *                values of a row
  *   weights      q [G,N,K], scales [G, ceil(N/128), ceil(K/128)]: a scale for
  *                each 128 x 128 block (edge blocks smaller)
- * Scales may be any F32 values (no power of two is assumed).
+ * Scales may be any F32 values (no power of two is assumed).  A product forms
+ * the two scales that meet into one F32 factor first: beyond F32's range it is
+ * infinite, and NaN against a sum of 0; below 2^-126 it is within 2^-150 (a
+ * block of zeros, whose scale is 2^-126, gives 0 with any finite scale).
  *
  * Every tensor is dense and row-major; rows follow one another without
  * padding.  K is a positive multiple of 16 with 8-bit operands and of 8 with
@@ -412,7 +415,8 @@ int fp8_prepare_bt(const void *B, void *Bq, float *scales, int64_t G,
 
 /* out[m,n] = sum_b a_scales[m,b] * b_scales[n/128,b] * sum_{k in b} A[m,k]*B[n,k]
  * with A [M,K] and B [N,K] in 8 bits.  The sum over a block runs on the
- * tensor cores; the scaled sum over blocks is in F32. */
+ * tensor cores; the scaled sum over blocks is in F32, the scales multiplied
+ * first. */
 int gemm_fp8_bt(const void *A, const float *a_scales, const void *B,
                 const float *b_scales, void *out, int64_t M, int64_t N,
                 int64_t K, int out_dtype, void *stream);

@@ -357,3 +357,33 @@ def test_sums_in_registers_for_16_bit_outputs(sk, planned, form, plan):
     got, right = (res.data[0], right) if form == "dw" else (res.data, right[0])
     check(got, left @ right, left.abs() @ right.abs(), c_16(L, "f32"), "f16")
     assert res.intact()
+
+
+# ------------------------------------------------------------------ scales at the ends of the range
+
+@pytest.mark.parametrize("M", [5, 130, 300])
+def test_products_of_scales_at_the_ends_of_the_range(sk, M):
+    """The two scales' product is formed in F32 first.  Where it is an ordinary
+    number the result is as exact as ever, however large one scale and small the
+    other; below 2^-126 it is within half of F32's smallest step, 2^-150; beyond
+    the range it is infinite, and NaN against a sum of 0."""
+    N, K = 200, 400
+    g = gen(M)
+    a, _ = fp8_rows(g, M, K)
+    b, _ = fp8_weights(g, 1, N, K)
+    b = b[0]
+    a[0, 128:256] = 0
+    pairs = [(1e30, 1e-30), (1e-37, 1e30), (2.0 ** -120, 2.0 ** -20), (2.0 ** -100, 2.0 ** -60), (1e25, 1e14)]
+    for left, right in pairs:
+        sa = (torch.rand(M, nblk(K), device="cuda", generator=g) + 0.5) * left
+        sb = (torch.rand(nblk(N), nblk(K), device="cuda", generator=g) + 0.5) * right
+        res = Guarded((M, N), torch.float32)
+        sk.gemm_fp8_bt(a, sa, b, sb, res.data, M, N, K, "f32")
+        A, B = real_rows(a, sa), real_weights(b, sb)
+        if left * right > 3.5e38:
+            assert not torch.isfinite(res.data).any() and torch.isnan(res.data[0]).all()
+            continue
+        codes = a.double().abs() @ b.double().abs().T
+        tol = c_fp8(K) * 2.0 ** -23 * (A.abs() @ B.abs().T) + 2.0 ** -150 * codes + 2.0 ** -148
+        assert bool(((res.data.double() - A @ B.T).abs() <= tol).all()), (left, right)
+    assert sk.splitk_get_device_status() == 0
