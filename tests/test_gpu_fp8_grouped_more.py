@@ -387,3 +387,53 @@ def test_products_of_scales_at_the_ends_of_the_range(sk, M):
         tol = c_fp8(K) * 2.0 ** -23 * (A.abs() @ B.abs().T) + 2.0 ** -150 * codes + 2.0 ** -148
         assert bool(((res.data.double() - A @ B.T).abs() <= tol).all()), (left, right)
     assert sk.splitk_get_device_status() == 0
+
+
+# ------------------------------------------------------------------ broken offsets over many runs
+
+@pytest.mark.parametrize("form", ["bt", "fp8", "dw"])
+@pytest.mark.parametrize("G", [33, 70, 129])
+def test_broken_offsets_over_many_runs(sk, G, form):
+    """Offsets that fall and leave [0, T], also across the 32 runs that a warp takes
+    at a time: the runs are those of the clamped, rising sequence, rows outside
+    them stay as they were, and the gradients of empty runs are zero."""
+    T, N, K = 300, 136, 144
+    g = gen(G)
+    bad = torch.randint(0, 7, (G + 1,), generator=torch.Generator().manual_seed(G)).cumsum(0).tolist()
+    bad[0] = 9
+    bad[5] = -1000
+    for i, v in ((30, 150), (31, 2 ** 31 - 1 if G == 33 else 160), (32, 20), (33, -2 ** 31), (63, 190), (64, 30), (128, 5)):
+        if i < G:
+            bad[i] = v
+    offs = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    o = [min(max(x, 0), T) for x in bad]
+    for i in range(1, len(o)):
+        o[i] = max(o[i], o[i - 1])
+    if form == "fp8":
+        a, sa = fp8_rows(g, T, K)
+        b, sb = fp8_weights(g, G, N, K)
+        res = Guarded((T, N), torch.float32)
+        sk.gemm_grouped_fp8_bt(a, sa, b, sb, offs, res.data, T, G, N, K, "f32")
+        A, B = real_rows(a, sa), real_weights(b, sb)
+    else:
+        a, b, d = (randn(g, *s).bfloat16() for s in ((T, K), (G, N, K), (T, N)))
+        A, B, D = a.double(), b.double(), d.double()
+        if form == "bt":
+            res = Guarded((T, N), torch.float32)
+            sk.gemm_grouped_bt(a, b, offs, res.data, T, G, N, K, "bf16", "f32")
+        else:
+            res = Guarded((G, N, K), torch.float32)
+            sk.gemm_grouped_dw(a, d, offs, res.data, T, G, N, K, "bf16", "f32")
+    assert sk.splitk_get_device_status() == 0
+    assert 0 < o[0] and len(runs(o)) >= 3
+    for e, r in runs(o):
+        if form == "dw":
+            check(res.data[e], D[r].T @ A[r], D[r].abs().T @ A[r].abs(), c_16(T, "f32"), "f32")
+        else:
+            check(res.data[r], A[r] @ B[e].T, A[r].abs() @ B[e].abs().T, c_fp8(K) + 48, "f32")
+    if form == "dw":
+        for e in set(range(G)) - {e for e, _ in runs(o)}:
+            assert not res.data[e].any()
+    else:
+        assert torch.isnan(res.data[:o[0]]).all() and torch.isnan(res.data[o[-1]:]).all()
+    assert res.intact()
