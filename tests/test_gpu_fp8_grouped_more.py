@@ -437,3 +437,130 @@ def test_broken_offsets_over_many_runs(sk, G, form):
     else:
         assert torch.isnan(res.data[:o[0]]).all() and torch.isnan(res.data[o[-1]:]).all()
     assert res.intact()
+
+
+# ------------------------------------------------------------------ beside the split-K calls, streams, threads
+
+class Chain:
+    """Split-K product -> norm to 8 bits -> 8-bit product -> split-K product ->
+    rows to 8 bits -> grouped product: each reads what the one before wrote."""
+
+    M, D = 128, 512
+    COUNTS = [50, 0, 78]
+
+    def __init__(self, sk, seed):
+        g = gen(seed)
+        M, D = self.M, self.D
+        self.sk = sk
+        self.x = randn(g, M, D).bfloat16()
+        self.b1, self.b2 = ((randn(g, D, D) * D ** -0.5).bfloat16() for _ in range(2))
+        self.w = (1 + 0.1 * randn(g, D))
+        self.b3, self.s3 = fp8_weights(g, 1, D, D)
+        self.b4, self.s4 = fp8_weights(g, len(self.COUNTS), D, D)
+        _, self.offs = offsets_of(self.COUNTS)
+        self.nbytes = sk.gemm_bt_workspace_bytes(M, D, D, 2, D // 2)
+        self.ws = torch.empty(self.nbytes // 4, device="cuda")
+        sk.gemm_bt_workspace_init(self.ws, self.nbytes)
+        self.mid = [torch.empty(M, D, device="cuda"), torch.empty(M, D, dtype=E4M3, device="cuda"),
+                    torch.empty(M, nblk(D), device="cuda"), torch.empty(M, D, dtype=torch.bfloat16, device="cuda")]
+        self.out = torch.empty(M, D, device="cuda")
+
+    def run(self, fused=1, wait=lambda: None, stream=None):
+        sk, M, D = self.sk, self.M, self.D
+        c, q, s, h = self.mid
+        steps = (
+            lambda: sk.gemm_bt(self.x, self.b1, c, self.ws, self.nbytes, M, D, D, 2, D // 2, "bf16", fused=fused, stream=stream),
+            lambda: sk.rmsnorm_fp8(c, self.w, q, s, M, D, "f32", stream=stream),
+            lambda: sk.gemm_fp8_bt(q, s, self.b3, self.s3, h, M, D, D, "bf16", stream=stream),
+            lambda: sk.gemm_bt(h, self.b2, c, self.ws, self.nbytes, M, D, D, 2, D // 2, "bf16", fused=fused, stream=stream),
+            lambda: sk.fp8_quantize(c, q, s, M, D, "f32", stream=stream),
+            lambda: sk.gemm_grouped_fp8_bt(q, s, self.b4, self.s4, self.offs, self.out, M, len(self.COUNTS), D, D, "f32",
+                                           stream=stream),
+        )
+        for step in steps:
+            step()
+            wait()
+
+    def poison(self):
+        for t in (*self.mid, self.out):
+            t.view(torch.uint8).fill_(0xFF)
+
+
+@pytest.mark.parametrize("fused", [0, 1, 3])
+@pytest.mark.parametrize("mode", [0, 1, 2])
+def test_split_k_and_8_bit_calls_feed_one_another(sk, mode, fused):
+    """Every buffer is written and read again within the capture, so a launch that
+    started before its input was there, or wrote over what was still read, shows."""
+    chain = Chain(sk, 31)
+    chain.poison()
+    chain.run(fused, wait=torch.cuda.synchronize)
+    want = chain.out.clone()
+    assert torch.isfinite(want).all()
+    sk.splitk_set_overlap(mode)
+    try:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(3):
+                chain.run(fused)
+    finally:
+        sk.splitk_set_overlap(2)
+    for _ in range(5):
+        chain.poison()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(chain.out, want)
+    chain.poison()
+    for _ in range(3):
+        chain.run(fused)
+    torch.cuda.synchronize()
+    assert torch.equal(chain.out, want)
+    assert sk.splitk_get_device_status() == 0
+
+
+def test_streams_side_by_side(sk):
+    chains = [Chain(sk, 40 + i) for i in range(3)]
+    want = []
+    for c in chains:
+        c.run(wait=torch.cuda.synchronize)
+        want.append(c.out.clone())
+        c.poison()
+    streams = [torch.cuda.Stream() for _ in chains]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s in zip(chains, streams):
+            c.run(stream=s)
+    torch.cuda.synchronize()
+    for c, w in zip(chains, want):
+        assert torch.equal(c.out, w)
+    assert sk.splitk_get_device_status() == 0
+
+
+def test_threads_side_by_side(sk):
+    import threading
+
+    chains = [Chain(sk, 50 + i) for i in range(4)]
+    want, errors = [], []
+    for c in chains:
+        c.run(wait=torch.cuda.synchronize)
+        want.append(c.out.clone())
+        c.poison()
+    torch.cuda.synchronize()
+
+    def work(c):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(30):
+                c.run(stream=stream)
+            stream.synchronize()
+        except BaseException as e:   # noqa: B036 -- reported by the test
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in chains]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for c, w in zip(chains, want):
+        assert torch.equal(c.out, w)
+    assert sk.splitk_get_device_status() == 0
