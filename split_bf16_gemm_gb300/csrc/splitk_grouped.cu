@@ -1283,6 +1283,8 @@ __global__ void __launch_bounds__(kThreads, Shape<TC>::kPerSm)
 
 constexpr int kMaxDevices = 64;
 
+std::atomic<bool> g_launched[kMaxDevices];   // a product of this file was launched (or captured)
+
 std::atomic<int> g_plan_override{0};   // columns of a tile << 8 | splits, 0 for either: the model's choice
 
 bool encode(CUtensorMap *map, CUtensorMapDataType type, int elem, int rank, const void *ptr, const uint64_t *dims,
@@ -1513,6 +1515,7 @@ cudaError_t launch_grouped(const GroupedProblem &p, cudaStream_t stream)
         if (e != cudaSuccess) return note_error(e, "cudaDeviceGetAttribute(MultiProcessorCount)");
         if (dev < kMaxDevices) counts[dev].store(sms, std::memory_order_relaxed);
     }
+    if (dev < kMaxDevices) g_launched[dev].store(true);
     const GroupedPlan plan = plan_grouped(p, sms);
     const int64_t tiles = grouped_tiles(p, plan.tc);
     switch (p.form) {
@@ -1526,6 +1529,10 @@ cudaError_t launch_grouped(const GroupedProblem &p, cudaStream_t stream)
 cudaError_t read_and_clear_grouped_status(unsigned *status)
 {
     const unsigned zero = 0;
+    *status = 0;
+    int dev = 0;
+    // nothing launched, nothing to read: a copy is 5 us
+    if (cudaGetDevice(&dev) == cudaSuccess && dev < kMaxDevices && !g_launched[dev].load()) return cudaSuccess;
     cudaError_t e = cudaMemcpyFromSymbol(status, g_grouped_status, sizeof *status);
     if (e == cudaSuccess && *status) e = cudaMemcpyToSymbol(g_grouped_status, &zero, sizeof zero);
     return note_error(e, "reading the grouped kernels' status word");

@@ -1481,7 +1481,7 @@ cudaError_t read_and_clear_device_status(cudaStream_t stream, unsigned *status)
     cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return e;
     e = cudaMemcpyFromSymbol(status, g_device_status, sizeof(unsigned));
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || *status == 0) return e;
     return cudaMemcpyToSymbol(g_device_status, &zero, sizeof(unsigned));
 }
 
