@@ -6,14 +6,14 @@
 // eps) in F32; each 128 consecutive y share the scale s = max(max|y| / 448,
 // 2^-126), and q = E4M3(y / s), to nearest even.  448 is E4M3's largest value;
 // the floor keeps y / s defined for a block of zeros and s out of the
-// subnormals.  A NaN or an infinity in a block gives it a NaN or infinite
+// subnormals.  Rows whose squares F32 does not hold are scaled (row_again).  A NaN or an infinity in a block gives it a NaN or infinite
 // scale and NaN products, never finite ones.
 //
 // A row is read once: its values stay in registers (8 to a 16-byte load of
 // 16-bit inputs) between the sum of squares and the output.  Rows longer than
 // the registers of a block hold are read twice.  Bound by memory: e + 1 to 4e +
 // 1 bytes a value for e-byte inputs.  GB300: 8192 rows of 8192 BF16 with a
-// residual 73 us, 6.4 TB/s (0.95 of the measured copy rate); one row of 2048
+// residual 72 us, 6.6 TB/s (0.97 of the measured copy rate); one row of 2048
 // 1.7 us in a graph.
 
 #include <cuda_bf16.h>
@@ -124,7 +124,7 @@ __device__ __forceinline__ float scale_of(float m)
 // y (1/s), then Markstein's correction q = q0 + (y - s q0) (1/s) (P. Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
 // 1990).  Three operations a value: the norm of 8192 x 8192 BF16 with a residual
-// takes 73 us, with a division 84, uncorrected 72.  An infinite scale gives 0 for
+// took 73 us, with a division 84, uncorrected 72.  An infinite scale gives 0 for
 // finite values and NaN for the infinity, as a division does.
 template <int N>
 __device__ __forceinline__ void divide(float (&y)[N], float s)
