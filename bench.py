@@ -14,6 +14,7 @@ better), the roofline of the dominant kernel measured live with CUDA events,
 the end-to-end figure through the C ABI with host buffers (gemm_bt_host_batch:
 activations in and results out every step, pipelined), the clocks
 seen during the timed region, and the CPU oracle's time for the same work.
+The pages' other workloads (`configs`) are one JSON line on standard error.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
                     [--mode fused|two_pass] [--pack 8] [--pool 40]
@@ -760,6 +761,17 @@ def run_ours(args, rank, world, dev, torch, dist):
     return line
 
 
+def emit(line, out=None, err=None):
+    """The result as one line on standard output, without the table of the other
+    workloads: that is 20 KB, more than what reads such a line may take, and
+    goes to standard error as a line of its own."""
+    line = dict(line)
+    configs = line.pop("configs", None)
+    if configs is not None:
+        print(json.dumps({"configs": configs}), file=err or sys.stderr)
+    print(json.dumps(line), file=out or sys.stdout)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -824,7 +836,7 @@ def main():
                                 "single_thread": {"value": round(us1, 2), "unit": "µs/op", "cores": 1,
                                                   "sample": sample1}}
     if rank == 0:
-        print(json.dumps(line))
+        emit(line)
     if dist:
         dist.destroy_process_group()
 
