@@ -13,7 +13,7 @@
 // 16-bit inputs) between the sum of squares and the output.  Rows longer than
 // the registers of a block hold are read twice.  Bound by memory: e + 1 to 4e +
 // 1 bytes a value for e-byte inputs.  GB300: 8192 rows of 8192 BF16 with a
-// residual 72 us, 6.6 TB/s (0.97 of the measured copy rate); one row of 2048
+// residual 72 us, 6.6 TB/s (0.98 of the measured copy rate); one row of 2048
 // 1.7 us in a graph.
 
 #include <cuda_bf16.h>
