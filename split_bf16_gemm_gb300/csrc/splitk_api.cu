@@ -14,6 +14,7 @@
 #include <cstdio>
 
 #include "splitk.h"
+#include "splitk_checks.h"
 #include "splitk_internal.h"
 
 namespace splitk {
@@ -41,8 +42,16 @@ const char *last_error_message() { return g_last_error; }
 
 namespace {
 
+using splitk::blocks_of;
+using splitk::cuda_status;
+using splitk::elem_bytes;
+using splitk::Extent;
 using splitk::GemmProblem;
+using splitk::overlap;
+using splitk::Range;
+using splitk::range_of;
 using splitk::TilePlan;
+using splitk::validate_extents;
 
 int geometry_status(int64_t M, int64_t N, int64_t K, int64_t S, int64_t kps)
 {
@@ -56,31 +65,7 @@ int geometry_status(int64_t M, int64_t N, int64_t K, int64_t S, int64_t kps)
     return SPLITK_OK;
 }
 
-int elem_bytes(int dtype)
-{
-    switch (dtype) {
-    case SPLITK_F32: return 4;
-    case SPLITK_F16: return 2;
-    case SPLITK_BF16: return 2;
-    default: return 0;
-    }
-}
-
-struct Range {
-    uintptr_t lo, hi;   // [lo, hi)
-};
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-
-Range range_of(const void *p, uint64_t bytes)
-{
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{lo, lo + static_cast<uintptr_t>(bytes)};
-}
-
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? SPLITK_OK : SPLITK_ERR_CUDA; }
 
 // Checks shared by gemm_splitk_bt and gemm_bt.
 int validate_gemm(const void *A, const void *B, int64_t M, int64_t N, int64_t K, int64_t S, int64_t kps,
@@ -436,42 +421,6 @@ int gemm_kn(const void *A, const void *W, float *out, void *workspace, size_t wo
 // ---- 8-bit operands, rows grouped by expert
 
 namespace {
-
-constexpr int kFp8Block = 128;
-
-struct Extent {
-    const void *p;
-    uint64_t bytes;
-    uintptr_t align = 16;
-};
-
-// NULL and alignment of every pointer (a tensor without elements may be NULL),
-// then each output against the inputs and the other outputs.  `in_place` (may
-// be -1): the one output that may be exactly one of the first `in_place_of`
-// inputs (same address and extent).
-int validate_extents(const Extent *in, int n_in, const Extent *out, int n_out, int in_place = -1, int in_place_of = 0)
-{
-    for (int i = 0; i < n_in; ++i)
-        if (!in[i].p && in[i].bytes) return SPLITK_ERR_NULL;
-    for (int i = 0; i < n_out; ++i)
-        if (!out[i].p && out[i].bytes) return SPLITK_ERR_NULL;
-    for (int i = 0; i < n_in; ++i)
-        if (reinterpret_cast<uintptr_t>(in[i].p) % in[i].align) return SPLITK_ERR_ALIGN;
-    for (int i = 0; i < n_out; ++i)
-        if (reinterpret_cast<uintptr_t>(out[i].p) % out[i].align) return SPLITK_ERR_ALIGN;
-    for (int o = 0; o < n_out; ++o) {
-        const Range r = range_of(out[o].p, out[o].bytes);
-        for (int i = 0; i < n_in; ++i)
-            if (overlap(r, range_of(in[i].p, in[i].bytes)) &&
-                !(o == in_place && i < in_place_of && in[i].p == out[o].p && in[i].bytes == out[o].bytes))
-                return SPLITK_ERR_ALIAS;
-        for (int i = 0; i < o; ++i)
-            if (overlap(r, range_of(out[i].p, out[i].bytes))) return SPLITK_ERR_ALIAS;
-    }
-    return SPLITK_OK;
-}
-
-int64_t blocks_of(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
 
 int rows_fp8(bool norm, const void *x, const void *residual, const void *weight, void *sum, void *y, void *q,
              float *scales, int64_t M, int64_t K, float eps, int dtype, void *stream)

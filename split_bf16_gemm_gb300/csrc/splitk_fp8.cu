@@ -16,13 +16,12 @@
 // residual 72 us, 6.6 TB/s (0.98 of the measured copy rate); one row of 2048
 // 1.7 us in a graph.
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include <type_traits>
 
 #include "ptx.cuh"
+#include "rows.cuh"
 #include "splitk_internal.h"
 
 namespace splitk {
@@ -30,7 +29,6 @@ namespace {
 
 constexpr float kE4m3Max = 448.f;
 constexpr float kScaleFloor = 1.17549435082228751e-38f;   // 2^-126
-constexpr int kVec = 8;                                    // values a thread takes at once
 constexpr int kBlockVecs = 128 / kVec;                     // threads that share a scale
 
 // max that keeps a NaN
@@ -39,62 +37,6 @@ __device__ __forceinline__ float max_nan(float a, float b)
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
-}
-
-template <typename T>
-struct Pack;   // 8 values as they lie in memory
-template <>
-struct Pack<float> {
-    float4 a, b;
-};
-template <>
-struct Pack<__half> {
-    uint4 a;
-};
-template <>
-struct Pack<__nv_bfloat16> {
-    uint4 a;
-};
-
-__device__ __forceinline__ void unpack(const Pack<float> &p, float (&v)[kVec])
-{
-    v[0] = p.a.x, v[1] = p.a.y, v[2] = p.a.z, v[3] = p.a.w;
-    v[4] = p.b.x, v[5] = p.b.y, v[6] = p.b.z, v[7] = p.b.w;
-}
-__device__ __forceinline__ void pack(const float (&v)[kVec], Pack<float> &p)
-{
-    p.a = make_float4(v[0], v[1], v[2], v[3]);
-    p.b = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void unpack(const Pack<__half> &p, float (&v)[kVec])
-{
-    const __half2 *h = reinterpret_cast<const __half2 *>(&p.a);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(h[i]);
-        v[2 * i] = f.x, v[2 * i + 1] = f.y;
-    }
-}
-__device__ __forceinline__ void pack(const float (&v)[kVec], Pack<__half> &p)
-{
-    __half2 *h = reinterpret_cast<__half2 *>(&p.a);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-}
-__device__ __forceinline__ void unpack(const Pack<__nv_bfloat16> &p, float (&v)[kVec])
-{
-    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&p.a);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __bfloat1622float2(h[i]);
-        v[2 * i] = f.x, v[2 * i + 1] = f.y;
-    }
-}
-__device__ __forceinline__ void pack(const float (&v)[kVec], Pack<__nv_bfloat16> &p)
-{
-    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&p.a);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
 }
 
 __device__ __forceinline__ uint32_t to_e4m3(float a, float b, float c, float d)
@@ -405,19 +347,6 @@ __global__ void __launch_bounds__(256) prepare_fp8_kernel(const T *B, uint8_t *q
         }
     }
     if (threadIdx.x == 0) scales[id] = s;
-}
-
-cudaLaunchConfig_t config(unsigned grid, unsigned block, cudaStream_t stream, cudaLaunchAttribute *attr)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(block, 1, 1);
-    cfg.stream = stream;
-    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr->val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cfg;
 }
 
 template <typename T, int TPR, int VPT, bool LONG = false>
