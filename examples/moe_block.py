@@ -3,12 +3,12 @@
 One block of a decoder, from the residual stream to what is added to it:
 
   residual addition + RMS norm -> 8 bits            rmsnorm_fp8
-  router: the `top` best experts of each token      torch
-  the tokens' rows sorted by expert                 torch
+  router: the `top` best experts of each token      torch (the product), moe_route
+  the tokens' rows sorted by expert                 moe_dispatch_fp8
   gate and up projections, per expert               gemm_grouped_fp8_bt
   silu(gate) * up -> 8 bits                         torch, fp8_quantize
   down projection, per expert                       gemm_grouped_fp8_bt
-  weighted sum of each token's experts              torch
+  weighted sum of each token's experts              moe_combine
 
 Nothing waits for the GPU: the counts per expert stay on it.
 
@@ -60,20 +60,25 @@ class MoeBlock:
         y = torch.empty_like(x)
         sk.rmsnorm_fp8(x, self.norm, q, scales, M, K, x.dtype, residual=residual, sum_out=residual, y=y)
 
-        share, expert = torch.topk(torch.softmax((y @ self.router).float(), -1), self.top)
-        order = torch.argsort(expert.flatten(), stable=True)
-        token = order // self.top
-        counts = torch.zeros(G, dtype=torch.int32, device=x.device)
-        counts.scatter_add_(0, expert.flatten(), torch.ones_like(expert.flatten(), dtype=torch.int32))
-        offsets = torch.nn.functional.pad(torch.cumsum(counts, 0, dtype=torch.int32), (1, 0))
+        T, top = M * self.top, self.top
 
-        gate, up = self.gate_up(q.view(torch.uint8)[token].view(E4M3), scales[token], offsets).chunk(2, -1)
+        def empty(*shape, dtype=torch.int32):
+            return torch.empty(*shape, dtype=dtype, device=x.device)
+
+        expert, share = empty(M, top), empty(M, top, dtype=torch.float32)
+        sk.moe_route(y @ self.router, expert, share, M, G, top, x.dtype)
+        offsets, slots = empty(G + 1), empty(M, top)
+        rows, row_scales = empty(T, K, dtype=E4M3), empty(T, blocks(K), dtype=torch.float32)
+        sk.moe_dispatch_fp8(expert, q, scales, offsets, slots, None, rows, row_scales, M, top, G, K)
+
+        gate, up = self.gate_up(rows, row_scales, offsets).chunk(2, -1)
         h = (torch.nn.functional.silu(gate.float()) * up.float()).bfloat16()
         hq = torch.empty(h.shape, dtype=E4M3, device=x.device)
         hs = torch.empty(h.shape[0], blocks(h.shape[1]), device=x.device)
         sk.fp8_quantize(h, hq, hs, h.shape[0], h.shape[1], h.dtype)
-        out = self.down(hq, hs, offsets)
-        return torch.zeros(M, K, device=x.device).index_add_(0, token, out.float() * share.flatten()[order, None]), residual
+        out = empty(M, K, dtype=torch.float32)
+        sk.moe_combine(self.down(hq, hs, offsets), slots, share, out, M, top, K, "bf16", "f32")
+        return out, residual
 
 
 def plain(block, x, residual, gate_up, down):

@@ -112,6 +112,11 @@ typedef enum {
 #define SPLITK_MAX_SPLITS 4096
 /* Runs (experts) of a grouped product. */
 #define SPLITK_MAX_GROUPS 1024
+/* Experts of one token. */
+#define SPLITK_MAX_TOP 32
+/* Tensors of one gradient norm, and values of one of them. */
+#define SPLITK_MAX_TENSORS 65536
+#define SPLITK_MAX_TENSOR_VALUES ((int64_t)1 << 34)
 /* Size of the scratch array gemm_bt_noalloc keeps in device memory. */
 #define SPLITK_NOALLOC_MAX_BYTES (32 << 20)
 
@@ -460,6 +465,163 @@ int gemm_grouped_kn(const void *A, const void *W, const int32_t *offsets,
 int gemm_grouped_dw(const void *A, const void *D, const int32_t *offsets,
                     void *dB, int64_t T, int64_t G, int64_t N, int64_t K,
                     int dtype, int out_dtype, void *stream);
+
+/* ---- Routing, and rows sorted by expert and back
+ *
+ * M tokens (M may be 0), each with `top` entries (1 .. SPLITK_MAX_TOP): entry
+ * m * top + j is token m's j-th expert.  M * top <= SPLITK_MAX_DIM, the rows that
+ * a grouped product takes.  Every tensor is dense and row-major.  The int32
+ * tensors are 4-byte aligned, the others 16-byte; outputs overlap nothing
+ * (exceptions are named).  Checks come before any device work, in the order
+ * shape, dtype, NULL, alignment, overlap, values.  The calls take no workspace,
+ * may be captured, and give the same bits for the same call every time. */
+
+/* The router's choice: each token's `top` largest logits and their shares.
+ *   logits   device, [M,G] of `dtype` (SPLITK_F32, _F16, _BF16), top <= G <=
+ *            SPLITK_MAX_GROUPS; -inf masks an expert
+ *   experts  device, int32 [M,top]: falling logits, the lowest index first among
+ *            equal ones; -1 where a token has fewer experts above -inf
+ *   shares   device, F32 [M,top]: exp(logit) / sum exp(logit), the sum over all
+ *            G (chosen_only = 0) or over the token's experts (1); 0 for a -1
+ * A NaN counts as larger than any number (and its experts are valid ones); a row
+ * with a NaN or +inf among the logits that are summed has NaN shares. */
+int moe_route(const void *logits, int32_t *experts, float *shares, int64_t M,
+              int64_t G, int64_t top, int chosen_only, int dtype, void *stream);
+
+/* The logits' gradient:
+ *   dlogits[m,i] = p[i] * (sum_{j: experts[m,j] = i} dshares[m,j] - c),
+ *   c = sum_j p[experts[m,j]] * dshares[m,j]
+ * with p the row's softmax (chosen_only: over the token's experts, 0 elsewhere).
+ *   logits, experts  as moe_route had and gave them; an entry outside [0,G) is
+ *                    passed over, and an expert that is there twice counts twice
+ *   dshares          device, F32 [M,top]
+ *   dlogits          device, [M,G] of `dtype`, fully overwritten */
+int moe_route_grad(const void *logits, const int32_t *experts,
+                   const float *dshares, void *dlogits, int64_t M, int64_t G,
+                   int64_t top, int chosen_only, int dtype, void *stream);
+
+/* Entries sorted by expert, equal experts in the entries' order:
+ *   experts  device, int32 [M,top]; an entry outside [0,G) goes nowhere
+ *   offsets  device, int32 [G+1]: run g of a grouped product; offsets[0] = 0
+ *   slots    device, int32 [M,top]: the entry's row, -1 for one that goes nowhere
+ *   source   device, int32 [M*top] or NULL: the row's entry, -1 from offsets[G] on
+ * With M = 0 the offsets are zeros. */
+int moe_sort(const int32_t *experts, int32_t *offsets, int32_t *slots,
+             int32_t *source, int64_t M, int64_t top, int64_t G, void *stream);
+
+/* moe_sort, and the tokens' rows with it: rows[slots[m,j]] = x[m].
+ *   x     device, [M,K] of `dtype`, K a positive multiple of 8
+ *   rows  device, [M*top,K]; rows from offsets[G] on are left as they are
+ * The gradient of x: moe_combine of the rows' gradients, without shares. */
+int moe_dispatch(const int32_t *experts, const void *x, int32_t *offsets,
+                 int32_t *slots, int32_t *source, void *rows, int64_t M,
+                 int64_t top, int64_t G, int64_t K, int dtype, void *stream);
+
+/* The same for rows in 8 bits with their scales: q [M,K] and scales
+ * [M,ceil(K/128)] to rows [M*top,K] and row_scales [M*top,ceil(K/128)]; K a
+ * positive multiple of 16. */
+int moe_dispatch_fp8(const int32_t *experts, const void *q, const float *scales,
+                     int32_t *offsets, int32_t *slots, int32_t *source,
+                     void *rows, float *row_scales, int64_t M, int64_t top,
+                     int64_t G, int64_t K, void *stream);
+
+/* Rows back to their tokens, weighted:
+ *   out[m] = sum_j shares[m,j] * rows[slots[m,j]]   in F32, j rising, rounded once
+ *   rows    device, [M*top,K] of `dtype`, K a positive multiple of 8
+ *   slots   device, int32 [M,top]; an entry outside [0,M*top) adds nothing
+ *   shares  device, F32 [M,top], or NULL for ones
+ *   out     device, [M,K] of out_dtype */
+int moe_combine(const void *rows, const int32_t *slots, const float *shares,
+                void *out, int64_t M, int64_t top, int64_t K, int dtype,
+                int out_dtype, void *stream);
+
+/* The gradients of moe_combine's rows and shares:
+ *   drows[slots[m,j]] = shares[m,j] * dout[m]
+ *   dshares[m,j]      = sum_k dout[m,k] * rows[slots[m,j],k]   (0 for a slot that
+ *                       is none)
+ *   dout     device, [M,K] of `dtype`
+ *   rows     device, [M*top,K] of `dtype`; read for dshares alone (else may be NULL)
+ *   drows    device, [M*top,K] of `dtype` or NULL; rows that no slot names are
+ *            left as they are; may be exactly `rows` (in place)
+ *   dshares  device, F32 [M,top] or NULL; one of the two is asked for (else
+ *            SPLITK_ERR_NULL)
+ * No two slots name the same row (moe_sort's never do). */
+int moe_combine_grad(const void *dout, const void *rows, const int32_t *slots,
+                     const float *shares, void *drows, float *dshares,
+                     int64_t M, int64_t top, int64_t K, int dtype, void *stream);
+
+/* ---- Layer norm
+ *
+ * Rows [M,K] (M may be 0), K a positive multiple of 8, M and K <= SPLITK_MAX_DIM,
+ * element type SPLITK_F32, _F16 or _BF16; pointers 16-byte aligned.  The checks
+ * and the rest as above; grad calls take a workspace, checked after the overlaps
+ * (SPLITK_ERR_WORKSPACE). */
+
+/* Residual addition and layer norm:
+ *   h = x + residual, rounded to `dtype` (h = x without a residual)
+ *   y = (h - mean) * rstd * weight + bias,  rstd = 1 / sqrt(mean_k (h - mean)^2 + eps)
+ *   x, residual   device, [M,K]; residual may be NULL
+ *   weight, bias  device, [K]; bias may be NULL
+ *   sum           device, [M,K] or NULL: receives h; may be exactly x or residual
+ *   y             device, [M,K], rounded once from F32
+ *   mean, rstd    device, F32 [M] or NULL: what layernorm_grad takes
+ * Finite rows of any size have their norm, also where the squares leave F32's
+ * range; a row that holds a NaN or an infinity is NaN.  eps >= 0 (else
+ * SPLITK_ERR_CONFIG); with eps = 0 a row of equal values is 0 / 0. */
+int layernorm(const void *x, const void *residual, const void *weight,
+              const void *bias, void *sum, void *y, float *mean, float *rstd,
+              int64_t M, int64_t K, float eps, int dtype, void *stream);
+
+/* Bytes of device workspace layernorm_grad needs; 0 for a rejected shape. */
+size_t layernorm_grad_workspace_bytes(int64_t M, int64_t K);
+
+/* Its gradients, with n = (h - mean) * rstd and g = dy * weight:
+ *   dx      = rstd * (g - mean_k g - n * mean_k (g n)) + dsum
+ *   dweight = sum_m dy * n,  dbias = sum_m dy
+ *   dy          device, [M,K]
+ *   h           device, [M,K]: the norm's input (`sum`, or x without a residual)
+ *   mean, rstd  device, F32 [M], from layernorm
+ *   dsum        device, [M,K] or NULL: the gradient that reaches h besides
+ *   dx          device, [M,K], rounded once: the gradient of x and of the
+ *               residual; may be exactly dy or dsum
+ *   dweight     device, F32 [K], fully overwritten (zeros with M = 0)
+ *   dbias       device, F32 [K] or NULL, as dweight
+ *   workspace   device, >= layernorm_grad_workspace_bytes(), needs no contents;
+ *               calls that may run at the same time need one each */
+int layernorm_grad(const void *dy, const void *h, const void *weight,
+                   const float *mean, const float *rstd, const void *dsum,
+                   void *dx, float *dweight, float *dbias, void *workspace,
+                   size_t workspace_bytes, int64_t M, int64_t K, int dtype,
+                   void *stream);
+
+/* ---- The norm of all gradients
+ *
+ * `count` (0 .. SPLITK_MAX_TENSORS) dense tensors, given as host arrays that are
+ * read before the call returns:
+ *   grads   device pointers, 16-byte aligned; NULL where the size is 0
+ *   sizes   values of each, 0 .. SPLITK_MAX_TENSOR_VALUES, any number
+ *   dtypes  SPLITK_F32, _F16 or _BF16 of each
+ *   norm    device, one F32 (4-byte aligned): sqrt of the sum of all squares
+ *   workspace  device, >= grad_norm_workspace_bytes(), 16-byte aligned, needs no
+ *              contents; calls that may run at the same time need one each
+ * Finite gradients of any size have their norm (infinite where F32 does not hold
+ * it).  A captured call keeps the tensors' addresses in its graph nodes.  Checks
+ * come before any device work, in the order sizes, dtype, NULL, alignment, overlap,
+ * workspace, max_norm; the same call gives the same bits every time. */
+size_t grad_norm_workspace_bytes(void);
+int grad_norm(const void *const *grads, const int64_t *sizes, const int *dtypes,
+              int64_t count, float *norm, void *workspace,
+              size_t workspace_bytes, void *stream);
+
+/* The norm as above (of the gradients before scaling), and
+ *   out[i] = grads[i] * min(1, max_norm / norm)   rounded once
+ *   out  device pointers of the same sizes and types, or NULL for grads (in
+ *        place; so may any single out[i]); no other overlap, and no tensor twice
+ * With a NaN norm every value becomes NaN, with an infinite one 0 (infinities
+ * NaN).  max_norm finite and >= 0, else SPLITK_ERR_CONFIG. */
+int grad_clip(void *const *grads, void *const *out, const int64_t *sizes,
+              const int *dtypes, int64_t count, float max_norm, float *norm,
+              void *workspace, size_t workspace_bytes, void *stream);
 
 /* Reads and clears the device status word on the current device,
  * synchronising `stream` first.  Returns SPLITK_OK, SPLITK_ERR_DEVICE_TIMEOUT

@@ -19,4 +19,7 @@ from .binding import (  # noqa: F401
     status_string,
     fp8_prepare_bt, fp8_quantize, gemm_fp8_bt, gemm_grouped_bt, gemm_grouped_dw, gemm_grouped_fp8_bt,
     gemm_grouped_kn, rmsnorm_fp8,
+    GradList, grad_clip, grad_list, grad_norm, grad_norm_workspace_bytes, layernorm, layernorm_grad,
+    layernorm_grad_workspace_bytes, moe_combine, moe_combine_grad, moe_dispatch, moe_dispatch_fp8, moe_route,
+    moe_route_grad, moe_sort,
 )

@@ -31,6 +31,8 @@ EXPORTS = (
     "gemm_bt_batch",
     "rmsnorm_fp8", "fp8_quantize", "fp8_prepare_bt", "gemm_fp8_bt", "gemm_grouped_fp8_bt", "gemm_grouped_bt",
     "gemm_grouped_kn", "gemm_grouped_dw", "splitk_set_grouped_override",
+    "moe_route", "moe_route_grad", "moe_sort", "moe_dispatch", "moe_dispatch_fp8", "moe_combine", "moe_combine_grad",
+    "layernorm", "layernorm_grad_workspace_bytes", "layernorm_grad", "grad_norm_workspace_bytes", "grad_norm", "grad_clip",
 )
 NOALLOC_MAX_BYTES = 32 << 20   # SPLITK_NOALLOC_MAX_BYTES
 
@@ -95,7 +97,24 @@ def lib() -> ctypes.CDLL:
             L.gemm_grouped_fp8_bt.argtypes = [vp] * 6 + [i64] * 4 + [i32, vp]
             for name in ("gemm_grouped_bt", "gemm_grouped_kn", "gemm_grouped_dw"):
                 getattr(L, name).argtypes = [vp] * 4 + [i64] * 4 + [i32, i32, vp]
-            for name in ("rmsnorm_fp8", "fp8_quantize", "fp8_prepare_bt", "gemm_fp8_bt", "gemm_grouped_fp8_bt",
+            L.moe_route.argtypes = [vp] * 3 + [i64] * 3 + [i32, i32, vp]
+            L.moe_route_grad.argtypes = [vp] * 4 + [i64] * 3 + [i32, i32, vp]
+            L.moe_sort.argtypes = [vp] * 4 + [i64] * 3 + [vp]
+            L.moe_dispatch.argtypes = [vp] * 6 + [i64] * 4 + [i32, vp]
+            L.moe_dispatch_fp8.argtypes = [vp] * 8 + [i64] * 4 + [vp]
+            L.moe_combine.argtypes = [vp] * 4 + [i64] * 3 + [i32, i32, vp]
+            L.moe_combine_grad.argtypes = [vp] * 6 + [i64] * 3 + [i32, vp]
+            L.layernorm.argtypes = [vp] * 8 + [i64] * 2 + [f32, i32, vp]
+            L.layernorm_grad_workspace_bytes.argtypes = [i64, i64]
+            L.layernorm_grad_workspace_bytes.restype = sz
+            L.layernorm_grad.argtypes = [vp] * 10 + [sz, i64, i64, i32, vp]
+            L.grad_norm_workspace_bytes.argtypes = []
+            L.grad_norm_workspace_bytes.restype = sz
+            L.grad_norm.argtypes = [vp] * 3 + [i64, vp, vp, sz, vp]
+            L.grad_clip.argtypes = [vp] * 4 + [i64, f32, vp, vp, sz, vp]
+            for name in ("moe_route", "moe_route_grad", "moe_sort", "moe_dispatch", "moe_dispatch_fp8", "moe_combine",
+                         "moe_combine_grad", "layernorm", "layernorm_grad", "grad_norm", "grad_clip",
+                         "rmsnorm_fp8", "fp8_quantize", "fp8_prepare_bt", "gemm_fp8_bt", "gemm_grouped_fp8_bt",
                          "gemm_grouped_bt", "gemm_grouped_kn", "gemm_grouped_dw",
                          "splitk_check_geometry", "gemm_splitk_bt", "splitk_reduce", "gemm_bt",
                          "gemm_splitk_kn", "gemm_kn",
@@ -416,3 +435,125 @@ def gemm_grouped_dw(A, D, offsets, dB, T, G, N, K, dtype, out_dtype, stream=None
     status = (_lib or lib()).gemm_grouped_dw(_ptr(A), _ptr(D), _ptr(offsets), _ptr(dB), T, G, N, K, _code(dtype),
                                              _code(out_dtype), _on(stream))
     _check(status, "gemm_grouped_dw")
+
+
+def moe_route(logits, experts, shares, M, G, top, dtype, chosen_only=False, stream=None) -> None:
+    """Each token's `top` best experts (int32 [M,top], -1 where there are fewer
+    above -inf) and their softmax shares (F32 [M,top]) over all G logits, or over
+    the chosen ones alone."""
+    status = (_lib or lib()).moe_route(_ptr(logits), _ptr(experts), _ptr(shares), M, G, top, chosen_only, _code(dtype),
+                                       _on(stream))
+    _check(status, "moe_route")
+
+
+def moe_route_grad(logits, experts, dshares, dlogits, M, G, top, dtype, chosen_only=False, stream=None) -> None:
+    """The gradient of moe_route's logits [M,G] from that of its shares [M,top]."""
+    status = (_lib or lib()).moe_route_grad(_ptr(logits), _ptr(experts), _ptr(dshares), _ptr(dlogits), M, G, top,
+                                            chosen_only, _code(dtype), _on(stream))
+    _check(status, "moe_route_grad")
+
+
+def moe_sort(experts, offsets, slots, source, M, top, G, stream=None) -> None:
+    """Entries sorted by expert: offsets (int32 [G+1]), each entry's row (slots
+    [M,top], -1 for one that goes nowhere) and each row's entry (source [M*top], or
+    None)."""
+    status = (_lib or lib()).moe_sort(_ptr(experts), _ptr(offsets), _ptr(slots), _ptr(source), M, top, G, _on(stream))
+    _check(status, "moe_sort")
+
+
+def moe_dispatch(experts, x, offsets, slots, source, rows, M, top, G, K, dtype, stream=None) -> None:
+    """moe_sort, and the tokens' rows x [M,K] sorted with it: rows [M*top,K]."""
+    status = (_lib or lib()).moe_dispatch(_ptr(experts), _ptr(x), _ptr(offsets), _ptr(slots), _ptr(source), _ptr(rows),
+                                          M, top, G, K, _code(dtype), _on(stream))
+    _check(status, "moe_dispatch")
+
+
+def moe_dispatch_fp8(experts, q, scales, offsets, slots, source, rows, row_scales, M, top, G, K, stream=None) -> None:
+    """moe_dispatch of 8-bit rows q [M,K] with their scales [M, ceil(K/128)]."""
+    status = (_lib or lib()).moe_dispatch_fp8(_ptr(experts), _ptr(q), _ptr(scales), _ptr(offsets), _ptr(slots),
+                                              _ptr(source), _ptr(rows), _ptr(row_scales), M, top, G, K, _on(stream))
+    _check(status, "moe_dispatch_fp8")
+
+
+def moe_combine(rows, slots, shares, out, M, top, K, dtype, out_dtype, stream=None) -> None:
+    """out [M,K]: each token's rows, weighted by its shares (None: ones); without
+    shares also the gradient of moe_dispatch's x."""
+    status = (_lib or lib()).moe_combine(_ptr(rows), _ptr(slots), _ptr(shares), _ptr(out), M, top, K, _code(dtype),
+                                         _code(out_dtype), _on(stream))
+    _check(status, "moe_combine")
+
+
+def moe_combine_grad(dout, rows, slots, shares, drows, dshares, M, top, K, dtype, stream=None) -> None:
+    """The gradients of moe_combine's rows (drows, or None; may be rows) and
+    shares (dshares F32, or None: then rows may be None too)."""
+    status = (_lib or lib()).moe_combine_grad(_ptr(dout), _ptr(rows), _ptr(slots), _ptr(shares), _ptr(drows),
+                                              _ptr(dshares), M, top, K, _code(dtype), _on(stream))
+    _check(status, "moe_combine_grad")
+
+
+def layernorm(x, weight, bias, y, M, K, dtype, eps=1e-5, residual=None, sum_out=None, mean=None, rstd=None,
+              stream=None) -> None:
+    """Residual addition and layer norm: y [M,K]; sum_out (x + residual; may be x
+    or residual), mean and rstd (F32 [M]) where given; bias may be None."""
+    status = (_lib or lib()).layernorm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(sum_out), _ptr(y),
+                                       _ptr(mean), _ptr(rstd), M, K, eps, _code(dtype), _on(stream))
+    _check(status, "layernorm")
+
+
+def layernorm_grad_workspace_bytes(M, K) -> int:
+    return int(lib().layernorm_grad_workspace_bytes(M, K))
+
+
+def layernorm_grad(dy, h, weight, mean, rstd, dx, dweight, dbias, workspace, workspace_bytes, M, K, dtype, dsum=None,
+                   stream=None) -> None:
+    """The gradients of layernorm's input (dx; may be dy or dsum, the gradient
+    that reaches the sum besides), weight and bias (F32 [K]; dbias may be None)."""
+    status = (_lib or lib()).layernorm_grad(_ptr(dy), _ptr(h), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dsum),
+                                            _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(workspace), workspace_bytes,
+                                            M, K, _code(dtype), _on(stream))
+    _check(status, "layernorm_grad")
+
+
+class GradList:
+    """The addresses, sizes and types of a model's gradients, as grad_norm and
+    grad_clip take them.  Keeps the tensors alive; made once, used every step."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        n = max(len(self.tensors), 1)
+        for t in self.tensors:
+            if not t.is_contiguous():
+                raise ValueError("a gradient is not contiguous")
+        self.pointers = pointer_array(self.tensors)
+        self.sizes = (ctypes.c_int64 * n)(*(t.numel() for t in self.tensors))
+        self.dtypes = (ctypes.c_int * n)(*(dtype_code(t.dtype) for t in self.tensors))
+        self.count = len(self.tensors)
+        self.kinds = tuple(self.sizes), tuple(self.dtypes)
+
+
+def grad_list(tensors) -> GradList:
+    return tensors if isinstance(tensors, GradList) else GradList(tensors)
+
+
+def grad_norm_workspace_bytes() -> int:
+    return int(lib().grad_norm_workspace_bytes())
+
+
+def grad_norm(grads, norm, workspace, workspace_bytes, stream=None) -> None:
+    """norm (F32, one value): the norm of all gradients (a grad_list, or tensors)."""
+    g = grad_list(grads)
+    status = (_lib or lib()).grad_norm(g.pointers, g.sizes, g.dtypes, g.count, _ptr(norm), _ptr(workspace),
+                                       workspace_bytes, _on(stream))
+    _check(status, "grad_norm")
+
+
+def grad_clip(grads, max_norm, norm, workspace, workspace_bytes, out=None, stream=None) -> None:
+    """The gradients scaled to a norm of at most max_norm, in place or into `out`
+    (a grad_list or tensors of the same sizes and types); norm as grad_norm's."""
+    g = grad_list(grads)
+    o = None if out is None else grad_list(out)
+    if o is not None and (o.count != g.count or o.kinds != g.kinds):
+        raise ValueError("out differs from the gradients in size or type")
+    status = (_lib or lib()).grad_clip(g.pointers, o and o.pointers, g.sizes, g.dtypes, g.count, max_norm, _ptr(norm),
+                                       _ptr(workspace), workspace_bytes, _on(stream))
+    _check(status, "grad_clip")

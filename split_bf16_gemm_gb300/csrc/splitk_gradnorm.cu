@@ -1,0 +1,230 @@
+// splitk_gradnorm.cu -- the norm of all gradients of a model, and the gradients
+// scaled to a largest norm.
+//
+//   norm = sqrt(sum over all tensors and values of g^2)
+//   out  = g f,  f = min(1, max_norm / norm), rounded once
+//
+// The tensors are cut into chunks of 8192 values that a persistent grid takes in
+// turn.  A thread squares 32 values of a chunk in F32 (four in flight), adds that
+// to its sum in F64, and a block writes one F64 part: at most 1216 of them, which
+// every block of the second launch adds in the same order.  Squares that F32 does
+// not hold (of gradients beyond 2^50 or all below 2^-40) are taken again of the
+// values times a power of two.  The second launch goes through the chunks backwards,
+// so that it finds the last ones of the first in L2.
+//
+// The tensors' addresses go into the kernels as parameters: no copy to the device
+// before the launch, nothing to keep for a captured graph.  Bound by memory: the
+// gradients read once for the norm, read again and written for the scaling.
+
+#include <math.h>
+
+#include "ptx.cuh"
+#include "rows.cuh"
+#include "splitk_internal.h"
+
+namespace splitk {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVecs = 4;                                // vectors of a chunk a thread takes
+constexpr int kChunk = kThreads * kVecs * kVec;
+
+template <int N>
+struct Table {
+    const void *g[N];
+    void *out[N];
+    int64_t size[N];
+    int first[N + 1];         // chunks before the tensor
+    uint8_t dtype[N];
+    int count;
+};
+
+// The sum of `v` over the block, in every thread.
+__device__ __forceinline__ double block_sum(double v, double *part)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = 0.;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) v += part[w];
+    return v;
+}
+
+// The squares of a thread's values of a chunk that starts at g, n values of the
+// tensor left there.
+template <typename T>
+__device__ __forceinline__ double squares(const T *g, int64_t n)
+{
+    float x[kVecs][kVec];
+    if (n >= kChunk) {
+        Pack<T> p[kVecs];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) p[i] = *reinterpret_cast<const Pack<T> *>(g + (i * kThreads + threadIdx.x) * kVec);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) unpack(p[i], x[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int at = (i * kThreads + threadIdx.x) * kVec;
+            if (at + kVec <= n) {
+                unpack(*reinterpret_cast<const Pack<T> *>(g + at), x[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) x[i][j] = at + j < n ? static_cast<float>(g[at + j]) : 0.f;
+            }
+        }
+    }
+    float s[kVecs] = {};
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) s[i] = fmaf(x[i][j], x[i][j], s[i]);
+    const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+    if (__builtin_expect(sum >= 0x1p-80f && sum <= 0x1p120f, true)) return static_cast<double>(sum);
+    const float scale = sum < 1.f ? 0x1p100f : 0x1p-80f;
+    float again = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) again = fmaf(x[i][j] * scale, x[i][j] * scale, again);
+    return static_cast<double>(again) * (sum < 1.f ? 0x1p-200 : 0x1p160);
+}
+
+template <typename T>
+__device__ __forceinline__ void scaled(const T *g, T *out, int64_t n, float f)
+{
+    if (n >= kChunk) {
+        Pack<T> p[kVecs];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) p[i] = *reinterpret_cast<const Pack<T> *>(g + (i * kThreads + threadIdx.x) * kVec);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            float x[kVec];
+            unpack(p[i], x);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) x[j] *= f;
+            pack(x, p[i]);
+            *reinterpret_cast<Pack<T> *>(out + (i * kThreads + threadIdx.x) * kVec) = p[i];
+        }
+        return;
+    }
+    for (int at = threadIdx.x; at < n; at += kThreads) out[at] = static_cast<T>(static_cast<float>(g[at]) * f);
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<N> t, double *parts, int more)
+{
+    __shared__ double part[kThreads / 32];
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    double sum = 0.;
+    int at = 0;
+    for (int c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
+        while (c >= t.first[at + 1]) ++at;
+        const int64_t from = static_cast<int64_t>(c - t.first[at]) * kChunk, n = t.size[at] - from;
+        sum += t.dtype[at] == 0   ? squares(static_cast<const float *>(t.g[at]) + from, n)
+               : t.dtype[at] == 1 ? squares(static_cast<const __half *>(t.g[at]) + from, n)
+                                  : squares(static_cast<const __nv_bfloat16 *>(t.g[at]) + from, n);
+    }
+    sum = block_sum(sum, part);
+    if (threadIdx.x == 0) parts[blockIdx.x] = more ? parts[blockIdx.x] + sum : sum;
+}
+
+// The norm from the blocks' parts, in every thread.
+__device__ __forceinline__ double norm_of(const double *parts, int blocks, double *part)
+{
+    double sum = 0.;
+    for (int i = threadIdx.x; i < blocks; i += kThreads) sum += parts[i];
+    return sqrt(block_sum(sum, part));
+}
+
+__global__ void __launch_bounds__(kThreads) finish_kernel(const double *parts, int blocks, float *norm)
+{
+    __shared__ double part[kThreads / 32];
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    const double n = norm_of(parts, blocks, part);
+    if (threadIdx.x == 0) *norm = static_cast<float>(n);
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Table<N> t, const double *parts, int blocks,
+                                                        float max_norm, float *norm)
+{
+    __shared__ double part[kThreads / 32];
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    const double n = norm_of(parts, blocks, part);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(n);
+    const float f = n > max_norm ? static_cast<float>(max_norm / n) : isnan(n) ? static_cast<float>(n) : 1.f;
+    int at = t.count - 1;
+    for (int c = t.first[t.count] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
+        while (c < t.first[at]) --at;
+        if (f == 1.f && t.out[at] == t.g[at]) continue;   // in place, and nothing to change
+        const int64_t from = static_cast<int64_t>(c - t.first[at]) * kChunk, left = t.size[at] - from;
+        if (t.dtype[at] == 0) scaled(static_cast<const float *>(t.g[at]) + from, static_cast<float *>(t.out[at]) + from, left, f);
+        else if (t.dtype[at] == 1) scaled(static_cast<const __half *>(t.g[at]) + from, static_cast<__half *>(t.out[at]) + from, left, f);
+        else scaled(static_cast<const __nv_bfloat16 *>(t.g[at]) + from, static_cast<__nv_bfloat16 *>(t.out[at]) + from, left, f);
+    }
+}
+
+constexpr int kMostTensors = 512;   // of one launch
+
+int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
+
+template <int N>
+cudaError_t launch(const GradNormProblem &p, int64_t begin, int64_t end, int blocks, bool clip, cudaStream_t stream)
+{
+    Table<N> t;
+    t.count = static_cast<int>(end - begin);
+    t.first[0] = 0;
+    for (int i = 0; i < t.count; ++i) {
+        t.g[i] = p.grads[begin + i];
+        t.out[i] = p.out ? p.out[begin + i] : nullptr;
+        t.size[i] = p.sizes[begin + i];
+        t.dtype[i] = static_cast<uint8_t>(p.dtypes[begin + i]);
+        t.first[i + 1] = t.first[i] + static_cast<int>(chunks_of(t.size[i]));
+    }
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config(static_cast<unsigned>(blocks), kThreads, stream, &attr);
+    if (clip)
+        return note_error(cudaLaunchKernelEx(&cfg, clip_kernel<N>, t, static_cast<const double *>(p.parts), blocks, p.max_norm,
+                                             begin == 0 ? p.norm : static_cast<float *>(nullptr)),
+                          "clip_kernel launch");
+    return note_error(cudaLaunchKernelEx(&cfg, norm_kernel<N>, t, p.parts, begin ? 1 : 0), "norm_kernel launch");
+}
+
+}  // namespace
+
+int64_t grad_norm_chunk() { return kChunk; }
+
+// At most kMostTensors tensors to a launch; a few take the kernel with the short table.
+cudaError_t launch_grad_norm(const GradNormProblem &p, cudaStream_t stream)
+{
+    constexpr int kFew = 32;
+    int64_t most = 1;
+    for (int64_t begin = 0; begin < p.count; begin += kMostTensors) {
+        int64_t chunks = 0;
+        for (int64_t i = begin; i < p.count && i < begin + kMostTensors; ++i) chunks += chunks_of(p.sizes[i]);
+        most = most > chunks ? most : chunks;
+    }
+    const int blocks = static_cast<int>(most < kGradNormParts ? most : kGradNormParts);
+    for (int pass = 0; pass < (p.out ? 2 : 1); ++pass) {
+        int64_t begin = 0;
+        do {   // (no tensors: one launch that finds nothing)
+            const int64_t end = begin + kMostTensors < p.count ? begin + kMostTensors : p.count;
+            const cudaError_t e = end - begin <= kFew ? launch<kFew>(p, begin, end, blocks, pass == 1, stream)
+                                                      : launch<kMostTensors>(p, begin, end, blocks, pass == 1, stream);
+            if (e != cudaSuccess) return e;
+            begin = end;
+        } while (begin < p.count);
+    }
+    if (p.out) return cudaSuccess;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config(1, kThreads, stream, &attr);
+    return note_error(cudaLaunchKernelEx(&cfg, finish_kernel, static_cast<const double *>(p.parts), blocks, p.norm), "finish_kernel launch");
+}
+
+}  // namespace splitk

@@ -155,6 +155,81 @@ cudaError_t launch_rows_fp8(const RowsProblem &p, cudaStream_t stream);
 cudaError_t launch_prepare_fp8(const void *B, void *q, float *scales, int64_t G, int64_t N, int64_t K, int dtype,
                                cudaStream_t stream);
 
+// The router's choice (splitk_route.cu): `top` experts of G for each of M tokens
+// and their shares; with dlogits the logits' gradient, `shares` being the shares'.
+struct RouteProblem {
+    const void *logits;      // [M,G] of dtype
+    int *experts;            // [M,top]
+    float *shares;           // [M,top]
+    void *dlogits;           // [M,G] of dtype, or nullptr
+    int64_t M, G, top;
+    int chosen_only, dtype;
+};
+cudaError_t launch_route(const RouteProblem &p, cudaStream_t stream);
+
+// Entries sorted by expert, and (x != nullptr) the tokens' rows with them
+// (splitk_rows.cu): row_bytes bytes a row, a multiple of 16, and scale_blocks F32
+// scales where there are any.
+struct DispatchProblem {
+    const int *experts;      // [M,top]
+    const void *x;
+    const float *scales;     // or nullptr
+    int *offsets, *slots, *source;   // [G+1], [M,top], [M*top] or nullptr
+    void *rows;
+    float *row_scales;
+    int64_t M, top, G, row_bytes, scale_blocks;
+};
+cudaError_t launch_dispatch(const DispatchProblem &p, cudaStream_t stream);
+// Rows [M*top,K] back to their tokens, weighted; with dout the gradients.
+struct CombineProblem {
+    const void *rows, *dout;
+    const int *slots;
+    const float *shares;     // or nullptr: ones
+    void *out, *drows;
+    float *dshares;
+    int64_t M, top, K;
+    int dtype, out_dtype;
+};
+cudaError_t launch_combine(const CombineProblem &p, cudaStream_t stream);
+
+// Layer norm and its gradients (splitk_layernorm.cu).
+struct LayerNormProblem {
+    const void *x, *residual, *weight, *bias;   // residual and bias may be nullptr
+    void *sum, *y;                              // sum may be nullptr
+    float *mean, *rstd;                         // may be nullptr
+    int64_t M, K;
+    float eps;
+    int dtype;
+};
+cudaError_t launch_layernorm(const LayerNormProblem &p, cudaStream_t stream);
+struct LayerNormGradProblem {
+    const void *dy, *h, *weight, *dsum;         // dsum may be nullptr
+    const float *mean, *rstd;
+    void *dx;
+    float *dweight, *dbias;                     // dbias may be nullptr
+    float *parts;                               // [layernorm_grad_parts()][2][K]
+    int64_t M, K;
+    int dtype;
+};
+int64_t layernorm_grad_parts(int64_t M, int64_t K);
+cudaError_t launch_layernorm_grad(const LayerNormGradProblem &p, cudaStream_t stream);
+
+// The norm of `count` tensors, and (out != nullptr) the tensors scaled to max_norm
+// (splitk_gradnorm.cu).  The arrays are the host's.
+constexpr int kGradNormParts = 8 * 152;         // blocks of the persistent grid
+struct GradNormProblem {
+    const void *const *grads;
+    void *const *out;
+    const int64_t *sizes;
+    const int *dtypes;
+    int64_t count;
+    float max_norm;
+    float *norm;
+    double *parts;                              // [kGradNormParts]
+};
+int64_t grad_norm_chunk();                      // values that a block takes at a time
+cudaError_t launch_grad_norm(const GradNormProblem &p, cudaStream_t stream);
+
 // The driver's cuTensorMapEncodeTiled (PFN_cuTensorMapEncodeTiled_v12000), or nullptr.
 void *tensor_map_encoder();
 
