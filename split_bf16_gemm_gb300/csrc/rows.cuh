@@ -54,12 +54,10 @@ __device__ __forceinline__ void pack(const float (&v)[kVec], Pack<__half> &p)
 }
 __device__ __forceinline__ void unpack(const Pack<__nv_bfloat16> &p, float (&v)[kVec])
 {
-    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&p.a);
+    // a BF16 is the upper half of its F32
+    const uint32_t u[4] = {p.a.x, p.a.y, p.a.z, p.a.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __bfloat1622float2(h[i]);
-        v[2 * i] = f.x, v[2 * i + 1] = f.y;
-    }
+    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
 }
 __device__ __forceinline__ void pack(const float (&v)[kVec], Pack<__nv_bfloat16> &p)
 {

@@ -36,27 +36,49 @@ struct NormArgs {
     float eps;
 };
 
-// The sum over a block's threads, the same in each.  `part` is free again after the
+template <typename T>
+__device__ __forceinline__ void unpack(const Pack<T> &p, float2 (&v)[kVec / 2])
+{
+    float f[kVec];
+    unpack(p, f);
+#pragma unroll
+    for (int j = 0; j < kVec / 2; ++j) v[j] = make_float2(f[2 * j], f[2 * j + 1]);
+}
+template <typename T>
+__device__ __forceinline__ Pack<T> packed(const float2 (&v)[kVec / 2])
+{
+    float f[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec / 2; ++j) f[2 * j] = v[j].x, f[2 * j + 1] = v[j].y;
+    Pack<T> p;
+    pack(f, p);
+    return p;
+}
+
+// The sums of x and of y over a warp: of x in lanes 0-15, of y in lanes 16-31, 5
+// exchanges for both (exchanges and shared memory's copies share a pipe).
+__device__ __forceinline__ float lanes_sum(float2 v)
+{
+    const bool upper = threadIdx.x & 16;
+    float s = (upper ? v.y : v.x) + __shfl_xor_sync(0xffffffffu, upper ? v.x : v.y, 16);
+#pragma unroll
+    for (int d = 8; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    return s;
+}
+// The sums over a block's threads, the same in each.  `part` is free again after the
 // next barrier.
-template <int THREADS, int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float *part)
+template <int THREADS>
+__device__ __forceinline__ float2 block_sum(float2 v, float2 *part)
 {
     constexpr int kWarps = THREADS / 32;
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int d = 16; d; d >>= 1) v[n] += __shfl_xor_sync(0xffffffffu, v[n], d);
-    if (threadIdx.x % 32 == 0) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) part[n * kWarps + threadIdx.x / 32] = v[n];
-    }
+    const int lane = threadIdx.x % 32;
+    const float s = lanes_sum(v);
+    if (lane % 16 == 0) reinterpret_cast<float *>(part + threadIdx.x / 32)[lane / 16] = s;
     __syncthreads();
+    v = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        v[n] = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) v[n] += part[n * kWarps + w];
-    }
+    for (int w = 0; w < kWarps; ++w) v = __fadd2_rn(v, part[w]);
+    return v;
 }
 
 // Whether F32 holds the squares that v + eps is made of.
@@ -66,103 +88,118 @@ __device__ __forceinline__ bool in_range(float v) { return v >= 0x1p-80f && v <=
 template <typename T, int THREADS, int VPT, bool LONG>
 __global__ void __launch_bounds__(THREADS) layernorm_kernel(const NormArgs a)
 {
-    constexpr int kWarps = THREADS / 32;
-    __shared__ float part[4][2 * kWarps];
+    constexpr int kWarps = THREADS / 32, kPairs = kVec / 2;
+    __shared__ float2 part[4][kWarps];
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     const int64_t row = blockIdx.x;
-    const size_t at = static_cast<size_t>(row) * a.K;
-    const T *const x = static_cast<const T *>(a.x) + at;
-    const T *const res = a.residual ? static_cast<const T *>(a.residual) + at : nullptr;
-    T *const sum = a.sum ? static_cast<T *>(a.sum) + at : nullptr;
-    T *const y = static_cast<T *>(a.y) + at;
-    float h[VPT][kVec];
+    const size_t at = static_cast<size_t>(row) * a.vecs;
+    const Pack<T> *const x = static_cast<const Pack<T> *>(a.x) + at;
+    const Pack<T> *const res = a.residual ? static_cast<const Pack<T> *>(a.residual) + at : nullptr;
+    Pack<T> *const sum = a.sum ? static_cast<Pack<T> *>(a.sum) + at : nullptr;
+    float2 h[VPT][kPairs];
     const int turns = LONG ? (a.vecs + THREADS * VPT - 1) / (THREADS * VPT) : 1;
+    const float inv = 1.f / static_cast<float>(a.K);
 
     // h of the turn's vectors; `again`: a later reading of a long row, from `sum`
     // where there is one (x or the residual may be the same memory)
     auto load = [&](int turn, bool again) {
+        Pack<T> px[VPT], pr[VPT];
+        const bool add = res && !(again && sum);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = (turn * VPT + i) * THREADS + threadIdx.x;
+            if (v >= a.vecs) continue;
+            px[i] = (again && sum ? sum : x)[v];
+            if (add) pr[i] = res[v];
+        }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = (turn * VPT + i) * THREADS + threadIdx.x;
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) h[i][j] = 0.f;
+            for (int j = 0; j < kPairs; ++j) h[i][j] = make_float2(0.f, 0.f);
             if (v >= a.vecs) continue;
-            Pack<T> p = *reinterpret_cast<const Pack<T> *>((again && sum ? sum : x) + static_cast<size_t>(v) * kVec);
-            unpack(p, h[i]);
-            if (res && !(again && sum)) {
-                float r[kVec];
-                unpack(*reinterpret_cast<const Pack<T> *>(res + static_cast<size_t>(v) * kVec), r);
+            unpack(px[i], h[i]);
+            if (add) {
+                float2 r[kPairs];
+                unpack(pr[i], r);
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) h[i][j] += r[j];
-                pack(h[i], p);
-                unpack(p, h[i]);
+                for (int j = 0; j < kPairs; ++j) h[i][j] = __fadd2_rn(h[i][j], r[j]);
+                px[i] = packed<T>(h[i]);
+                unpack(px[i], h[i]);
             }
-            if (sum && !again) *reinterpret_cast<Pack<T> *>(sum + static_cast<size_t>(v) * kVec) = p;
+            if (sum && !again) sum[v] = px[i];
         }
     };
-    // mean and 1 / sqrt of the row times `scale`, (h - mean) times `wide` in the squares
-    float mean, rest, rstd;
-    auto moments = [&](float scale, float wide, float *p, bool again) {
-        float s[1] = {0.f};
+    // Mean (and the mean of what is left of it, `rest`) and the root.  scaled: of the
+    // row times `scale`, the deviations times `wide`.
+    float mean, rest, rstd, scale = 1.f, wide = 1.f;
+    auto moments = [&](const bool scaled, float2 *p) {
+        float2 s = {0.f, 0.f}, q = {0.f, 0.f};
         for (int turn = 0; turn < turns; ++turn) {
-            if (LONG || !again) load(turn, again);
+            if (LONG || !scaled) load(turn, scaled);
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) s[0] += h[i][j] * scale;
+                for (int j = 0; j < kPairs; ++j)
+                    s = scaled ? __ffma2_rn(h[i][j], make_float2(scale, scale), s) : __fadd2_rn(s, h[i][j]);
         }
-        block_sum<THREADS>(s, p);
-        mean = s[0] / static_cast<float>(a.K);
-        float q[2] = {0.f, 0.f};
+        mean = block_sum<THREADS>(make_float2(s.x + s.y, 0.f), p).x * inv;
+        s = {0.f, 0.f};
         for (int turn = 0; turn < turns; ++turn) {
             if (LONG) load(turn, true);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 if ((turn * VPT + i) * THREADS + static_cast<int>(threadIdx.x) >= a.vecs) continue;
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    const float d = fmaf(h[i][j], scale, -mean) * wide;
-                    q[0] += d;
-                    q[1] = fmaf(d, d, q[1]);
+                for (int j = 0; j < kPairs; ++j) {
+                    const float2 off = make_float2(-mean, -mean);
+                    const float2 d = scaled ? __fmul2_rn(__ffma2_rn(h[i][j], make_float2(scale, scale), off), make_float2(wide, wide))
+                                            : __fadd2_rn(h[i][j], off);
+                    s = __fadd2_rn(s, d);
+                    q = __ffma2_rn(d, d, q);
                 }
             }
         }
-        block_sum<THREADS>(q, p + 2 * kWarps);
-        rest = q[0] / static_cast<float>(a.K);
-        float var = q[1] / static_cast<float>(a.K) - rest * rest;
-        var = (var < 0.f ? 0.f : var) + a.eps * (scale * wide) * (scale * wide);   // (keeps a NaN)
+        const float2 t = block_sum<THREADS>(make_float2(s.x + s.y, q.x + q.y), p + kWarps);
+        rest = t.x * inv;
+        float var = t.y * inv - rest * rest;
+        var = (var < 0.f ? 0.f : var) + (scaled ? a.eps * (scale * wide) * (scale * wide) : a.eps);   // (keeps a NaN)
         rstd = rsqrtf(var);
         return var;
     };
-    float scale = 1.f, wide = 1.f;
-    const float var = moments(1.f, 1.f, part[0], false);
-    if (__builtin_expect(!in_range(var), false)) {
+    auto outputs = [&](const bool scaled) {
+        const float2 off = make_float2(-mean, -mean), less = make_float2(-rest, -rest), r = make_float2(rstd, rstd);
+        for (int turn = 0; turn < turns; ++turn) {
+            if (LONG) load(turn, true);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int v = (turn * VPT + i) * THREADS + threadIdx.x;
+                if (v >= a.vecs) continue;
+                float2 w[kPairs], b[kPairs] = {};
+                unpack(static_cast<const Pack<T> *>(a.weight)[v], w);
+                if (a.bias) unpack(static_cast<const Pack<T> *>(a.bias)[v], b);
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) {
+                    float2 d = scaled ? __fmul2_rn(__ffma2_rn(h[i][j], make_float2(scale, scale), off), make_float2(wide, wide))
+                                      : __fadd2_rn(h[i][j], off);
+                    d = __fmul2_rn(__fadd2_rn(d, less), r);
+                    b[j] = __ffma2_rn(d, w[j], b[j]);
+                }
+                (static_cast<Pack<T> *>(a.y) + at)[v] = packed<T>(b);
+            }
+        }
+    };
+    const float var = moments(false, part[0]);
+    if (__builtin_expect(in_range(var), true)) {
+        outputs(false);
+    } else {
         // deviations whose squares F32 does not hold: the row times a power of two,
         // which the norm cancels
         if (var < 1.f) wide = 0x1p100f;
         else scale = 0x1p-80f;
-        moments(scale, wide, part[2], true);
-    }
-    for (int turn = 0; turn < turns; ++turn) {
-        if (LONG) load(turn, true);
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = (turn * VPT + i) * THREADS + threadIdx.x;
-            if (v >= a.vecs) continue;
-            float w[kVec], b[kVec] = {};
-            unpack(*reinterpret_cast<const Pack<T> *>(static_cast<const T *>(a.weight) + static_cast<size_t>(v) * kVec), w);
-            if (a.bias) unpack(*reinterpret_cast<const Pack<T> *>(static_cast<const T *>(a.bias) + static_cast<size_t>(v) * kVec), b);
-            float o[kVec];
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                const float d = fmaf(h[i][j], scale, -mean) * wide - rest;
-                o[j] = fmaf(d * rstd, w[j], b[j]);
-            }
-            Pack<T> p;
-            pack(o, p);
-            *reinterpret_cast<Pack<T> *>(y + static_cast<size_t>(v) * kVec) = p;
-        }
+        moments(true, part[2]);
+        outputs(true);
     }
     if (threadIdx.x == 0) {
         if (a.mean) a.mean[row] = (mean + rest / wide) / scale;
@@ -187,7 +224,7 @@ template <typename T, int THREADS, int VPT>
 __global__ void __launch_bounds__(THREADS) layernorm_grad_kernel(const NormGradArgs a)
 {
     constexpr int kWarps = THREADS / 32;
-    __shared__ float part[2][2 * kWarps];
+    __shared__ float2 part[2][kWarps];
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     float dw[VPT][kVec] = {}, db[VPT][kVec] = {};
@@ -215,8 +252,8 @@ __global__ void __launch_bounds__(THREADS) layernorm_grad_kernel(const NormGradA
                 s[1] = fmaf(g[i][j], x[i][j], s[1]);
             }
         }
-        block_sum<THREADS>(s, part[turn]);
-        const float mg = s[0] / static_cast<float>(a.K), mgx = s[1] / static_cast<float>(a.K);
+        const float2 t = block_sum<THREADS>(make_float2(s[0], s[1]), part[turn]);
+        const float mg = t.x / static_cast<float>(a.K), mgx = t.y / static_cast<float>(a.K);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = i * THREADS + threadIdx.x;
@@ -244,11 +281,154 @@ __global__ void __launch_bounds__(THREADS) layernorm_grad_kernel(const NormGradA
     }
 }
 
+// ---- rows of up to 8192 values: copies into shared memory ahead of the sums
+
+constexpr int kRingThreads = 1024;
+constexpr int kSmCount = 152;
+
+// Rows in flight for each thread: what 192 KB of shared memory hold of dy, h and dsum.
+template <typename T>
+constexpr int ring_stages()
+{
+    return sizeof(T) == 2 ? 4 : 2;
+}
+
+template <typename T>
+constexpr size_t ring_bytes()
+{
+    return static_cast<size_t>(ring_stages<T>()) * 3 * kRingThreads * sizeof(Pack<T>);
+}
+
+template <typename T>
+__device__ __forceinline__ void copy_ahead(Pack<T> *dst, const void *src)
+{
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(Pack<T>) / 16); ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst) + 16u * i),
+                     "l"(reinterpret_cast<uint64_t>(src) + 16u * i)
+                     : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// The sums of a row's TPR threads, the same in each.
+template <int TPR>
+__device__ __forceinline__ float2 row_sum(float2 v, float2 *part, int group)
+{
+    float s = lanes_sum(v);
+    if constexpr (TPR > 32) {
+        constexpr int kWarps = TPR / 32;
+        const int lane = threadIdx.x % 32, warp = threadIdx.x % TPR / 32;
+        if (lane % 16 == 0) reinterpret_cast<float *>(part + warp)[lane / 16] = s;
+        if constexpr (TPR == kRingThreads) __syncthreads();
+        else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
+        s = lanes_sum(lane < kWarps ? part[lane] : make_float2(0.f, 0.f));
+    }
+    return make_float2(__shfl_sync(0xffffffffu, s, 0), __shfl_sync(0xffffffffu, s, 16));
+}
+
+// TPR threads a row, one vector each; groups of them take rows in turn.  A thread
+// copies its own vectors of the next rows into its own places of shared memory, and
+// reads them again when it comes to the row: no barrier but the row's sum.
+template <typename T, int TPR>
+__global__ void __launch_bounds__(kRingThreads, 1) layernorm_grad_ring_kernel(const NormGradArgs a)
+{
+    constexpr int kGroups = kRingThreads / TPR, kStages = ring_stages<T>();
+    extern __shared__ __align__(16) uint8_t ring_raw[];
+    __shared__ float2 part[2][kRingThreads / 32];
+    Pack<T> *const ring = reinterpret_cast<Pack<T> *>(ring_raw) + threadIdx.x;   // [stage][tensor][thread]
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    const int group = threadIdx.x / TPR, v = threadIdx.x % TPR;
+    const bool in = v < a.vecs;
+    // rows are counted in 32 bits (M <= 2^22), their addresses by a running offset
+    const int M = static_cast<int>(a.M), step = static_cast<int>(gridDim.x) * kGroups, first = static_cast<int>(blockIdx.x) * kGroups + group;
+    const size_t stride = static_cast<size_t>(step) * a.vecs * sizeof(Pack<T>);
+    size_t at = (static_cast<size_t>(first) * a.vecs + v) * sizeof(Pack<T>);
+    Pack<T> weight;
+    if (in) weight = static_cast<const Pack<T> *>(a.weight)[v];
+    auto ahead = [&](bool there, size_t from, int stage) {
+        if (in && there) {
+            Pack<T> *const to = ring + stage * 3 * kRingThreads;
+            copy_ahead(to, static_cast<const uint8_t *>(a.dy) + from);
+            copy_ahead(to + kRingThreads, static_cast<const uint8_t *>(a.h) + from);
+            if (a.dsum) copy_ahead(to + 2 * kRingThreads, static_cast<const uint8_t *>(a.dsum) + from);
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) ahead(first + s * step < M, at + s * stride, s);
+    float2 dw[kVec / 2] = {}, db[kVec / 2] = {};
+    float mean = 0.f, rstd = 0.f;
+    if (first < M) mean = a.mean[first], rstd = a.rstd[first];
+    int stage = 0, turn = 0;
+    const float inv = 1.f / static_cast<float>(a.K);
+    for (int row = first; row < M; row += step, at += stride, turn ^= 1) {
+        copies_wait<kStages - 1>();
+        const float2 half = {0.5f, 0.5f}, off = {-0.5f * mean, -0.5f * mean}, r = {rstd, rstd}, r2 = {2.f * rstd, 2.f * rstd};
+        if (row + step < M) mean = a.mean[row + step], rstd = a.rstd[row + step];
+        const Pack<T> *const from = ring + stage * 3 * kRingThreads;
+        float2 g[kVec / 2], x[kVec / 2], s0 = {0.f, 0.f}, s1 = {0.f, 0.f};
+        if (in) {
+            float2 w[kVec / 2];
+            unpack(from[0], g);
+            unpack(from[kRingThreads], x);
+            unpack(weight, w);
+#pragma unroll
+            for (int j = 0; j < kVec / 2; ++j) {
+                x[j] = __fmul2_rn(__ffma2_rn(half, x[j], off), r2);   // normal_of
+                dw[j] = __ffma2_rn(g[j], x[j], dw[j]);
+                db[j] = __fadd2_rn(db[j], g[j]);
+                g[j] = __fmul2_rn(g[j], w[j]);
+                s0 = __fadd2_rn(s0, g[j]);
+                s1 = __ffma2_rn(g[j], x[j], s1);
+            }
+        }
+        const float2 s = row_sum<TPR>(make_float2(s0.x + s0.y, s1.x + s1.y), part[turn] + group * (TPR / 32), group);
+        if (in) {
+            const float2 mg = {-s.x * inv, -s.x * inv}, mgx = {-s.y * inv, -s.y * inv};
+            float2 o[kVec / 2] = {};
+            if (a.dsum) unpack(from[2 * kRingThreads], o);
+#pragma unroll
+            for (int j = 0; j < kVec / 2; ++j) o[j] = __ffma2_rn(r, __ffma2_rn(x[j], mgx, __fadd2_rn(g[j], mg)), o[j]);
+            *reinterpret_cast<Pack<T> *>(static_cast<uint8_t *>(a.dx) + at) = packed<T>(o);
+        }
+        ahead(row + kStages * step < M, at + kStages * stride, stage);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    copies_wait<0>();
+    float *const to = a.parts + static_cast<size_t>(blockIdx.x) * 2 * a.K;
+    if constexpr (kGroups == 1) {
+        if (in) {
+            *reinterpret_cast<Pack<float> *>(to + v * kVec) = packed<float>(dw);
+            *reinterpret_cast<Pack<float> *>(to + a.K + v * kVec) = packed<float>(db);
+        }
+    } else {
+        // the groups' sums, in their order
+        float *const sums = reinterpret_cast<float *>(ring_raw);   // [group][2][TPR * kVec]
+        __syncthreads();
+        *reinterpret_cast<Pack<float> *>(sums + (group * 2 * TPR + v) * kVec) = packed<float>(dw);
+        *reinterpret_cast<Pack<float> *>(sums + (group * 2 * TPR + TPR + v) * kVec) = packed<float>(db);
+        __syncthreads();
+        for (int c = threadIdx.x; c < 2 * TPR * kVec; c += kRingThreads) {
+            float sum = 0.f;
+#pragma unroll 8
+            for (int i = 0; i < kGroups; ++i) sum += sums[i * 2 * TPR * kVec + c];
+            const int which = c / (TPR * kVec), k = c % (TPR * kVec);
+            if (k < a.K) to[which * a.K + k] = sum;
+        }
+    }
+}
+
 // A row of any length, read twice: its dx.
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS) layernorm_grad_long_kernel(const NormGradArgs a)
 {
-    __shared__ float part[2 * THREADS / 32];
+    __shared__ float2 part[THREADS / 32];
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     const int64_t row = blockIdx.x;
@@ -276,8 +456,8 @@ __global__ void __launch_bounds__(THREADS) layernorm_grad_long_kernel(const Norm
             s[1] = fmaf(g[j], x[j], s[1]);
         }
     }
-    block_sum<THREADS>(s, part);
-    const float mg = s[0] / static_cast<float>(a.K), mgx = s[1] / static_cast<float>(a.K);
+    const float2 t = block_sum<THREADS>(make_float2(s[0], s[1]), part);
+    const float mg = t.x / static_cast<float>(a.K), mgx = t.y / static_cast<float>(a.K);
     for (int v = threadIdx.x; v < a.vecs; v += THREADS) {
         load(v);
         const size_t k = static_cast<size_t>(v) * kVec;
@@ -348,7 +528,9 @@ __global__ void __launch_bounds__(kSumThreads) layernorm_sum_kernel(const float 
 }
 
 constexpr int kLongVecs = 2048;   // vectors of the longest row that a block's registers hold
-constexpr int kMostParts = 304;   // two blocks to each of 152 SMs
+constexpr int kRingVecs = 1024;   // the same for the ring
+
+int ring_row_threads(int64_t vecs) { return vecs <= 32 ? 32 : vecs <= 128 ? 128 : vecs <= 256 ? 256 : vecs <= 512 ? 512 : 1024; }
 
 template <typename T, int THREADS, int VPT, bool LONG = false>
 cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream)
@@ -364,6 +546,7 @@ cudaError_t launch_norm_type(const NormArgs &a, cudaStream_t stream)
     if (a.vecs <= 128) return launch_norm<T, 128, 1>(a, stream);
     if (a.vecs <= 256) return launch_norm<T, 256, 1>(a, stream);
     if (a.vecs <= 512) return launch_norm<T, 256, 2>(a, stream);
+    if (a.vecs <= 768) return launch_norm<T, 256, 3>(a, stream);
     if (a.vecs <= 1024) return launch_norm<T, 256, 4>(a, stream);
     if (a.vecs <= kLongVecs) return launch_norm<T, 512, 4>(a, stream);
     return launch_norm<T, 512, 4, true>(a, stream);
@@ -377,13 +560,31 @@ cudaError_t launch_grad(const NormGradArgs &a, int blocks, cudaStream_t stream)
     return note_error(cudaLaunchKernelEx(&cfg, layernorm_grad_kernel<T, THREADS, VPT>, a), "layernorm_grad_kernel launch");
 }
 
+template <typename T, int TPR>
+cudaError_t launch_ring(const NormGradArgs &a, int blocks, cudaStream_t stream)
+{
+    const cudaError_t e = note_error(cudaFuncSetAttribute(layernorm_grad_ring_kernel<T, TPR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                          static_cast<int>(ring_bytes<T>())),
+                                     "layernorm_grad_ring_kernel shared memory");
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = config(static_cast<unsigned>(blocks), kRingThreads, stream, &attr);
+    cfg.dynamicSmemBytes = ring_bytes<T>();
+    return note_error(cudaLaunchKernelEx(&cfg, layernorm_grad_ring_kernel<T, TPR>, a), "layernorm_grad_ring_kernel launch");
+}
+
 template <typename T>
 cudaError_t launch_grad_type(const NormGradArgs &a, int blocks, cudaStream_t stream)
 {
-    if (a.vecs <= 128) return launch_grad<T, 128, 1>(a, blocks, stream);
-    if (a.vecs <= 256) return launch_grad<T, 256, 1>(a, blocks, stream);
-    if (a.vecs <= 512) return launch_grad<T, 256, 2>(a, blocks, stream);
-    if (a.vecs <= 1024) return launch_grad<T, 512, 2>(a, blocks, stream);
+    if (a.vecs <= kRingVecs) {
+        switch (ring_row_threads(a.vecs)) {
+        case 32: return launch_ring<T, 32>(a, blocks, stream);
+        case 128: return launch_ring<T, 128>(a, blocks, stream);
+        case 256: return launch_ring<T, 256>(a, blocks, stream);
+        case 512: return launch_ring<T, 512>(a, blocks, stream);
+        default: return launch_ring<T, 1024>(a, blocks, stream);
+        }
+    }
     if (a.vecs <= kLongVecs) return launch_grad<T, 512, 4>(a, blocks, stream);
     constexpr int kThreads = 512;
     cudaLaunchAttribute attr;
@@ -408,9 +609,10 @@ cudaError_t launch_layernorm(const LayerNormProblem &p, cudaStream_t stream)
 
 int64_t layernorm_grad_parts(int64_t M, int64_t K)
 {
-    // Long rows have columns enough for the threads: few parts.
-    const int64_t most = K / kVec <= kLongVecs ? kMostParts : 16;
-    return M < most ? M : most;
+    // A block to an SM; long rows have columns enough for the threads: few parts.
+    const int64_t vecs = K / kVec, rows = vecs <= kRingVecs ? kRingThreads / ring_row_threads(vecs) : 1;
+    const int64_t blocks = (M + rows - 1) / rows, most = vecs <= kLongVecs ? kSmCount : 16;
+    return blocks < most ? blocks : most;
 }
 
 cudaError_t launch_layernorm_grad(const LayerNormGradProblem &p, cudaStream_t stream)

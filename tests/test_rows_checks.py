@@ -99,7 +99,7 @@ REFUSED = [
     (norm_grad, dict(K=4), SHAPE), (norm_grad, dict(M=-1), SHAPE), (norm_grad, dict(dt=3), DTYPE), (norm_grad, dict(h=None), NULL),
     (norm_grad, dict(mu=None), NULL), (norm_grad, dict(dw=None), NULL), (norm_grad, dict(ws=None), NULL), (norm_grad, dict(ws=at(9, 8)), ALIGN),
     (norm_grad, dict(dx=at(1)), ALIAS), (norm_grad, dict(dx=at(0, 16)), ALIAS), (norm_grad, dict(dw=at(2)), ALIAS),
-    (norm_grad, dict(db=at(7)), ALIAS), (norm_grad, dict(ws=at(6)), ALIAS), (norm_grad, dict(nb=4 * 2 * 64 * 4 - 1), WORK),
+    (norm_grad, dict(db=at(7)), ALIAS), (norm_grad, dict(ws=at(6)), ALIAS), (norm_grad, dict(nb=2 * 64 * 4 - 1), WORK),
     (total, dict(count=-1), SHAPE), (total, dict(count=65537), SHAPE), (total, dict(n=(8, -1)), SHAPE), (total, dict(n=(8, (1 << 34) + 1)), SHAPE),
     (total, dict(dt=(F32, 3)), DTYPE), (total, dict(g=(at(0), None)), NULL), (total, dict(norm=None), NULL), (total, dict(ws=None), NULL),
     (total, dict(g=(at(0), at(1, 8))), ALIGN), (total, dict(norm=at(4, 2)), ALIGN), (total, dict(norm=at(0, 4)), ALIAS),
@@ -151,7 +151,7 @@ def test_no_tokens_is_no_work(L):
 def test_workspace_sizes(L):
     assert L.layernorm_grad_workspace_bytes(4, 12) == 0
     assert L.layernorm_grad_workspace_bytes(-1, 64) == 0
-    assert L.layernorm_grad_workspace_bytes(4, 64) == 4 * 2 * 64 * 4
+    assert 0 < L.layernorm_grad_workspace_bytes(4, 64) <= 4 * 2 * 64 * 4
     for M, K in ((100000, 64), (100000, 8192), (5, 1 << 20), (1 << 22, 1 << 22)):
         assert 0 < L.layernorm_grad_workspace_bytes(M, K) <= 512 * 2 * K * 4
     assert L.grad_norm_workspace_bytes() > 0
