@@ -105,7 +105,7 @@ int grad_norm_call(const void *const *grads, void *const *out, const int64_t *si
     if (alias) return SPLITK_ERR_ALIAS;
     if (workspace_bytes < grad_norm_workspace_bytes()) return SPLITK_ERR_WORKSPACE;
     if (clip && !(max_norm >= 0.f && std::isfinite(max_norm))) return SPLITK_ERR_CONFIG;
-    const splitk::GradNormProblem p = {grads, clip ? out : nullptr, sizes, dtypes, count, max_norm, norm, static_cast<double *>(workspace)};
+    const splitk::GradNormProblem p = {grads, clip ? out : nullptr, sizes, dtypes, count, max_norm, norm, workspace};
     return cuda_status(splitk::launch_grad_norm(p, static_cast<cudaStream_t>(stream)));
 }
 
@@ -271,7 +271,7 @@ int layernorm_grad(const void *dy, const void *h, const void *weight, const floa
         {dy, h, weight, dsum, mean, rstd, dx, dweight, dbias, static_cast<float *>(workspace), M, K, dtype}, static_cast<cudaStream_t>(stream)));
 }
 
-size_t grad_norm_workspace_bytes(void) { return splitk::kGradNormParts * sizeof(double); }
+size_t grad_norm_workspace_bytes(void) { return splitk::kGradNormParts * 8; }
 
 int grad_norm(const void *const *grads, const int64_t *sizes, const int *dtypes, int64_t count, float *norm, void *workspace,
               size_t workspace_bytes, void *stream)

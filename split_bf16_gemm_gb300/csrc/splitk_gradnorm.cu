@@ -5,12 +5,15 @@
 //   out  = g f,  f = min(1, max_norm / norm), rounded once
 //
 // The tensors are cut into chunks of 8192 values that a persistent grid takes in
-// turn.  A thread squares 32 values of a chunk in F32 (four in flight), adds that
-// to its sum in F64, and a block writes one F64 part: at most 1216 of them, which
-// every block of the second launch adds in the same order.  Squares that F32 does
-// not hold (of gradients beyond 2^50 or all below 2^-40) are taken again of the
-// values times a power of two.  The second launch goes through the chunks backwards,
-// so that it finds the last ones of the first in L2.
+// turn.  A thread squares 32 values of a chunk in F32 (four in flight) and adds that to
+// a sum of two F32 numbers, the second of which holds what the first's roundings lose.
+// A block writes one part, a number and a power of two: at most 1216 of them, which
+// every block of the second launch adds in the same order.  F64 is kept out of the
+// way: this chip does two F64 operations a clock and SM (9 tensors of 1.3 M values
+// 18 us with the parts, the root and the quotient in F64).  Squares that F32 does not
+// hold (of gradients beyond 2^50 or all below 2^-40) are taken again of the values
+// times a power of two.  The second launch goes through the chunks backwards, so that
+// it finds the last ones of the first in L2.
 //
 // The tensors' addresses go into the kernels as parameters: no copy to the device
 // before the launch, nothing to keep for a captured graph.  Bound by memory: the
@@ -39,23 +42,74 @@ struct Table {
     int count;
 };
 
-// The sum of `v` over the block, in every thread.
-__device__ __forceinline__ double block_sum(double v, double *part)
+// A sum of two F32 numbers: what `hi`'s additions lose is in `lo` (D. Knuth, "The Art
+// of Computer Programming", volume 2, 4.2.2, theorem B).
+struct Sum {
+    float hi, lo;
+};
+__device__ __forceinline__ void add(Sum &s, float x)
 {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = 0.;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) v += part[w];
-    return v;
+    const float t = s.hi + x, y = t - s.hi;
+    s.lo += (s.hi - (t - y)) + (x - y);
+    s.hi = t;
 }
 
-// The squares of a thread's values of a chunk that starts at g, n values of the
-// tensor left there.
+__device__ __forceinline__ float value(const Sum &s) { return isfinite(s.hi) ? s.hi + s.lo : s.hi; }
+
+// m 2^e, m in [1, 2) or 0, an infinity or NaN
+struct Part {
+    float m;
+    int e;
+};
+__device__ __forceinline__ Part part_of(double v)
+{
+    const int64_t bits = __double_as_longlong(v);
+    const int e = static_cast<int>(bits >> 52) & 2047;
+    if (e == 0) return {0.f, -1023};                               // (0: no square is that small)
+    if (e == 2047) return {static_cast<float>(v), 1023};
+    return {static_cast<float>(__longlong_as_double((bits & 0xfffffffffffffll) | 0x3ff0000000000000ll)), e - 1023};
+}
+
+// 2^e, 0 below F32's range
+__device__ __forceinline__ float power(int e) { return e < -126 ? 0.f : __int_as_float((e + 127) << 23); }
+
+struct Shared {
+    int e[kThreads / 32];
+    Sum s[kThreads / 32];
+};
+
+// The block's sum of the threads' numbers, the same in every thread: 2^e times the Sum.
+__device__ __forceinline__ Sum block_sum(const Part &p, int &e, Shared &shared)
+{
+    const int warp = threadIdx.x / 32;
+    const int most = __reduce_max_sync(0xffffffffu, p.e);
+    if (threadIdx.x % 32 == 0) shared.e[warp] = most;
+    __syncthreads();
+    e = shared.e[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) e = max(e, shared.e[w]);
+    Sum s = {p.m * power(p.e - e), 0.f};
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        const Sum o = {__shfl_xor_sync(0xffffffffu, s.hi, d), __shfl_xor_sync(0xffffffffu, s.lo, d)};
+        add(s, o.hi);
+        s.lo += o.lo;
+    }
+    if (threadIdx.x % 32 == 0) shared.s[warp] = s;
+    __syncthreads();
+    s = shared.s[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) {
+        add(s, shared.s[w].hi);
+        s.lo += shared.s[w].lo;
+    }
+    return s;
+}
+
+// Adds the squares of a thread's values of a chunk that starts at g, n values of the
+// tensor left there; `far` takes those that F32 does not hold.
 template <typename T>
-__device__ __forceinline__ double squares(const T *g, int64_t n)
+__device__ __forceinline__ void squares(const T *g, int64_t n, Sum &total, double &far)
 {
     float x[kVecs][kVec];
     if (n >= kChunk) {
@@ -82,14 +136,25 @@ __device__ __forceinline__ double squares(const T *g, int64_t n)
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) s[i] = fmaf(x[i][j], x[i][j], s[i]);
     const float sum = (s[0] + s[1]) + (s[2] + s[3]);
-    if (__builtin_expect(sum >= 0x1p-80f && sum <= 0x1p120f, true)) return static_cast<double>(sum);
+    if (__builtin_expect(sum >= 0x1p-80f && sum <= 0x1p90f, true)) {   // (2^27 of them and more are below 2^127)
+        add(total, sum);
+        return;
+    }
+    if (sum == 0.f) {   // zeros, or all below 2^-75: F32 squares none of them
+        bool zeros = true;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) zeros &= x[i][j] == 0.f;
+        if (zeros) return;
+    }
     const float scale = sum < 1.f ? 0x1p100f : 0x1p-80f;
     float again = 0.f;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
 #pragma unroll
         for (int j = 0; j < kVec; ++j) again = fmaf(x[i][j] * scale, x[i][j] * scale, again);
-    return static_cast<double>(again) * (sum < 1.f ? 0x1p-200 : 0x1p160);
+    far += static_cast<double>(again) * (sum < 1.f ? 0x1p-200 : 0x1p160);
 }
 
 template <typename T>
@@ -114,51 +179,80 @@ __device__ __forceinline__ void scaled(const T *g, T *out, int64_t n, float f)
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<N> t, double *parts, int more)
+__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<N> t, Part *parts, int more)
 {
-    __shared__ double part[kThreads / 32];
+    __shared__ Shared shared;
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
-    double sum = 0.;
+    Sum sum = {0.f, 0.f};
+    double far = 0.;
     int at = 0;
     for (int c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
         while (c >= t.first[at + 1]) ++at;
         const int64_t from = static_cast<int64_t>(c - t.first[at]) * kChunk, n = t.size[at] - from;
-        sum += t.dtype[at] == 0   ? squares(static_cast<const float *>(t.g[at]) + from, n)
-               : t.dtype[at] == 1 ? squares(static_cast<const __half *>(t.g[at]) + from, n)
-                                  : squares(static_cast<const __nv_bfloat16 *>(t.g[at]) + from, n);
+        if (t.dtype[at] == 0) squares(static_cast<const float *>(t.g[at]) + from, n, sum, far);
+        else if (t.dtype[at] == 1) squares(static_cast<const __half *>(t.g[at]) + from, n, sum, far);
+        else squares(static_cast<const __nv_bfloat16 *>(t.g[at]) + from, n, sum, far);
     }
-    sum = block_sum(sum, part);
-    if (threadIdx.x == 0) parts[blockIdx.x] = more ? parts[blockIdx.x] + sum : sum;
+    double total = static_cast<double>(sum.hi) + static_cast<double>(sum.lo);
+    if (far != 0.) total += far;
+    if (more && threadIdx.x == 0) total += ldexp(static_cast<double>(parts[blockIdx.x].m), parts[blockIdx.x].e);
+    int e;
+    const Sum s = block_sum(part_of(total), e, shared);
+    if (threadIdx.x == 0) parts[blockIdx.x] = part_of(ldexp(static_cast<double>(s.hi) + (isfinite(s.hi) ? static_cast<double>(s.lo) : 0.), e));
 }
 
-// The norm from the blocks' parts, in every thread.
-__device__ __forceinline__ double norm_of(const double *parts, int blocks, double *part)
+// The norm from the blocks' parts, as root * 2^half, in every thread.
+__device__ __forceinline__ float norm_of(const Part *parts, int blocks, int &half, Shared &shared)
 {
-    double sum = 0.;
-    for (int i = threadIdx.x; i < blocks; i += kThreads) sum += parts[i];
-    return sqrt(block_sum(sum, part));
+    constexpr int kEach = (kGradNormParts + kThreads - 1) / kThreads;
+    Part p[kEach], mine = {0.f, -1023};
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int at = i * kThreads + static_cast<int>(threadIdx.x);
+        p[i] = at < blocks ? parts[at] : Part{0.f, -1023};
+        mine.e = max(mine.e, p[i].e);
+    }
+    Sum s = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) add(s, p[i].m * power(p[i].e - mine.e));
+    mine.m = value(s);
+    int e;
+    s = block_sum(mine, e, shared);
+    const int odd = e & 1;
+    half = (e - odd) / 2;
+    return sqrtf(value(s) * (odd ? 2.f : 1.f));
 }
 
-__global__ void __launch_bounds__(kThreads) finish_kernel(const double *parts, int blocks, float *norm)
+__device__ __forceinline__ float norm_value(float root, int half)
 {
-    __shared__ double part[kThreads / 32];
+    return half > 120 ? root * power(120) * power(min(half - 120, 127)) : half < -120 ? root * power(-120) * power(half + 120) : root * power(half);
+}
+
+__global__ void __launch_bounds__(kThreads) finish_kernel(const Part *parts, int blocks, float *norm)
+{
+    __shared__ Shared shared;
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
-    const double n = norm_of(parts, blocks, part);
-    if (threadIdx.x == 0) *norm = static_cast<float>(n);
+    int half;
+    const float root = norm_of(parts, blocks, half, shared);
+    if (threadIdx.x == 0) *norm = norm_value(root, half);
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Table<N> t, const double *parts, int blocks,
+__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Table<N> t, const Part *parts, int blocks,
                                                         float max_norm, float *norm)
 {
-    __shared__ double part[kThreads / 32];
+    __shared__ Shared shared;
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
-    const double n = norm_of(parts, blocks, part);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(n);
-    const float f = n > max_norm ? static_cast<float>(max_norm / n) : isnan(n) ? static_cast<float>(n) : 1.f;
+    int half;
+    const float root = norm_of(parts, blocks, half, shared);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = norm_value(root, half);
+    // max_norm / norm, by halves of the power: neither has to be in F32's range
+    const int some = -half / 2;
+    const float q = max_norm / root * power(some) * power(-half - some);
+    const float f = isnan(root) ? root : root != 0.f && q < 1.f ? q : 1.f;
     int at = t.count - 1;
     for (int c = t.first[t.count] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
         while (c < t.first[at]) --at;
@@ -190,10 +284,10 @@ cudaError_t launch(const GradNormProblem &p, int64_t begin, int64_t end, int blo
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config(static_cast<unsigned>(blocks), kThreads, stream, &attr);
     if (clip)
-        return note_error(cudaLaunchKernelEx(&cfg, clip_kernel<N>, t, static_cast<const double *>(p.parts), blocks, p.max_norm,
+        return note_error(cudaLaunchKernelEx(&cfg, clip_kernel<N>, t, static_cast<const Part *>(p.parts), blocks, p.max_norm,
                                              begin == 0 ? p.norm : static_cast<float *>(nullptr)),
                           "clip_kernel launch");
-    return note_error(cudaLaunchKernelEx(&cfg, norm_kernel<N>, t, p.parts, begin ? 1 : 0), "norm_kernel launch");
+    return note_error(cudaLaunchKernelEx(&cfg, norm_kernel<N>, t, static_cast<Part *>(p.parts), begin ? 1 : 0), "norm_kernel launch");
 }
 
 }  // namespace
@@ -224,7 +318,7 @@ cudaError_t launch_grad_norm(const GradNormProblem &p, cudaStream_t stream)
     if (p.out) return cudaSuccess;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config(1, kThreads, stream, &attr);
-    return note_error(cudaLaunchKernelEx(&cfg, finish_kernel, static_cast<const double *>(p.parts), blocks, p.norm), "finish_kernel launch");
+    return note_error(cudaLaunchKernelEx(&cfg, finish_kernel, static_cast<const Part *>(p.parts), blocks, p.norm), "finish_kernel launch");
 }
 
 }  // namespace splitk

@@ -225,7 +225,7 @@ struct GradNormProblem {
     int64_t count;
     float max_norm;
     float *norm;
-    double *parts;                              // [kGradNormParts]
+    void *parts;                                // [kGradNormParts], 8 bytes each
 };
 int64_t grad_norm_chunk();                      // values that a block takes at a time
 cudaError_t launch_grad_norm(const GradNormProblem &p, cudaStream_t stream);
