@@ -131,9 +131,10 @@ def lib() -> ctypes.CDLL:
 def _ptr(x) -> int | None:
     if x is None:
         return None
-    if isinstance(x, int):
+    try:
+        return x.data_ptr()
+    except AttributeError:   # an address
         return x
-    return x.data_ptr()
 
 
 def _stream(stream) -> int | None:

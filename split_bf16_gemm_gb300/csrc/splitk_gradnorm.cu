@@ -4,8 +4,8 @@
 //   norm = sqrt(sum over all tensors and values of g^2)
 //   out  = g f,  f = min(1, max_norm / norm), rounded once
 //
-// The tensors are cut into chunks of 8192 values that a persistent grid takes in
-// turn.  A thread squares 32 values of a chunk in F32 (four in flight) and adds that to
+// The tensors are cut into chunks of 8192 values (2048 where there are few) that a persistent grid takes in
+// turn.  A thread squares 32 (8) values of a chunk in F32 (four in flight) and adds that to
 // a sum of two F32 numbers, the second of which holds what the first's roundings lose.
 // A block writes one part, a number and a power of two: at most 1216 of them, which
 // every block of the second launch adds in the same order.  F64 is kept out of the
@@ -29,8 +29,7 @@ namespace splitk {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVecs = 4;                                // vectors of a chunk a thread takes
-constexpr int kChunk = kThreads * kVecs * kVec;
+constexpr int chunk_of(int vecs) { return kThreads * vecs * kVec; }   // values, `vecs` vectors to a thread
 
 template <int N>
 struct Table {
@@ -56,16 +55,25 @@ __device__ __forceinline__ void add(Sum &s, float x)
 
 __device__ __forceinline__ float value(const Sum &s) { return isfinite(s.hi) ? s.hi + s.lo : s.hi; }
 
-// m 2^e, m in [1, 2) or 0, an infinity or NaN
+// m 2^e
 struct Part {
     float m;
     int e;
 };
+constexpr int kNothing = -1023;   // e of a 0
+// (m in [1, 2), or 0, an infinity or NaN)
+__device__ __forceinline__ Part part_of(float v)
+{
+    const int bits = __float_as_int(v), e = bits >> 23 & 255;
+    if (e == 0) return {0.f, kNothing};                            // (no sum is that small)
+    if (e == 255) return {v, 1023};
+    return {__int_as_float((bits & 0x7fffff) | 0x3f800000), e - 127};
+}
 __device__ __forceinline__ Part part_of(double v)
 {
     const int64_t bits = __double_as_longlong(v);
     const int e = static_cast<int>(bits >> 52) & 2047;
-    if (e == 0) return {0.f, -1023};                               // (0: no square is that small)
+    if (e == 0) return {0.f, kNothing};                            // (no square is that small)
     if (e == 2047) return {static_cast<float>(v), 1023};
     return {static_cast<float>(__longlong_as_double((bits & 0xfffffffffffffll) | 0x3ff0000000000000ll)), e - 1023};
 }
@@ -108,11 +116,11 @@ __device__ __forceinline__ Sum block_sum(const Part &p, int &e, Shared &shared)
 
 // Adds the squares of a thread's values of a chunk that starts at g, n values of the
 // tensor left there; `far` takes those that F32 does not hold.
-template <typename T>
+template <int kVecs, typename T>
 __device__ __forceinline__ void squares(const T *g, int64_t n, Sum &total, double &far)
 {
     float x[kVecs][kVec];
-    if (n >= kChunk) {
+    if (n >= chunk_of(kVecs)) {
         Pack<T> p[kVecs];
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) p[i] = *reinterpret_cast<const Pack<T> *>(g + (i * kThreads + threadIdx.x) * kVec);
@@ -135,7 +143,9 @@ __device__ __forceinline__ void squares(const T *g, int64_t n, Sum &total, doubl
     for (int j = 0; j < kVec; ++j)
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) s[i] = fmaf(x[i][j], x[i][j], s[i]);
-    const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+    float sum = s[0];
+#pragma unroll
+    for (int i = 1; i < kVecs; ++i) sum += s[i];
     if (__builtin_expect(sum >= 0x1p-80f && sum <= 0x1p90f, true)) {   // (2^27 of them and more are below 2^127)
         add(total, sum);
         return;
@@ -157,10 +167,10 @@ __device__ __forceinline__ void squares(const T *g, int64_t n, Sum &total, doubl
     far += static_cast<double>(again) * (sum < 1.f ? 0x1p-200 : 0x1p160);
 }
 
-template <typename T>
+template <int kVecs, typename T>
 __device__ __forceinline__ void scaled(const T *g, T *out, int64_t n, float f)
 {
-    if (n >= kChunk) {
+    if (n >= chunk_of(kVecs)) {
         Pack<T> p[kVecs];
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) p[i] = *reinterpret_cast<const Pack<T> *>(g + (i * kThreads + threadIdx.x) * kVec);
@@ -178,7 +188,20 @@ __device__ __forceinline__ void scaled(const T *g, T *out, int64_t n, float f)
     for (int at = threadIdx.x; at < n; at += kThreads) out[at] = static_cast<T>(static_cast<float>(g[at]) * f);
 }
 
+// The tensor that chunk c is of.
 template <int N>
+__device__ __forceinline__ int tensor_of(const Table<N> &t, int c)
+{
+    int lo = 0, hi = t.count - 1;   // the last with first[] <= c
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (t.first[mid] <= c) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+template <int N, int kVecs>
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<N> t, Part *parts, int more)
 {
     __shared__ Shared shared;
@@ -186,31 +209,38 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     ptx::grid_dependency_wait();
     Sum sum = {0.f, 0.f};
     double far = 0.;
-    int at = 0;
+    int at = tensor_of(t, blockIdx.x);
     for (int c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
         while (c >= t.first[at + 1]) ++at;
-        const int64_t from = static_cast<int64_t>(c - t.first[at]) * kChunk, n = t.size[at] - from;
-        if (t.dtype[at] == 0) squares(static_cast<const float *>(t.g[at]) + from, n, sum, far);
-        else if (t.dtype[at] == 1) squares(static_cast<const __half *>(t.g[at]) + from, n, sum, far);
-        else squares(static_cast<const __nv_bfloat16 *>(t.g[at]) + from, n, sum, far);
+        const int64_t from = static_cast<int64_t>(c - t.first[at]) * chunk_of(kVecs), n = t.size[at] - from;
+        if (t.dtype[at] == 0) squares<kVecs>(static_cast<const float *>(t.g[at]) + from, n, sum, far);
+        else if (t.dtype[at] == 1) squares<kVecs>(static_cast<const __half *>(t.g[at]) + from, n, sum, far);
+        else squares<kVecs>(static_cast<const __nv_bfloat16 *>(t.g[at]) + from, n, sum, far);
     }
-    double total = static_cast<double>(sum.hi) + static_cast<double>(sum.lo);
-    if (far != 0.) total += far;
-    if (more && threadIdx.x == 0) total += ldexp(static_cast<double>(parts[blockIdx.x].m), parts[blockIdx.x].e);
+    Part mine = part_of(value(sum));
+    if (__builtin_expect(far != 0., false)) mine = part_of(far + static_cast<double>(value(sum)));
     int e;
-    const Sum s = block_sum(part_of(total), e, shared);
-    if (threadIdx.x == 0) parts[blockIdx.x] = part_of(ldexp(static_cast<double>(s.hi) + (isfinite(s.hi) ? static_cast<double>(s.lo) : 0.), e));
+    const Sum s = block_sum(mine, e, shared);
+    if (threadIdx.x == 0) {
+        Part p = {value(s), e};
+        if (more) {
+            const Part q = parts[blockIdx.x];
+            p.e = max(e, q.e);
+            p.m = p.m * power(e - p.e) + q.m * power(q.e - p.e);
+        }
+        parts[blockIdx.x] = p;
+    }
 }
 
 // The norm from the blocks' parts, as root * 2^half, in every thread.
 __device__ __forceinline__ float norm_of(const Part *parts, int blocks, int &half, Shared &shared)
 {
     constexpr int kEach = (kGradNormParts + kThreads - 1) / kThreads;
-    Part p[kEach], mine = {0.f, -1023};
+    Part p[kEach], mine = {0.f, kNothing};
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int at = i * kThreads + static_cast<int>(threadIdx.x);
-        p[i] = at < blocks ? parts[at] : Part{0.f, -1023};
+        p[i] = at < blocks ? parts[at] : Part{0.f, kNothing};
         mine.e = max(mine.e, p[i].e);
     }
     Sum s = {0.f, 0.f};
@@ -239,7 +269,7 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const Part *parts, int
     if (threadIdx.x == 0) *norm = norm_value(root, half);
 }
 
-template <int N>
+template <int N, int kVecs>
 __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Table<N> t, const Part *parts, int blocks,
                                                         float max_norm, float *norm)
 {
@@ -253,22 +283,23 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
     const int some = -half / 2;
     const float q = max_norm / root * power(some) * power(-half - some);
     const float f = isnan(root) ? root : root != 0.f && q < 1.f ? q : 1.f;
-    int at = t.count - 1;
-    for (int c = t.first[t.count] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
+    const int last = t.first[t.count] - 1 - static_cast<int>(blockIdx.x);
+    int at = tensor_of(t, last);
+    for (int c = last; c >= 0; c -= gridDim.x) {
         while (c < t.first[at]) --at;
         if (f == 1.f && t.out[at] == t.g[at]) continue;   // in place, and nothing to change
-        const int64_t from = static_cast<int64_t>(c - t.first[at]) * kChunk, left = t.size[at] - from;
-        if (t.dtype[at] == 0) scaled(static_cast<const float *>(t.g[at]) + from, static_cast<float *>(t.out[at]) + from, left, f);
-        else if (t.dtype[at] == 1) scaled(static_cast<const __half *>(t.g[at]) + from, static_cast<__half *>(t.out[at]) + from, left, f);
-        else scaled(static_cast<const __nv_bfloat16 *>(t.g[at]) + from, static_cast<__nv_bfloat16 *>(t.out[at]) + from, left, f);
+        const int64_t from = static_cast<int64_t>(c - t.first[at]) * chunk_of(kVecs), left = t.size[at] - from;
+        if (t.dtype[at] == 0) scaled<kVecs>(static_cast<const float *>(t.g[at]) + from, static_cast<float *>(t.out[at]) + from, left, f);
+        else if (t.dtype[at] == 1) scaled<kVecs>(static_cast<const __half *>(t.g[at]) + from, static_cast<__half *>(t.out[at]) + from, left, f);
+        else scaled<kVecs>(static_cast<const __nv_bfloat16 *>(t.g[at]) + from, static_cast<__nv_bfloat16 *>(t.out[at]) + from, left, f);
     }
 }
 
 constexpr int kMostTensors = 512;   // of one launch
 
-int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
+int64_t chunks_of(int64_t n, int vecs) { return (n + chunk_of(vecs) - 1) / chunk_of(vecs); }
 
-template <int N>
+template <int N, int kVecs>
 cudaError_t launch(const GradNormProblem &p, int64_t begin, int64_t end, int blocks, bool clip, cudaStream_t stream)
 {
     Table<N> t;
@@ -279,38 +310,45 @@ cudaError_t launch(const GradNormProblem &p, int64_t begin, int64_t end, int blo
         t.out[i] = p.out ? p.out[begin + i] : nullptr;
         t.size[i] = p.sizes[begin + i];
         t.dtype[i] = static_cast<uint8_t>(p.dtypes[begin + i]);
-        t.first[i + 1] = t.first[i] + static_cast<int>(chunks_of(t.size[i]));
+        t.first[i + 1] = t.first[i] + static_cast<int>(chunks_of(t.size[i], kVecs));
     }
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config(static_cast<unsigned>(blocks), kThreads, stream, &attr);
     if (clip)
-        return note_error(cudaLaunchKernelEx(&cfg, clip_kernel<N>, t, static_cast<const Part *>(p.parts), blocks, p.max_norm,
+        return note_error(cudaLaunchKernelEx(&cfg, clip_kernel<N, kVecs>, t, static_cast<const Part *>(p.parts), blocks, p.max_norm,
                                              begin == 0 ? p.norm : static_cast<float *>(nullptr)),
                           "clip_kernel launch");
-    return note_error(cudaLaunchKernelEx(&cfg, norm_kernel<N>, t, static_cast<Part *>(p.parts), begin ? 1 : 0), "norm_kernel launch");
+    return note_error(cudaLaunchKernelEx(&cfg, norm_kernel<N, kVecs>, t, static_cast<Part *>(p.parts), begin ? 1 : 0), "norm_kernel launch");
 }
 
 }  // namespace
-
-int64_t grad_norm_chunk() { return kChunk; }
 
 // At most kMostTensors tensors to a launch; a few take the kernel with the short table.
 cudaError_t launch_grad_norm(const GradNormProblem &p, cudaStream_t stream)
 {
     constexpr int kFew = 32;
-    int64_t most = 1;
-    for (int64_t begin = 0; begin < p.count; begin += kMostTensors) {
-        int64_t chunks = 0;
-        for (int64_t i = begin; i < p.count && i < begin + kMostTensors; ++i) chunks += chunks_of(p.sizes[i]);
-        most = most > chunks ? most : chunks;
-    }
+    auto most_of = [&](int vecs) {
+        int64_t most = 1;
+        for (int64_t begin = 0; begin < p.count; begin += kMostTensors) {
+            int64_t chunks = 0;
+            for (int64_t i = begin; i < p.count && i < begin + kMostTensors; ++i) chunks += chunks_of(p.sizes[i], vecs);
+            most = most > chunks ? most : chunks;
+        }
+        return most;
+    };
+    // Chunks of 8192 values keep 4 loads in flight; where they are fewer than the blocks
+    // that the device holds, chunks of 2048 spread the work.
+    int64_t most = most_of(4);
+    const int vecs = most <= 512 ? 1 : 4;
+    if (vecs == 1) most = most_of(1);
     const int blocks = static_cast<int>(most < kGradNormParts ? most : kGradNormParts);
     for (int pass = 0; pass < (p.out ? 2 : 1); ++pass) {
         int64_t begin = 0;
         do {   // (no tensors: one launch that finds nothing)
             const int64_t end = begin + kMostTensors < p.count ? begin + kMostTensors : p.count;
-            const cudaError_t e = end - begin <= kFew ? launch<kFew>(p, begin, end, blocks, pass == 1, stream)
-                                                      : launch<kMostTensors>(p, begin, end, blocks, pass == 1, stream);
+            const auto go = vecs == 1 ? end - begin <= kFew ? launch<kFew, 1> : launch<kMostTensors, 1>
+                            : end - begin <= kFew ? launch<kFew, 4> : launch<kMostTensors, 4>;
+            const cudaError_t e = go(p, begin, end, blocks, pass == 1, stream);
             if (e != cudaSuccess) return e;
             begin = end;
         } while (begin < p.count);

@@ -227,7 +227,6 @@ struct GradNormProblem {
     float *norm;
     void *parts;                                // [kGradNormParts], 8 bytes each
 };
-int64_t grad_norm_chunk();                      // values that a block takes at a time
 cudaError_t launch_grad_norm(const GradNormProblem &p, cudaStream_t stream);
 
 // The driver's cuTensorMapEncodeTiled (PFN_cuTensorMapEncodeTiled_v12000), or nullptr.

@@ -13,8 +13,9 @@
 // Blocks take rows in turn; a thread keeps the same columns for all its rows and
 // their dw and db in registers.  A second launch adds the blocks' parts in order.
 //
-// Rows longer than the registers of a block hold are read twice, and their dw and
-// db are sums of a launch of their own.  Bound by memory.
+// Longer rows than a block's registers hold dw and db of have them from a launch of
+// their own, which reads dy and h once more, and the longest are read twice for dx.
+// Bound by memory.
 
 #include <math.h>
 
@@ -65,7 +66,7 @@ __device__ __forceinline__ float lanes_sum(float2 v)
     for (int d = 8; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
     return s;
 }
-// The sums over a block's threads, the same in each.  `part` is free again after the
+// The sums over a row's threads (a block, or a warp), the same in each.  `part` is free again after the
 // next barrier.
 template <int THREADS>
 __device__ __forceinline__ float2 block_sum(float2 v, float2 *part)
@@ -73,6 +74,7 @@ __device__ __forceinline__ float2 block_sum(float2 v, float2 *part)
     constexpr int kWarps = THREADS / 32;
     const int lane = threadIdx.x % 32;
     const float s = lanes_sum(v);
+    if constexpr (kWarps == 1) return make_float2(__shfl_sync(0xffffffffu, s, 0), __shfl_sync(0xffffffffu, s, 16));
     if (lane % 16 == 0) reinterpret_cast<float *>(part + threadIdx.x / 32)[lane / 16] = s;
     __syncthreads();
     v = make_float2(0.f, 0.f);
@@ -84,15 +86,20 @@ __device__ __forceinline__ float2 block_sum(float2 v, float2 *part)
 // Whether F32 holds the squares that v + eps is made of.
 __device__ __forceinline__ bool in_range(float v) { return v >= 0x1p-80f && v <= 0x1p120f; }
 
-// One row a block.  LONG: any row length, VPT vectors in registers at a time.
+constexpr int kRowThreads = 256;   // of a block with a row to a warp
+
+// THREADS a row, one row a block, or one a warp.  LONG: any row length, VPT vectors in
+// registers at a time.
 template <typename T, int THREADS, int VPT, bool LONG>
-__global__ void __launch_bounds__(THREADS) layernorm_kernel(const NormArgs a)
+__global__ void __launch_bounds__(THREADS == 32 ? kRowThreads : THREADS) layernorm_kernel(const NormArgs a)
 {
     constexpr int kWarps = THREADS / 32, kPairs = kVec / 2;
     __shared__ float2 part[4][kWarps];
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
-    const int64_t row = blockIdx.x;
+    const int t = THREADS == 32 ? threadIdx.x % 32 : threadIdx.x;
+    const int64_t row = THREADS == 32 ? static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + threadIdx.x / 32 : blockIdx.x;
+    if (THREADS == 32 && row >= a.M) return;
     const size_t at = static_cast<size_t>(row) * a.vecs;
     const Pack<T> *const x = static_cast<const Pack<T> *>(a.x) + at;
     const Pack<T> *const res = a.residual ? static_cast<const Pack<T> *>(a.residual) + at : nullptr;
@@ -108,14 +115,14 @@ __global__ void __launch_bounds__(THREADS) layernorm_kernel(const NormArgs a)
         const bool add = res && !(again && sum);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int v = (turn * VPT + i) * THREADS + threadIdx.x;
+            const int v = (turn * VPT + i) * THREADS + t;
             if (v >= a.vecs) continue;
             px[i] = (again && sum ? sum : x)[v];
             if (add) pr[i] = res[v];
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int v = (turn * VPT + i) * THREADS + threadIdx.x;
+            const int v = (turn * VPT + i) * THREADS + t;
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) h[i][j] = make_float2(0.f, 0.f);
             if (v >= a.vecs) continue;
@@ -150,7 +157,7 @@ __global__ void __launch_bounds__(THREADS) layernorm_kernel(const NormArgs a)
             if (LONG) load(turn, true);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                if ((turn * VPT + i) * THREADS + static_cast<int>(threadIdx.x) >= a.vecs) continue;
+                if ((turn * VPT + i) * THREADS + t >= a.vecs) continue;
 #pragma unroll
                 for (int j = 0; j < kPairs; ++j) {
                     const float2 off = make_float2(-mean, -mean);
@@ -161,9 +168,9 @@ __global__ void __launch_bounds__(THREADS) layernorm_kernel(const NormArgs a)
                 }
             }
         }
-        const float2 t = block_sum<THREADS>(make_float2(s.x + s.y, q.x + q.y), p + kWarps);
-        rest = t.x * inv;
-        float var = t.y * inv - rest * rest;
+        const float2 sums = block_sum<THREADS>(make_float2(s.x + s.y, q.x + q.y), p + kWarps);
+        rest = sums.x * inv;
+        float var = sums.y * inv - rest * rest;
         var = (var < 0.f ? 0.f : var) + (scaled ? a.eps * (scale * wide) * (scale * wide) : a.eps);   // (keeps a NaN)
         rstd = rsqrtf(var);
         return var;
@@ -174,7 +181,7 @@ __global__ void __launch_bounds__(THREADS) layernorm_kernel(const NormArgs a)
             if (LONG) load(turn, true);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int v = (turn * VPT + i) * THREADS + threadIdx.x;
+                const int v = (turn * VPT + i) * THREADS + t;
                 if (v >= a.vecs) continue;
                 float2 w[kPairs], b[kPairs] = {};
                 unpack(static_cast<const Pack<T> *>(a.weight)[v], w);
@@ -201,7 +208,7 @@ __global__ void __launch_bounds__(THREADS) layernorm_kernel(const NormArgs a)
         moments(true, part[2]);
         outputs(true);
     }
-    if (threadIdx.x == 0) {
+    if (t == 0) {
         if (a.mean) a.mean[row] = (mean + rest / wide) / scale;
         if (a.rstd) a.rstd[row] = rstd * (scale * wide);
     }
@@ -219,100 +226,61 @@ struct NormGradArgs {
 // (h - mean) rstd; by halves, as the difference may leave F32's range
 __device__ __forceinline__ float normal_of(float h, float half_mean, float rstd2) { return fmaf(0.5f, h, -half_mean) * rstd2; }
 
-// Rows blockIdx.x, + gridDim.x, ...; a thread's columns are the same for all of them.
-template <typename T, int THREADS, int VPT>
-__global__ void __launch_bounds__(THREADS) layernorm_grad_kernel(const NormGradArgs a)
-{
-    constexpr int kWarps = THREADS / 32;
-    __shared__ float2 part[2][kWarps];
-    ptx::launch_dependents();
-    ptx::grid_dependency_wait();
-    float dw[VPT][kVec] = {}, db[VPT][kVec] = {};
-    int turn = 0;
-    for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1) {
-        const size_t at = static_cast<size_t>(row) * a.K;
-        const float half_mean = 0.5f * a.mean[row], rstd = a.rstd[row], rstd2 = 2.f * rstd;
-        float g[VPT][kVec], x[VPT][kVec], s[2] = {0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = i * THREADS + threadIdx.x;
-            if (v >= a.vecs) continue;
-            const size_t k = static_cast<size_t>(v) * kVec;
-            float w[kVec];
-            unpack(*reinterpret_cast<const Pack<T> *>(static_cast<const T *>(a.dy) + at + k), g[i]);
-            unpack(*reinterpret_cast<const Pack<T> *>(static_cast<const T *>(a.h) + at + k), x[i]);
-            unpack(*reinterpret_cast<const Pack<T> *>(static_cast<const T *>(a.weight) + k), w);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                x[i][j] = normal_of(x[i][j], half_mean, rstd2);
-                dw[i][j] = fmaf(g[i][j], x[i][j], dw[i][j]);
-                db[i][j] += g[i][j];
-                g[i][j] *= w[j];
-                s[0] += g[i][j];
-                s[1] = fmaf(g[i][j], x[i][j], s[1]);
-            }
-        }
-        const float2 t = block_sum<THREADS>(make_float2(s[0], s[1]), part[turn]);
-        const float mg = t.x / static_cast<float>(a.K), mgx = t.y / static_cast<float>(a.K);
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = i * THREADS + threadIdx.x;
-            if (v >= a.vecs) continue;
-            const size_t k = static_cast<size_t>(v) * kVec;
-            float o[kVec] = {};
-            if (a.dsum) unpack(*reinterpret_cast<const Pack<T> *>(static_cast<const T *>(a.dsum) + at + k), o);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) o[j] = fmaf(rstd, g[i][j] - mg - x[i][j] * mgx, o[j]);
-            Pack<T> p;
-            pack(o, p);
-            *reinterpret_cast<Pack<T> *>(static_cast<T *>(a.dx) + at + k) = p;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int v = i * THREADS + threadIdx.x;
-        if (v >= a.vecs) continue;
-        float *const to = a.parts + static_cast<size_t>(blockIdx.x) * 2 * a.K + static_cast<size_t>(v) * kVec;
-        Pack<float> p;
-        pack(dw[i], p);
-        *reinterpret_cast<Pack<float> *>(to) = p;
-        pack(db[i], p);
-        *reinterpret_cast<Pack<float> *>(to + a.K) = p;
-    }
-}
 
 // ---- rows of up to 8192 values: copies into shared memory ahead of the sums
 
 constexpr int kRingThreads = 1024;
 constexpr int kSmCount = 152;
 
-// Rows in flight for each thread: what 192 KB of shared memory hold of dy, h and dsum.
+// A thread takes pieces of 16 bytes of a row, piece q at (thread + q TPR) pieces.
 template <typename T>
+constexpr int piece_values()
+{
+    return static_cast<int>(16 / sizeof(T));
+}
+
+// Rows in flight for each thread: what 192 KB of shared memory hold of dy, h and dsum.
+template <int PIECES>
 constexpr int ring_stages()
 {
-    return sizeof(T) == 2 ? 4 : 2;
+    return 4 / PIECES;
 }
 
-template <typename T>
+template <int PIECES>
 constexpr size_t ring_bytes()
 {
-    return static_cast<size_t>(ring_stages<T>()) * 3 * kRingThreads * sizeof(Pack<T>);
+    return static_cast<size_t>(ring_stages<PIECES>()) * 3 * PIECES * kRingThreads * 16;
 }
 
-template <typename T>
-__device__ __forceinline__ void copy_ahead(Pack<T> *dst, const void *src)
+__device__ __forceinline__ void copy_ahead(uint4 *dst, const uint8_t *src)
 {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(Pack<T>) / 16); ++i)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst) + 16u * i),
-                     "l"(reinterpret_cast<uint64_t>(src) + 16u * i)
-                     : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>
 __device__ __forceinline__ void copies_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+__device__ __forceinline__ void pairs(const uint4 &p, float2 (&v)[2], float)
+{
+    v[0] = make_float2(__uint_as_float(p.x), __uint_as_float(p.y));
+    v[1] = make_float2(__uint_as_float(p.z), __uint_as_float(p.w));
+}
+template <typename T>
+__device__ __forceinline__ void pairs(const uint4 &p, float2 (&v)[4], T)
+{
+    unpack(Pack<T>{p}, v);
+}
+__device__ __forceinline__ uint4 piece(const float2 (&v)[2], float)
+{
+    return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+}
+template <typename T>
+__device__ __forceinline__ uint4 piece(const float2 (&v)[4], T)
+{
+    return packed<T>(v).a;
 }
 
 // The sums of a row's TPR threads, the same in each.
@@ -331,38 +299,48 @@ __device__ __forceinline__ float2 row_sum(float2 v, float2 *part, int group)
     return make_float2(__shfl_sync(0xffffffffu, s, 0), __shfl_sync(0xffffffffu, s, 16));
 }
 
-// TPR threads a row, one vector each; groups of them take rows in turn.  A thread
-// copies its own vectors of the next rows into its own places of shared memory, and
-// reads them again when it comes to the row: no barrier but the row's sum.
-template <typename T, int TPR>
+// TPR threads a row, PIECES pieces each; groups of them take rows in turn.  A thread
+// copies its own pieces of the next rows into its own places of shared memory, and
+// reads them again when it comes to the row: no barrier but the row's sum.  Where the
+// pieces are more than 8 values, the registers hold no dw and db: dx alone is made, and
+// a row's values are read and worked out once more after its sum.
+template <typename T, int TPR, int PIECES>
 __global__ void __launch_bounds__(kRingThreads, 1) layernorm_grad_ring_kernel(const NormGradArgs a)
 {
-    constexpr int kGroups = kRingThreads / TPR, kStages = ring_stages<T>();
+    constexpr int kGroups = kRingThreads / TPR, kStages = ring_stages<PIECES>(), kValues = piece_values<T>(), kPairs = kValues / 2;
+    constexpr int kTensor = PIECES * kRingThreads;
+    constexpr bool kSums = PIECES * kValues <= kVec;
+    constexpr int kKept = kSums ? PIECES : 1;
     extern __shared__ __align__(16) uint8_t ring_raw[];
     __shared__ float2 part[2][kRingThreads / 32];
-    Pack<T> *const ring = reinterpret_cast<Pack<T> *>(ring_raw) + threadIdx.x;   // [stage][tensor][thread]
+    uint4 *const ring = reinterpret_cast<uint4 *>(ring_raw) + threadIdx.x;   // [stage][tensor][piece][thread]
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
-    const int group = threadIdx.x / TPR, v = threadIdx.x % TPR;
-    const bool in = v < a.vecs;
+    const int group = threadIdx.x / TPR, v = threadIdx.x % TPR, pieces = a.K / kValues;
+    auto in = [&](int q) { return v + q * TPR < pieces; };
     // rows are counted in 32 bits (M <= 2^22), their addresses by a running offset
     const int M = static_cast<int>(a.M), step = static_cast<int>(gridDim.x) * kGroups, first = static_cast<int>(blockIdx.x) * kGroups + group;
-    const size_t stride = static_cast<size_t>(step) * a.vecs * sizeof(Pack<T>);
-    size_t at = (static_cast<size_t>(first) * a.vecs + v) * sizeof(Pack<T>);
-    Pack<T> weight;
-    if (in) weight = static_cast<const Pack<T> *>(a.weight)[v];
+    const size_t stride = static_cast<size_t>(step) * pieces * 16;
+    size_t at = (static_cast<size_t>(first) * pieces + v) * 16;
+    uint4 weight[PIECES];
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q)
+        if (in(q)) weight[q] = static_cast<const uint4 *>(a.weight)[v + q * TPR];
     auto ahead = [&](bool there, size_t from, int stage) {
-        if (in && there) {
-            Pack<T> *const to = ring + stage * 3 * kRingThreads;
-            copy_ahead(to, static_cast<const uint8_t *>(a.dy) + from);
-            copy_ahead(to + kRingThreads, static_cast<const uint8_t *>(a.h) + from);
-            if (a.dsum) copy_ahead(to + 2 * kRingThreads, static_cast<const uint8_t *>(a.dsum) + from);
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) {
+            if (!in(q) || !there) continue;
+            uint4 *const to = ring + stage * 3 * kTensor + q * kRingThreads;
+            const size_t f = from + static_cast<size_t>(q) * TPR * 16;
+            copy_ahead(to, static_cast<const uint8_t *>(a.dy) + f);
+            copy_ahead(to + kTensor, static_cast<const uint8_t *>(a.h) + f);
+            if (a.dsum) copy_ahead(to + 2 * kTensor, static_cast<const uint8_t *>(a.dsum) + f);
         }
         copies_commit();
     };
 #pragma unroll
     for (int s = 0; s < kStages; ++s) ahead(first + s * step < M, at + s * stride, s);
-    float2 dw[kVec / 2] = {}, db[kVec / 2] = {};
+    float2 dw[kKept][kPairs] = {}, db[kKept][kPairs] = {};
     float mean = 0.f, rstd = 0.f;
     if (first < M) mean = a.mean[first], rstd = a.rstd[first];
     int stage = 0, turn = 0;
@@ -371,55 +349,77 @@ __global__ void __launch_bounds__(kRingThreads, 1) layernorm_grad_ring_kernel(co
         copies_wait<kStages - 1>();
         const float2 half = {0.5f, 0.5f}, off = {-0.5f * mean, -0.5f * mean}, r = {rstd, rstd}, r2 = {2.f * rstd, 2.f * rstd};
         if (row + step < M) mean = a.mean[row + step], rstd = a.rstd[row + step];
-        const Pack<T> *const from = ring + stage * 3 * kRingThreads;
-        float2 g[kVec / 2], x[kVec / 2], s0 = {0.f, 0.f}, s1 = {0.f, 0.f};
-        if (in) {
-            float2 w[kVec / 2];
-            unpack(from[0], g);
-            unpack(from[kRingThreads], x);
-            unpack(weight, w);
+        const uint4 *const from = ring + stage * 3 * kTensor;
+        float2 g[kKept][kPairs], x[kKept][kPairs], s0 = {0.f, 0.f}, s1 = {0.f, 0.f};
+        auto values = [&](int q, int to) {   // g = dy w and the normal of h; dw and db on the way
+            float2 w[kPairs];
+            pairs(from[q * kRingThreads], g[to], T{});
+            pairs(from[q * kRingThreads + kTensor], x[to], T{});
+            pairs(weight[q], w, T{});
 #pragma unroll
-            for (int j = 0; j < kVec / 2; ++j) {
-                x[j] = __fmul2_rn(__ffma2_rn(half, x[j], off), r2);   // normal_of
-                dw[j] = __ffma2_rn(g[j], x[j], dw[j]);
-                db[j] = __fadd2_rn(db[j], g[j]);
-                g[j] = __fmul2_rn(g[j], w[j]);
-                s0 = __fadd2_rn(s0, g[j]);
-                s1 = __ffma2_rn(g[j], x[j], s1);
+            for (int j = 0; j < kPairs; ++j) {
+                x[to][j] = __fmul2_rn(__ffma2_rn(half, x[to][j], off), r2);   // normal_of
+                if constexpr (kSums) {
+                    dw[to][j] = __ffma2_rn(g[to][j], x[to][j], dw[to][j]);
+                    db[to][j] = __fadd2_rn(db[to][j], g[to][j]);
+                }
+                g[to][j] = __fmul2_rn(g[to][j], w[j]);
+            }
+        };
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) {
+            if (!in(q)) continue;
+            const int to = kSums ? q : 0;
+            values(q, to);
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                s0 = __fadd2_rn(s0, g[to][j]);
+                s1 = __ffma2_rn(g[to][j], x[to][j], s1);
             }
         }
         const float2 s = row_sum<TPR>(make_float2(s0.x + s0.y, s1.x + s1.y), part[turn] + group * (TPR / 32), group);
-        if (in) {
-            const float2 mg = {-s.x * inv, -s.x * inv}, mgx = {-s.y * inv, -s.y * inv};
-            float2 o[kVec / 2] = {};
-            if (a.dsum) unpack(from[2 * kRingThreads], o);
+        const float2 mg = {-s.x * inv, -s.x * inv}, mgx = {-s.y * inv, -s.y * inv};
 #pragma unroll
-            for (int j = 0; j < kVec / 2; ++j) o[j] = __ffma2_rn(r, __ffma2_rn(x[j], mgx, __fadd2_rn(g[j], mg)), o[j]);
-            *reinterpret_cast<Pack<T> *>(static_cast<uint8_t *>(a.dx) + at) = packed<T>(o);
+        for (int q = 0; q < PIECES; ++q) {
+            if (!in(q)) continue;
+            const int to = kSums ? q : 0;
+            if constexpr (!kSums) values(q, 0);
+            float2 o[kPairs] = {};
+            if (a.dsum) pairs(from[q * kRingThreads + 2 * kTensor], o, T{});
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) o[j] = __ffma2_rn(r, __ffma2_rn(x[to][j], mgx, __fadd2_rn(g[to][j], mg)), o[j]);
+            *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.dx) + at + static_cast<size_t>(q) * TPR * 16) = piece(o, T{});
         }
         ahead(row + kStages * step < M, at + kStages * stride, stage);
         stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     copies_wait<0>();
-    float *const to = a.parts + static_cast<size_t>(blockIdx.x) * 2 * a.K;
-    if constexpr (kGroups == 1) {
-        if (in) {
-            *reinterpret_cast<Pack<float> *>(to + v * kVec) = packed<float>(dw);
-            *reinterpret_cast<Pack<float> *>(to + a.K + v * kVec) = packed<float>(db);
+    if constexpr (kSums) {
+        // Column k of dw, then of db; several groups' through shared memory, in their order.
+        constexpr int kRow = TPR * PIECES * kValues;
+        float *const to = a.parts + static_cast<size_t>(blockIdx.x) * 2 * a.K;
+        float *const sums = kGroups == 1 ? to : reinterpret_cast<float *>(ring_raw) + group * 2 * kRow;   // [group][2][kRow]
+        const int width = kGroups == 1 ? a.K : kRow;
+        if constexpr (kGroups > 1) __syncthreads();
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) {
+            if (kGroups == 1 && !in(q)) continue;
+            const int k = (v + q * TPR) * kValues;
+#pragma unroll
+            for (int j = 0; j < kPairs; j += 2) {
+                *reinterpret_cast<float4 *>(sums + k + 2 * j) = make_float4(dw[q][j].x, dw[q][j].y, dw[q][j + 1].x, dw[q][j + 1].y);
+                *reinterpret_cast<float4 *>(sums + width + k + 2 * j) = make_float4(db[q][j].x, db[q][j].y, db[q][j + 1].x, db[q][j + 1].y);
+            }
         }
-    } else {
-        // the groups' sums, in their order
-        float *const sums = reinterpret_cast<float *>(ring_raw);   // [group][2][TPR * kVec]
-        __syncthreads();
-        *reinterpret_cast<Pack<float> *>(sums + (group * 2 * TPR + v) * kVec) = packed<float>(dw);
-        *reinterpret_cast<Pack<float> *>(sums + (group * 2 * TPR + TPR + v) * kVec) = packed<float>(db);
-        __syncthreads();
-        for (int c = threadIdx.x; c < 2 * TPR * kVec; c += kRingThreads) {
-            float sum = 0.f;
+        if constexpr (kGroups > 1) {
+            __syncthreads();
+            for (int c = threadIdx.x; c < 2 * kRow; c += kRingThreads) {
+                float sum = 0.f;
 #pragma unroll 8
-            for (int i = 0; i < kGroups; ++i) sum += sums[i * 2 * TPR * kVec + c];
-            const int which = c / (TPR * kVec), k = c % (TPR * kVec);
-            if (k < a.K) to[which * a.K + k] = sum;
+                for (int i = 0; i < kGroups; ++i) sum += reinterpret_cast<float *>(ring_raw)[i * 2 * kRow + c];
+                const int which = c / kRow, k = c % kRow;
+                if (k < a.K) to[which * a.K + k] = sum;
+            }
         }
     }
 }
@@ -514,8 +514,15 @@ __global__ void __launch_bounds__(kSumThreads) layernorm_sum_kernel(const float 
     const int64_t c = static_cast<int64_t>(blockIdx.x) * kSumLanes + lane;
     float sum = 0.f;
     if (c < 2 * static_cast<int64_t>(K)) {
-#pragma unroll 8
-        for (int b = slice; b < blocks; b += kSumSlices) sum += parts[static_cast<size_t>(b) * 2 * K + c];
+        constexpr int kAtOnce = 10;   // loads in flight: two rounds for 152 parts
+        for (int b = slice; b < blocks; b += kAtOnce * kSumSlices) {
+            float x[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                x[i] = b + i * kSumSlices < blocks ? parts[static_cast<size_t>(b + i * kSumSlices) * 2 * K + c] : 0.f;
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) sum += x[i];
+        }
     }
     part[slice][lane] = sum;
     __syncthreads();
@@ -536,13 +543,16 @@ template <typename T, int THREADS, int VPT, bool LONG = false>
 cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream)
 {
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config(static_cast<unsigned>(a.M), THREADS, stream, &attr);
+    constexpr int kThreads = THREADS == 32 ? kRowThreads : THREADS, kRows = kThreads / THREADS;
+    const cudaLaunchConfig_t cfg = config(static_cast<unsigned>((a.M + kRows - 1) / kRows), kThreads, stream, &attr);
     return note_error(cudaLaunchKernelEx(&cfg, layernorm_kernel<T, THREADS, VPT, LONG>, a), "layernorm_kernel launch");
 }
 
 template <typename T>
 cudaError_t launch_norm_type(const NormArgs &a, cudaStream_t stream)
 {
+    if (a.vecs <= 32) return launch_norm<T, 32, 1>(a, stream);
+    if (a.vecs <= 64) return launch_norm<T, 32, 2>(a, stream);
     if (a.vecs <= 128) return launch_norm<T, 128, 1>(a, stream);
     if (a.vecs <= 256) return launch_norm<T, 256, 1>(a, stream);
     if (a.vecs <= 512) return launch_norm<T, 256, 2>(a, stream);
@@ -552,25 +562,17 @@ cudaError_t launch_norm_type(const NormArgs &a, cudaStream_t stream)
     return launch_norm<T, 512, 4, true>(a, stream);
 }
 
-template <typename T, int THREADS, int VPT>
-cudaError_t launch_grad(const NormGradArgs &a, int blocks, cudaStream_t stream)
-{
-    cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config(static_cast<unsigned>(blocks), THREADS, stream, &attr);
-    return note_error(cudaLaunchKernelEx(&cfg, layernorm_grad_kernel<T, THREADS, VPT>, a), "layernorm_grad_kernel launch");
-}
-
-template <typename T, int TPR>
+template <typename T, int TPR, int PIECES = kVec / piece_values<T>()>
 cudaError_t launch_ring(const NormGradArgs &a, int blocks, cudaStream_t stream)
 {
-    const cudaError_t e = note_error(cudaFuncSetAttribute(layernorm_grad_ring_kernel<T, TPR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                          static_cast<int>(ring_bytes<T>())),
+    const cudaError_t e = note_error(cudaFuncSetAttribute(layernorm_grad_ring_kernel<T, TPR, PIECES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                          static_cast<int>(ring_bytes<PIECES>())),
                                      "layernorm_grad_ring_kernel shared memory");
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = config(static_cast<unsigned>(blocks), kRingThreads, stream, &attr);
-    cfg.dynamicSmemBytes = ring_bytes<T>();
-    return note_error(cudaLaunchKernelEx(&cfg, layernorm_grad_ring_kernel<T, TPR>, a), "layernorm_grad_ring_kernel launch");
+    cfg.dynamicSmemBytes = ring_bytes<PIECES>();
+    return note_error(cudaLaunchKernelEx(&cfg, layernorm_grad_ring_kernel<T, TPR, PIECES>, a), "layernorm_grad_ring_kernel launch");
 }
 
 template <typename T>
@@ -585,7 +587,6 @@ cudaError_t launch_grad_type(const NormGradArgs &a, int blocks, cudaStream_t str
         default: return launch_ring<T, 1024>(a, blocks, stream);
         }
     }
-    if (a.vecs <= kLongVecs) return launch_grad<T, 512, 4>(a, blocks, stream);
     constexpr int kThreads = 512;
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = config(static_cast<unsigned>(a.M), kThreads, stream, &attr);
@@ -593,6 +594,8 @@ cudaError_t launch_grad_type(const NormGradArgs &a, int blocks, cudaStream_t str
     cfg.gridDim = dim3(static_cast<unsigned>((a.vecs + kThreads - 1) / kThreads), static_cast<unsigned>(blocks), 1);
     cudaError_t e = note_error(cudaLaunchKernelEx(&cfg, layernorm_grad_columns_kernel<T, kThreads>, a), "layernorm_grad_columns_kernel launch");
     if (e != cudaSuccess) return e;
+    if constexpr (sizeof(T) == 2)
+        if (a.vecs <= 2 * kRingVecs) return launch_ring<T, 1024, 2>(a, static_cast<int>(a.M < kSmCount ? a.M : kSmCount), stream);
     cfg.gridDim = dim3(static_cast<unsigned>(a.M), 1, 1);
     return note_error(cudaLaunchKernelEx(&cfg, layernorm_grad_long_kernel<T, kThreads>, a), "layernorm_grad_long_kernel launch");
 }
@@ -609,10 +612,11 @@ cudaError_t launch_layernorm(const LayerNormProblem &p, cudaStream_t stream)
 
 int64_t layernorm_grad_parts(int64_t M, int64_t K)
 {
-    // A block to an SM; long rows have columns enough for the threads: few parts.
+    // A block to an SM, as few as the same number of turns takes (333 rows of 5120 F16: 111
+    // blocks 9.9 us, 152 blocks 10.6); long rows have columns enough for the threads.
     const int64_t vecs = K / kVec, rows = vecs <= kRingVecs ? kRingThreads / ring_row_threads(vecs) : 1;
-    const int64_t blocks = (M + rows - 1) / rows, most = vecs <= kLongVecs ? kSmCount : 16;
-    return blocks < most ? blocks : most;
+    const int64_t tiles = (M + rows - 1) / rows, most = vecs <= kRingVecs ? kSmCount : 64, turns = (tiles + most - 1) / most;
+    return turns ? (tiles + turns - 1) / turns : 0;
 }
 
 cudaError_t launch_layernorm_grad(const LayerNormGradProblem &p, cudaStream_t stream)
