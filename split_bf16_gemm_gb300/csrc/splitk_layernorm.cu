@@ -535,7 +535,8 @@ __global__ void __launch_bounds__(kSumThreads) layernorm_sum_kernel(const float 
 }
 
 constexpr int kLongVecs = 2048;   // vectors of the longest row that a block's registers hold
-constexpr int kRingVecs = 1024;   // the same for the ring
+constexpr int kRingVecs = 1024;   // the same for the ring with dw and db
+constexpr int kColumnThreads = 512;
 
 int ring_row_threads(int64_t vecs) { return vecs <= 32 ? 32 : vecs <= 128 ? 128 : vecs <= 256 ? 256 : vecs <= 512 ? 512 : 1024; }
 
@@ -587,7 +588,7 @@ cudaError_t launch_grad_type(const NormGradArgs &a, int blocks, cudaStream_t str
         default: return launch_ring<T, 1024>(a, blocks, stream);
         }
     }
-    constexpr int kThreads = 512;
+    constexpr int kThreads = kColumnThreads;
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = config(static_cast<unsigned>(a.M), kThreads, stream, &attr);
     // dw and db first: dx may be dy
@@ -613,9 +614,11 @@ cudaError_t launch_layernorm(const LayerNormProblem &p, cudaStream_t stream)
 int64_t layernorm_grad_parts(int64_t M, int64_t K)
 {
     // A block to an SM, as few as the same number of turns takes (333 rows of 5120 F16: 111
-    // blocks 9.9 us, 152 blocks 10.6); long rows have columns enough for the threads.
+    // blocks 9.9 us, 152 blocks 10.6).  Long rows have columns for many blocks of
+    // kColumnThreads, and fewer parts the longer they are.
     const int64_t vecs = K / kVec, rows = vecs <= kRingVecs ? kRingThreads / ring_row_threads(vecs) : 1;
-    const int64_t tiles = (M + rows - 1) / rows, most = vecs <= kRingVecs ? kSmCount : 64, turns = (tiles + most - 1) / most;
+    const int64_t across = (vecs + kColumnThreads - 1) / kColumnThreads, tiles = (M + rows - 1) / rows;
+    const int64_t most = vecs <= kRingVecs ? kSmCount : across >= 40 ? 8 : across <= 5 ? 64 : 320 / across, turns = (tiles + most - 1) / most;
     return turns ? (tiles + turns - 1) / turns : 0;
 }
 

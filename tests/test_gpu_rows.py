@@ -101,6 +101,23 @@ def test_route_ties_zeros_and_types(sk):
         assert s[0].tolist() == [0.25] * 4
 
 
+@pytest.mark.parametrize("G", [8, 40, 64, 100, 256, 500, 1024])
+def test_route_of_equal_logits(sk, G):
+    """As a router whose weights are zeros gives them; and groups of equal ones."""
+    M = 5
+    for top in (1, 4, 8, min(G, 32)):
+        logits = torch.zeros(M, G, device="cuda")
+        logits[1] = (torch.arange(G, device="cuda") % 3).float()
+        logits[2, G // 2:] = -math.inf
+        logits[3] = torch.arange(G, device="cuda") // 40
+        logits[4, ::2] = -0.0
+        e, s = torch.empty(M, top, dtype=INT, device="cuda"), torch.empty(M, top, device="cuda")
+        sk.moe_route(logits, e, s, M, G, top, "f32")
+        experts, shares, p = ref.route(logits.cpu(), top, False)
+        assert torch.equal(e.cpu().long(), experts)
+        within(s, shares, shares * route_tolerance(logits, p).gather(1, experts.clamp(min=0)))
+
+
 def test_route_extremes(sk):
     inf, nan = math.inf, math.nan
     rows = [[nan, 1.0, 2.0, inf], [1.0, inf, 0.0, inf], [3e38, -3e38, 0.0, -inf], [-inf, -inf, -3e38, -inf], [1e-45, 0.0, -1e-45, -inf]]
@@ -138,7 +155,7 @@ def test_route_gradient_of_repeated_and_foreign_experts(sk):
 # ------------------------------------------------------------------ sorted rows
 
 SORTS = [(1, 1, 1, 0), (1, 8, 8, 0), (5, 3, 2, 1), (64, 4, 32, 0), (33, 3, 1000, 7), (255, 4, 16, 9), (256, 4, 256, 0), (257, 4, 7, 11),
-         (1000, 1, 1024, 0), (1025, 2, 64, 100), (4099, 8, 256, 31), (8192, 8, 256, 100), (20000, 6, 60, 5), (131, 32, 40, 3), (3, 32, 1024, 0)]
+         (1000, 1, 1024, 0), (1025, 2, 64, 100), (4099, 8, 256, 31), (8192, 8, 256, 100), (20000, 6, 60, 5), (4096, 4, 100, 0), (16385, 1, 16, 0), (131, 32, 40, 3), (3, 32, 1024, 0)]
 
 
 def choose(g, M, top, G, padded):
@@ -478,6 +495,83 @@ def test_streams_and_threads(sk):
     for layer, w in zip(layers, want):
         for n, t in w.items():
             assert torch.equal(t, getattr(layer, n)), n
+
+
+def test_captured_beside_the_split_k_product(sk):
+    """Layer norm, a split-K product of its output, route of the product's rows, and back
+    through the norm, captured in one graph: the eager bits."""
+    M, K, G = 64, 1024, 64
+    g = gen(12)
+    x, w, router = randn(g, M, K).half(), randn(g, K).half(), randn(g, G, K).half()
+    nbytes = sk.gemm_bt_workspace_bytes(M, G, K, 2, 512)
+    ws = torch.empty(nbytes // 4, device="cuda")
+    y, logits, e, s = torch.empty_like(x), torch.empty(M, G, device="cuda"), torch.empty(M, 4, dtype=INT, device="cuda"), torch.empty(M, 4, device="cuda")
+    o, sl, rows, out = (torch.empty(G + 1, dtype=INT, device="cuda"), torch.empty(M, 4, dtype=INT, device="cuda"),
+                        torch.empty(4 * M, K, dtype=torch.float16, device="cuda"), torch.empty(M, K, device="cuda"))
+
+    def step():
+        for fused in (0, 1):
+            sk.layernorm(x, w, None, y, M, K, "f16")
+            sk.gemm_bt(y, router, logits, ws, nbytes, M, G, K, 2, 512, "f16", fused=fused)
+            sk.moe_route(logits, e, s, M, G, 4, "f32")
+            sk.moe_dispatch(e, y, o, sl, None, rows, M, 4, G, K, "f16")
+            sk.moe_combine(rows, sl, s, out, M, 4, K, "f16", "f32")
+            x.copy_(out)
+
+    kept = x.clone()
+    step()
+    want = [t.clone() for t in (logits, e, s, o, sl, rows, out)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        x.copy_(kept)
+        for t in (logits, e, s, o, sl, rows, out):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, (logits, e, s, o, sl, rows, out)))
+    assert sk.splitk_get_device_status() == 0
+
+
+FIRST = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+import split_bf16_gemm_gb300 as sk
+M, top, G, K = 5000, 4, 500, 264
+e = torch.arange(M * top, device="cuda").mul(7).remainder(G).int().view(M, top)
+x = torch.arange(M, device="cuda").float()[:, None].expand(M, K).contiguous()
+o, s = torch.zeros(G + 1, dtype=torch.int32, device="cuda"), torch.zeros(M, top, dtype=torch.int32, device="cuda")
+src, rows, back = torch.zeros(M * top, dtype=torch.int32, device="cuda"), torch.zeros(M * top, K, device="cuda"), torch.zeros(M, K, device="cuda")
+dw, db, one = torch.zeros(K, device="cuda"), torch.zeros(K, device="cuda"), torch.ones(M, device="cuda")
+nb = sk.layernorm_grad_workspace_bytes(M, K)
+ws = torch.zeros(nb, dtype=torch.uint8, device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    sk.moe_dispatch(e, x, o, s, src, rows, M, top, G, K, "f32")
+    sk.moe_sort(e, o, s, src, M, top, G)
+    sk.moe_combine(rows, s, None, back, M, top, K, "f32", "f32")
+    sk.layernorm_grad(back, x, one[:K].contiguous(), one, one, rows[:M], dw, db, ws, nb, M, K, "f32")
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(back, top * x), "rows"
+key, order = torch.sort(e.flatten(), stable=True)
+assert torch.equal(src.long(), order), "source"
+assert torch.equal(db, torch.full_like(db, float(top * M * (M - 1) // 2))) or (db / (top * M * (M - 1) / 2) - 1).abs().max() < 1e-5
+print("first calls captured")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured(sk):
+    """Kernels that need more shared memory or wider clusters than the default set
+    that up in any call."""
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root)], capture_output=True, text=True, timeout=200)
+    assert "first calls captured" in r.stdout, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("M", [4, 300])
