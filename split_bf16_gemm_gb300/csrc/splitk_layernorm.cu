@@ -560,6 +560,8 @@ cudaError_t launch_norm_type(const NormArgs &a, cudaStream_t stream)
     if (a.vecs <= 768) return launch_norm<T, 256, 3>(a, stream);
     if (a.vecs <= 1024) return launch_norm<T, 256, 4>(a, stream);
     if (a.vecs <= kLongVecs) return launch_norm<T, 512, 4>(a, stream);
+    if constexpr (sizeof(T) == 2)
+        if (a.vecs <= 2 * kLongVecs) return launch_norm<T, 1024, 4>(a, stream);
     return launch_norm<T, 512, 4, true>(a, stream);
 }
 
