@@ -14,7 +14,7 @@
 // every time.
 //
 // dispatch_kernel: a token's row is read once and written to each of its rows.
-// For few entries (sorted_here) every block finds the rows of its own tokens by
+// For up to 2048 entries every block finds the rows of its own tokens by
 // itself, comparing their entries with all others, and one more block makes the
 // offsets: one launch instead of two.
 //
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) source_kernel(const int *slots, int 
 // ------------------------------------------------------------------ rows to their experts
 
 struct DispatchArgs {
-    const int *experts;      // sorted_here: [M,top]
+    const int *experts;      // [M,top]
     const uint4 *x;          // [M, vecs] 16-byte vectors
     const float *scales;     // [M, blocks] or nullptr
     int *offsets, *slots, *source;
@@ -219,39 +219,46 @@ struct DispatchArgs {
     int M, top, G, vecs, blocks;
 };
 
-constexpr int kHere = 1024;                    // most entries that every block sorts by itself
-constexpr int kMaxTop = 32;
+constexpr int kHere = 2048;   // most entries that every block sorts by itself
+constexpr int kMaxTop = 32;   // SPLITK_MAX_TOP
 
-// The block's token: where its entries go, by comparison with every entry.
+// The block's token: where its entries go, by comparison with every entry, E of them
+// in each thread.
+template <int E>
 __device__ __forceinline__ void places_of(const DispatchArgs &a, int m, int *place)
 {
-    const int T = a.M * a.top;
-    for (int j = threadIdx.x; j < a.top; j += kThreads) place[j] = 0;
-    __syncthreads();
-    int e[kHere / kThreads];
+    __shared__ int own[kMaxTop], part[kMaxTop][kThreads / 32];
+    const int T = a.M * a.top, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int e[E];
 #pragma unroll
-    for (int i = 0; i < kHere / kThreads; ++i) {
+    for (int i = 0; i < E; ++i) {
         const int t = i * kThreads + static_cast<int>(threadIdx.x);
         e[i] = t < T ? a.experts[t] : -1;
     }
+    if (static_cast<int>(threadIdx.x) < a.top) own[threadIdx.x] = a.experts[m * a.top + threadIdx.x];
+    __syncthreads();
+#pragma unroll 4
     for (int j = 0; j < a.top; ++j) {
-        const int at = m * a.top + j, mine = a.experts[at];
+        const int at = m * a.top + j, mine = own[j];
         int lower = 0;
 #pragma unroll
-        for (int i = 0; i < kHere / kThreads; ++i) {
+        for (int i = 0; i < E; ++i) {
             const int t = i * kThreads + static_cast<int>(threadIdx.x);
             lower += e[i] >= 0 && (e[i] < mine || (e[i] == mine && t < at));
         }
         lower = __reduce_add_sync(0xffffffffu, lower);
-        if (threadIdx.x % 32 == 0 && lower) atomicAdd(&place[j], lower);   // (whole numbers: any order)
+        if (lane == 0) part[j][warp] = lower;
     }
     __syncthreads();
-    if (threadIdx.x < a.top) {
-        const int at = m * a.top + static_cast<int>(threadIdx.x);
-        const bool in = static_cast<unsigned>(a.experts[at]) < static_cast<unsigned>(a.G);
-        if (!in) place[threadIdx.x] = -1;
-        a.slots[at] = place[threadIdx.x];
-        if (in && a.source) a.source[place[threadIdx.x]] = at;
+    if (static_cast<int>(threadIdx.x) < a.top) {
+        const int at = m * a.top + static_cast<int>(threadIdx.x), mine = own[threadIdx.x];
+        int lower = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) lower += part[threadIdx.x][w];
+        if (static_cast<unsigned>(mine) >= static_cast<unsigned>(a.G)) lower = -1;
+        place[threadIdx.x] = lower;
+        a.slots[at] = lower;
+        if (a.source && lower >= 0) a.source[lower] = at;
     }
     __syncthreads();
 }
@@ -267,42 +274,71 @@ __device__ __forceinline__ void offsets_of(const DispatchArgs &a, int *counts)
         if (static_cast<unsigned>(e) < static_cast<unsigned>(a.G)) atomicAdd(&counts[e], 1);
     }
     __syncthreads();
-    if (threadIdx.x < 32) {
-        int before = 0;
-        for (int g0 = 0; g0 <= a.G; g0 += 32) {
-            const int g = g0 + static_cast<int>(threadIdx.x);
-            const int c = g < a.G ? counts[g] : 0;
-            int scan = c;
+    // four consecutive experts to a thread
+    constexpr int kEach = kMaxGroups / kThreads;
+    __shared__ int sums[kThreads / 32];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int c[kEach], mine = 0;
 #pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int x = __shfl_up_sync(0xffffffffu, scan, d);
-                if (static_cast<int>(threadIdx.x) >= d) scan += x;
-            }
-            if (g <= a.G) a.offsets[g] = before + scan - c;
-            before += __shfl_sync(0xffffffffu, scan, 31);
-        }
-        if (threadIdx.x == 0) counts[0] = before;
+    for (int i = 0; i < kEach; ++i) {
+        const int g = kEach * static_cast<int>(threadIdx.x) + i;
+        c[i] = g < a.G ? counts[g] : 0;
+        mine += c[i];
     }
+    int scan = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, scan, d);
+        if (lane >= d) scan += x;
+    }
+    if (lane == 31) sums[warp] = scan;
     __syncthreads();
+    int before = scan - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int g = kEach * static_cast<int>(threadIdx.x) + i;
+        if (g < a.G) a.offsets[g] = before;
+        before += c[i];
+    }
+    if (threadIdx.x == 0) a.offsets[a.G] = total;
     if (a.source)
-        for (int r = counts[0] + static_cast<int>(threadIdx.x); r < T; r += kThreads) a.source[r] = -1;
+        for (int r = total + static_cast<int>(threadIdx.x); r < T; r += kThreads) a.source[r] = -1;
 }
 
-// A token to each block of x, split over the blocks of y along the row.
-template <bool HERE>
+// A token to a block.  E > 0: the launch sorts too, up to 256 E entries.
+template <int E>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchArgs a)
 {
-    __shared__ int place[HERE ? 1032 : kMaxTop];   // (HERE: G + 1 counts of the last block)
-    if constexpr (HERE) ptx::launch_dependents();
-    ptx::grid_dependency_wait();
-    if constexpr (!HERE) ptx::launch_dependents();
+    constexpr bool HERE = E > 0;
+    __shared__ int place[HERE ? kMaxGroups + 1 : kMaxTop];   // (HERE: the last block's counts)
     const int m = static_cast<int>(blockIdx.x);
-    if (HERE && m == a.M) {
-        offsets_of(a, place);
-        return;
+    if constexpr (HERE) {
+        ptx::launch_dependents();
+        ptx::grid_dependency_wait();
+        if (m == a.M) {
+            offsets_of(a, place);
+            return;
+        }
+    }
+    // Vectors on their way while the rows are found.  (After the sort's launch: it lets
+    // this one start when what was before it is done, so x is there.)
+    const uint4 *const x = a.x + static_cast<int64_t>(m) * a.vecs;
+    constexpr int kAhead = 2;
+    uint4 p[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (static_cast<int>(threadIdx.x) + i * kThreads < a.vecs) p[i] = x[threadIdx.x + i * kThreads];
+    if constexpr (!HERE) {
+        ptx::grid_dependency_wait();
+        ptx::launch_dependents();
     }
     if constexpr (HERE) {
-        places_of(a, m, place);
+        places_of<E>(a, m, place);
     } else {
         if (threadIdx.x < a.top) {
             const int at = m * a.top + static_cast<int>(threadIdx.x), r = a.slots[at];
@@ -311,11 +347,19 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchArgs a
         }
         __syncthreads();
     }
-    const uint4 *const x = a.x + static_cast<int64_t>(m) * a.vecs;
-    for (int v = threadIdx.x; v < a.vecs; v += kThreads) {
-        const uint4 p = x[v];
-        for (int j = 0; j < a.top; ++j)
-            if (place[j] >= 0) a.rows[static_cast<int64_t>(place[j]) * a.vecs + v] = p;
+    for (int v0 = threadIdx.x; v0 < a.vecs; v0 += kAhead * kThreads) {
+        if (v0 >= kAhead * kThreads) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (v0 + i * kThreads < a.vecs) p[i] = x[v0 + i * kThreads];
+        }
+        for (int j = 0; j < a.top; ++j) {
+            if (place[j] < 0) continue;
+            uint4 *const to = a.rows + static_cast<int64_t>(place[j]) * a.vecs;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (v0 + i * kThreads < a.vecs) to[v0 + i * kThreads] = p[i];
+        }
     }
     if (a.scales)
         for (int b = threadIdx.x; b < a.blocks; b += kThreads) {
@@ -592,8 +636,10 @@ cudaError_t launch_dispatch(const DispatchProblem &p, cudaStream_t stream)
     }
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config(static_cast<unsigned>(p.M + (here ? 1 : 0)), kThreads, stream, &attr);
-    return note_error(here ? cudaLaunchKernelEx(&cfg, dispatch_kernel<true>, a) : cudaLaunchKernelEx(&cfg, dispatch_kernel<false>, a),
-                      "dispatch_kernel launch");
+    const int64_t T = p.M * p.top;
+    auto *const kernel = !here ? dispatch_kernel<0> : T <= kThreads ? dispatch_kernel<1> : T <= 2 * kThreads ? dispatch_kernel<2>
+                         : T <= 4 * kThreads ? dispatch_kernel<4> : dispatch_kernel<8>;
+    return note_error(cudaLaunchKernelEx(&cfg, kernel, a), "dispatch_kernel launch");
 }
 
 cudaError_t launch_combine(const CombineProblem &p, cudaStream_t stream)
