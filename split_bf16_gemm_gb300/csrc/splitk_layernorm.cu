@@ -283,27 +283,45 @@ __device__ __forceinline__ uint4 piece(const float2 (&v)[4], T)
     return packed<T>(v).a;
 }
 
-// The sums of a row's TPR threads, the same in each.
+// The sums of a row's TPR threads: a warp puts its own down, and after a barrier each
+// warp gets them all and joins them.
 template <int TPR>
-__device__ __forceinline__ float2 row_sum(float2 v, float2 *part, int group)
+__device__ __forceinline__ void row_put(float2 v, float2 *part)
 {
-    float s = lanes_sum(v);
-    if constexpr (TPR > 32) {
-        constexpr int kWarps = TPR / 32;
-        const int lane = threadIdx.x % 32, warp = threadIdx.x % TPR / 32;
-        if (lane % 16 == 0) reinterpret_cast<float *>(part + warp)[lane / 16] = s;
-        if constexpr (TPR == kRingThreads) __syncthreads();
-        else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
-        s = lanes_sum(lane < kWarps ? part[lane] : make_float2(0.f, 0.f));
-    }
+    const float s = lanes_sum(v);
+    const int lane = threadIdx.x % 32, warp = threadIdx.x % TPR / 32;
+    if (lane % 16 == 0) reinterpret_cast<float *>(part + warp)[lane / 16] = s;
+}
+template <int TPR>
+__device__ __forceinline__ void row_barrier(int group)
+{
+    if constexpr (TPR == 32) __syncwarp();
+    else if constexpr (TPR == kRingThreads) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
+}
+template <int TPR>
+__device__ __forceinline__ float2 row_get(const float2 *part)
+{
+    const int lane = threadIdx.x % 32;
+    return lane < TPR / 32 ? part[lane] : make_float2(0.f, 0.f);
+}
+template <int TPR>
+__device__ __forceinline__ float2 row_join(float2 v)
+{
+    if constexpr (TPR == 32) return make_float2(__shfl_sync(0xffffffffu, v.x, 0), __shfl_sync(0xffffffffu, v.y, 0));
+    const float s = lanes_sum(v);
     return make_float2(__shfl_sync(0xffffffffu, s, 0), __shfl_sync(0xffffffffu, s, 16));
 }
 
 // TPR threads a row, PIECES pieces each; groups of them take rows in turn.  A thread
 // copies its own pieces of the next rows into its own places of shared memory, and
-// reads them again when it comes to the row: no barrier but the row's sum.  Where the
-// pieces are more than 8 values, the registers hold no dw and db: dx alone is made, and
-// a row's values are read and worked out once more after its sum.
+// reads them again when it comes to the row: no barrier but the row's sum.
+//   kSums   8 values a thread at most: dw and db stay in its registers, and with more
+//           dx alone is made, a row's values worked out once more after its sum.
+//   kAhead  the next row's sums are under way while this row's are joined, and its
+//           values are worked out once more for dx (2048 x 4096 BF16 17.7 us, without
+//           19.8; not where a block is one group, 8192 x 8192: 106 us, without 93, as two
+//           of the four rows in flight are then in use).
 template <typename T, int TPR, int PIECES>
 __global__ void __launch_bounds__(kRingThreads, 1) layernorm_grad_ring_kernel(const NormGradArgs a)
 {
@@ -311,6 +329,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) layernorm_grad_ring_kernel(co
     constexpr int kTensor = PIECES * kRingThreads;
     constexpr bool kSums = PIECES * kValues <= kVec;
     constexpr int kKept = kSums ? PIECES : 1;
+    constexpr bool kAhead = kSums && PIECES == 1 && TPR < kRingThreads;
     extern __shared__ __align__(16) uint8_t ring_raw[];
     __shared__ float2 part[2][kRingThreads / 32];
     uint4 *const ring = reinterpret_cast<uint4 *>(ring_raw) + threadIdx.x;   // [stage][tensor][piece][thread]
@@ -341,57 +360,118 @@ __global__ void __launch_bounds__(kRingThreads, 1) layernorm_grad_ring_kernel(co
 #pragma unroll
     for (int s = 0; s < kStages; ++s) ahead(first + s * step < M, at + s * stride, s);
     float2 dw[kKept][kPairs] = {}, db[kKept][kPairs] = {};
-    float mean = 0.f, rstd = 0.f;
-    if (first < M) mean = a.mean[first], rstd = a.rstd[first];
-    int stage = 0, turn = 0;
     const float inv = 1.f / static_cast<float>(a.K);
-    for (int row = first; row < M; row += step, at += stride, turn ^= 1) {
-        copies_wait<kStages - 1>();
-        const float2 half = {0.5f, 0.5f}, off = {-0.5f * mean, -0.5f * mean}, r = {rstd, rstd}, r2 = {2.f * rstd, 2.f * rstd};
-        if (row + step < M) mean = a.mean[row + step], rstd = a.rstd[row + step];
-        const uint4 *const from = ring + stage * 3 * kTensor;
-        float2 g[kKept][kPairs], x[kKept][kPairs], s0 = {0.f, 0.f}, s1 = {0.f, 0.f};
-        auto values = [&](int q, int to) {   // g = dy w and the normal of h; dw and db on the way
-            float2 w[kPairs];
-            pairs(from[q * kRingThreads], g[to], T{});
-            pairs(from[q * kRingThreads + kTensor], x[to], T{});
-            pairs(weight[q], w, T{});
+    struct Moments {
+        float mean, rstd;
+    };
+    auto moments_of = [&](int row) { return row < M ? Moments{a.mean[row], a.rstd[row]} : Moments{0.f, 0.f}; };
+    auto stage_of = [&](int stage) { return ring + stage * 3 * kTensor; };
+    // A row's factors, doubled for packed arithmetic.
+    struct Factors {
+        float2 off, r, r2;
+        __device__ __forceinline__ explicit Factors(Moments m)
+            : off(make_float2(-0.5f * m.mean, -0.5f * m.mean)), r(make_float2(m.rstd, m.rstd)), r2(make_float2(2.f * m.rstd, 2.f * m.rstd))
+        {
+        }
+    };
+    // g = dy w and x = the normal of h, from a stage; `first`: dw and db on the way
+    auto values = [&](const uint4 *from, const Factors &f, int q, float2 (&g)[kPairs], float2 (&x)[kPairs], const bool first) {
+        const float2 half = {0.5f, 0.5f};
+        float2 w[kPairs];
+        pairs(from[q * kRingThreads], g, T{});
+        pairs(from[q * kRingThreads + kTensor], x, T{});
+        pairs(weight[q], w, T{});
 #pragma unroll
-            for (int j = 0; j < kPairs; ++j) {
-                x[to][j] = __fmul2_rn(__ffma2_rn(half, x[to][j], off), r2);   // normal_of
-                if constexpr (kSums) {
-                    dw[to][j] = __ffma2_rn(g[to][j], x[to][j], dw[to][j]);
-                    db[to][j] = __fadd2_rn(db[to][j], g[to][j]);
+        for (int j = 0; j < kPairs; ++j) {
+            x[j] = __fmul2_rn(__ffma2_rn(half, x[j], f.off), f.r2);   // normal_of
+            if (kSums && first) {
+                float2 &w_sum = dw[kSums ? q : 0][j], &b_sum = db[kSums ? q : 0][j];
+                w_sum = __ffma2_rn(g[j], x[j], w_sum);
+                b_sum = __fadd2_rn(b_sum, g[j]);
+            }
+            g[j] = __fmul2_rn(g[j], w[j]);
+        }
+    };
+    auto output = [&](const uint4 *from, const Factors &f, int q, float2 mg, float2 mgx, const float2 (&g)[kPairs], const float2 (&x)[kPairs]) {
+        float2 o[kPairs] = {};
+        if (a.dsum) pairs(from[q * kRingThreads + 2 * kTensor], o, T{});
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) o[j] = __ffma2_rn(f.r, __ffma2_rn(x[j], mgx, __fadd2_rn(g[j], mg)), o[j]);
+        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.dx) + at + static_cast<size_t>(q) * TPR * 16) = piece(o, T{});
+    };
+    auto negated_mean = [&](float s) { return make_float2(-s * inv, -s * inv); };
+    int stage = 0, turn = 0;
+    float2 *const row_part = &part[0][group * (TPR / 32)];
+    constexpr int kParts = kRingThreads / 32;   // to the other turn's
+    if constexpr (kAhead) {
+        auto sums_of = [&](const uint4 *from, Moments m) {
+            const Factors f(m);
+            float2 s0 = {0.f, 0.f}, s1 = {0.f, 0.f}, g[kPairs], x[kPairs];
+            if (in(0)) {
+                values(from, f, 0, g, x, true);
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) {
+                    s0 = __fadd2_rn(s0, g[j]);
+                    s1 = __ffma2_rn(g[j], x[j], s1);
                 }
-                g[to][j] = __fmul2_rn(g[to][j], w[j]);
             }
+            return make_float2(s0.x + s0.y, s1.x + s1.y);
         };
-#pragma unroll
-        for (int q = 0; q < PIECES; ++q) {
-            if (!in(q)) continue;
-            const int to = kSums ? q : 0;
-            values(q, to);
-#pragma unroll
-            for (int j = 0; j < kPairs; ++j) {
-                s0 = __fadd2_rn(s0, g[to][j]);
-                s1 = __ffma2_rn(g[to][j], x[to][j], s1);
+        Moments now = moments_of(first), next = moments_of(first + step);
+        copies_wait<kStages - 1>();
+        if (first < M) row_put<TPR>(sums_of(stage_of(0), now), row_part);
+        for (int row = first; row < M; row += step, at += stride, turn ^= 1) {
+            row_barrier<TPR>(group);
+            const float2 mine = row_get<TPR>(row_part + turn * kParts);
+            const int after = stage + 1 == kStages ? 0 : stage + 1;
+            const Moments later = moments_of(row + 2 * step);
+            copies_wait<kStages - 2>();
+            float2 s_next = {0.f, 0.f};
+            if (row + step < M) s_next = sums_of(stage_of(after), next);
+            const float2 s = row_join<TPR>(mine);
+            if (row + step < M) row_put<TPR>(s_next, row_part + (turn ^ 1) * kParts);
+            if (in(0)) {
+                const Factors f(now);
+                float2 g[kPairs], x[kPairs];
+                values(stage_of(stage), f, 0, g, x, false);
+                output(stage_of(stage), f, 0, negated_mean(s.x), negated_mean(s.y), g, x);
             }
+            ahead(row + kStages * step < M, at + kStages * stride, stage);
+            stage = after;
+            now = next, next = later;
         }
-        const float2 s = row_sum<TPR>(make_float2(s0.x + s0.y, s1.x + s1.y), part[turn] + group * (TPR / 32), group);
-        const float2 mg = {-s.x * inv, -s.x * inv}, mgx = {-s.y * inv, -s.y * inv};
+    } else {
+        Moments now = moments_of(first);
+        for (int row = first; row < M; row += step, at += stride, turn ^= 1) {
+            copies_wait<kStages - 1>();
+            const Factors f(now);
+            if (row + step < M) now = {a.mean[row + step], a.rstd[row + step]};
+            const uint4 *const from = stage_of(stage);
+            float2 g[kKept][kPairs], x[kKept][kPairs], s0 = {0.f, 0.f}, s1 = {0.f, 0.f};
 #pragma unroll
-        for (int q = 0; q < PIECES; ++q) {
-            if (!in(q)) continue;
-            const int to = kSums ? q : 0;
-            if constexpr (!kSums) values(q, 0);
-            float2 o[kPairs] = {};
-            if (a.dsum) pairs(from[q * kRingThreads + 2 * kTensor], o, T{});
+            for (int q = 0; q < PIECES; ++q) {
+                if (!in(q)) continue;
+                const int to = kSums ? q : 0;
+                values(from, f, q, g[to], x[to], true);
 #pragma unroll
-            for (int j = 0; j < kPairs; ++j) o[j] = __ffma2_rn(r, __ffma2_rn(x[to][j], mgx, __fadd2_rn(g[to][j], mg)), o[j]);
-            *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.dx) + at + static_cast<size_t>(q) * TPR * 16) = piece(o, T{});
+                for (int j = 0; j < kPairs; ++j) {
+                    s0 = __fadd2_rn(s0, g[to][j]);
+                    s1 = __ffma2_rn(g[to][j], x[to][j], s1);
+                }
+            }
+            row_put<TPR>(make_float2(s0.x + s0.y, s1.x + s1.y), row_part + turn * kParts);
+            row_barrier<TPR>(group);
+            const float2 s = row_join<TPR>(row_get<TPR>(row_part + turn * kParts)), mg = negated_mean(s.x), mgx = negated_mean(s.y);
+#pragma unroll
+            for (int q = 0; q < PIECES; ++q) {
+                if (!in(q)) continue;
+                const int to = kSums ? q : 0;
+                if constexpr (!kSums) values(from, f, q, g[0], x[0], false);
+                output(from, f, q, mg, mgx, g[to], x[to]);
+            }
+            ahead(row + kStages * step < M, at + kStages * stride, stage);
+            stage = stage + 1 == kStages ? 0 : stage + 1;
         }
-        ahead(row + kStages * step < M, at + kStages * stride, stage);
-        stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     copies_wait<0>();
     if constexpr (kSums) {
