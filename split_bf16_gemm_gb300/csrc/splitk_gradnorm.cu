@@ -4,16 +4,16 @@
 //   norm = sqrt(sum over all tensors and values of g^2)
 //   out  = g f,  f = min(1, max_norm / norm), rounded once
 //
-// The tensors are cut into chunks of 8192 values (2048 where there are few) that a persistent grid takes in
-// turn.  A thread squares 32 (8) values of a chunk in F32 (four in flight) and adds that to
-// a sum of two F32 numbers, the second of which holds what the first's roundings lose.
-// A block writes one part, a number and a power of two: at most 1216 of them, which
-// every block of the second launch adds in the same order.  F64 is kept out of the
-// way: this chip does two F64 operations a clock and SM (9 tensors of 1.3 M values
-// 18 us with the parts, the root and the quotient in F64).  Squares that F32 does not
-// hold (of gradients beyond 2^50 or all below 2^-40) are taken again of the values
-// times a power of two.  The second launch goes through the chunks backwards, so that
-// it finds the last ones of the first in L2.
+// The tensors are cut into chunks of 8192 values (2048 where there are few) that a
+// grid's blocks take in turn.  A thread squares 32 (8) values of a chunk in F32 and adds
+// that to a sum of two F32 numbers, the second of which holds what the first's
+// roundings lose.  A block writes one part, a number and a power of two; they are added
+// in the same order every time.  F64 is kept out of the way: this chip does two F64
+// operations a clock and SM (9 tensors of 1.3 M values 18 us with the parts, the root
+// and the quotient in F64, 6.4 without).  Squares that F32 does not hold (of gradients
+// beyond 2^43 or all below 2^-40) are taken again of the values times a power of two.
+// The scaling goes through the chunks backwards, so that it finds the last ones of the
+// sum in L2.
 //
 // The tensors' addresses go into the kernels as parameters: no copy to the device
 // before the launch, nothing to keep for a captured graph.  Bound by memory: the
@@ -29,6 +29,7 @@ namespace splitk {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kFewParts = 4 * 152;                      // blocks for few values
 constexpr int chunk_of(int vecs) { return kThreads * vecs * kVec; }   // values, `vecs` vectors to a thread
 
 template <int N>
@@ -235,17 +236,24 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
 // The norm from the blocks' parts, as root * 2^half, in every thread.
 __device__ __forceinline__ float norm_of(const Part *parts, int blocks, int &half, Shared &shared)
 {
-    constexpr int kEach = (kGradNormParts + kThreads - 1) / kThreads;
-    Part p[kEach], mine = {0.f, kNothing};
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int at = i * kThreads + static_cast<int>(threadIdx.x);
-        p[i] = at < blocks ? parts[at] : Part{0.f, kNothing};
-        mine.e = max(mine.e, p[i].e);
-    }
+    constexpr int kAtOnce = (kFewParts + kThreads - 1) / kThreads;   // loads in flight
+    Part mine = {0.f, kNothing};
     Sum s = {0.f, 0.f};
+    for (int from = 0; from < blocks; from += kAtOnce * kThreads) {
+        Part p[kAtOnce];
+        int most = mine.e;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) add(s, p[i].m * power(p[i].e - mine.e));
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int at = from + i * kThreads + static_cast<int>(threadIdx.x);
+            p[i] = at < blocks ? parts[at] : Part{0.f, kNothing};
+            most = max(most, p[i].e);
+        }
+        const float down = power(mine.e - most);
+        s.hi *= down, s.lo *= down;
+        mine.e = most;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) add(s, p[i].m * power(p[i].e - most));
+    }
     mine.m = value(s);
     int e;
     s = block_sum(mine, e, shared);
@@ -259,30 +267,46 @@ __device__ __forceinline__ float norm_value(float root, int half)
     return half > 120 ? root * power(120) * power(min(half - 120, 127)) : half < -120 ? root * power(-120) * power(half + 120) : root * power(half);
 }
 
-__global__ void __launch_bounds__(kThreads) finish_kernel(const Part *parts, int blocks, float *norm)
+// min(1, max_norm / norm), by halves of the power: neither has to be in F32's range
+__device__ __forceinline__ float factor_of(float root, int half, float max_norm)
 {
-    __shared__ Shared shared;
-    ptx::launch_dependents();
-    ptx::grid_dependency_wait();
-    int half;
-    const float root = norm_of(parts, blocks, half, shared);
-    if (threadIdx.x == 0) *norm = norm_value(root, half);
-}
-
-template <int N, int kVecs>
-__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Table<N> t, const Part *parts, int blocks,
-                                                        float max_norm, float *norm)
-{
-    __shared__ Shared shared;
-    ptx::launch_dependents();
-    ptx::grid_dependency_wait();
-    int half;
-    const float root = norm_of(parts, blocks, half, shared);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = norm_value(root, half);
-    // max_norm / norm, by halves of the power: neither has to be in F32's range
     const int some = -half / 2;
     const float q = max_norm / root * power(some) * power(-half - some);
-    const float f = isnan(root) ? root : root != 0.f && q < 1.f ? q : 1.f;
+    return isnan(root) ? root : root != 0.f && q < 1.f ? q : 1.f;
+}
+
+// The norm, and (factor != nullptr) the factor.
+__global__ void __launch_bounds__(kThreads) finish_kernel(const Part *parts, int blocks, float *norm, float max_norm, float *factor)
+{
+    __shared__ Shared shared;
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    int half;
+    const float root = norm_of(parts, blocks, half, shared);
+    if (threadIdx.x == 0) {
+        *norm = norm_value(root, half);
+        if (factor) *factor = factor_of(root, half, max_norm);
+    }
+}
+
+// FINISHED: the factor is there, and a block takes one chunk; else every block finds the
+// norm, the first writes it, and blocks take chunks in turn.
+template <int N, int kVecs, bool FINISHED>
+__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Table<N> t, const Part *parts, int blocks,
+                                                        float max_norm, float *norm, const float *factor)
+{
+    __shared__ Shared shared;
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    float f;
+    if constexpr (FINISHED) {
+        f = *factor;
+    } else {
+        int half;
+        const float root = norm_of(parts, blocks, half, shared);
+        if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = norm_value(root, half);
+        f = factor_of(root, half, max_norm);
+    }
     const int last = t.first[t.count] - 1 - static_cast<int>(blockIdx.x);
     int at = tensor_of(t, last);
     for (int c = last; c >= 0; c -= gridDim.x) {
@@ -296,6 +320,9 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
 }
 
 constexpr int kMostTensors = 512;   // of one launch
+
+// The factor's place behind the parts.
+float *factor_at(void *parts) { return reinterpret_cast<float *>(static_cast<Part *>(parts) + kGradNormParts); }
 
 int64_t chunks_of(int64_t n, int vecs) { return (n + chunk_of(vecs) - 1) / chunk_of(vecs); }
 
@@ -312,13 +339,15 @@ cudaError_t launch(const GradNormProblem &p, int64_t begin, int64_t end, int blo
         t.dtype[i] = static_cast<uint8_t>(p.dtypes[begin + i]);
         t.first[i + 1] = t.first[i] + static_cast<int>(chunks_of(t.size[i], kVecs));
     }
+    Part *const parts = static_cast<Part *>(p.parts);
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config(static_cast<unsigned>(blocks), kThreads, stream, &attr);
-    if (clip)
-        return note_error(cudaLaunchKernelEx(&cfg, clip_kernel<N, kVecs>, t, static_cast<const Part *>(p.parts), blocks, p.max_norm,
-                                             begin == 0 ? p.norm : static_cast<float *>(nullptr)),
-                          "clip_kernel launch");
-    return note_error(cudaLaunchKernelEx(&cfg, norm_kernel<N, kVecs>, t, static_cast<Part *>(p.parts), begin ? 1 : 0), "norm_kernel launch");
+    cudaLaunchConfig_t cfg = config(static_cast<unsigned>(blocks), kThreads, stream, &attr);
+    if (!clip) return note_error(cudaLaunchKernelEx(&cfg, norm_kernel<N, kVecs>, t, parts, begin ? 1 : 0), "norm_kernel launch");
+    constexpr bool kFinished = kVecs > 1;
+    if (kFinished) cfg.gridDim.x = static_cast<unsigned>(t.first[t.count] ? t.first[t.count] : 1);
+    return note_error(cudaLaunchKernelEx(&cfg, clip_kernel<N, kVecs, kFinished>, t, static_cast<const Part *>(parts), blocks, p.max_norm,
+                                         begin == 0 ? p.norm : static_cast<float *>(nullptr), static_cast<const float *>(factor_at(p.parts))),
+                      "clip_kernel launch");
 }
 
 }  // namespace
@@ -336,27 +365,38 @@ cudaError_t launch_grad_norm(const GradNormProblem &p, cudaStream_t stream)
         }
         return most;
     };
-    // Chunks of 8192 values keep 4 loads in flight; where they are fewer than the blocks
-    // that the device holds, chunks of 2048 spread the work.
+    // Chunks of 8192 values keep 4 loads in flight, and more blocks than the device holds
+    // even out what each meets: 1.6 GB in 290 tensors 909 us with 24 blocks to an SM, 954
+    // with 8.  A block to a chunk then scales, after a launch that finds the factor for
+    // them all.  Few values: chunks of 2048, and no launch between.
     int64_t most = most_of(4);
-    const int vecs = most <= 512 ? 1 : 4;
-    if (vecs == 1) most = most_of(1);
-    const int blocks = static_cast<int>(most < kGradNormParts ? most : kGradNormParts);
-    for (int pass = 0; pass < (p.out ? 2 : 1); ++pass) {
+    const bool few = most <= 512;
+    if (few) most = most_of(1);
+    const int64_t limit = few ? kFewParts : kGradNormParts;
+    const int blocks = static_cast<int>(most < limit ? most : limit);
+    auto all = [&](bool clip) {
         int64_t begin = 0;
         do {   // (no tensors: one launch that finds nothing)
             const int64_t end = begin + kMostTensors < p.count ? begin + kMostTensors : p.count;
-            const auto go = vecs == 1 ? end - begin <= kFew ? launch<kFew, 1> : launch<kMostTensors, 1>
+            const auto go = few ? end - begin <= kFew ? launch<kFew, 1> : launch<kMostTensors, 1>
                             : end - begin <= kFew ? launch<kFew, 4> : launch<kMostTensors, 4>;
-            const cudaError_t e = go(p, begin, end, blocks, pass == 1, stream);
+            const cudaError_t e = go(p, begin, end, blocks, clip, stream);
             if (e != cudaSuccess) return e;
             begin = end;
         } while (begin < p.count);
+        return cudaSuccess;
+    };
+    const cudaError_t e = all(false);
+    if (e != cudaSuccess) return e;
+    if (!p.out || !few) {
+        cudaLaunchAttribute attr;
+        const cudaLaunchConfig_t cfg = config(1, kThreads, stream, &attr);
+        const cudaError_t f = note_error(cudaLaunchKernelEx(&cfg, finish_kernel, static_cast<const Part *>(p.parts), blocks, p.norm, p.max_norm,
+                                                            p.out ? factor_at(p.parts) : static_cast<float *>(nullptr)),
+                                         "finish_kernel launch");
+        if (f != cudaSuccess || !p.out) return f;
     }
-    if (p.out) return cudaSuccess;
-    cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config(1, kThreads, stream, &attr);
-    return note_error(cudaLaunchKernelEx(&cfg, finish_kernel, static_cast<const Part *>(p.parts), blocks, p.norm), "finish_kernel launch");
+    return all(true);
 }
 
 }  // namespace splitk

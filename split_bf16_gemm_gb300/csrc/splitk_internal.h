@@ -216,7 +216,7 @@ cudaError_t launch_layernorm_grad(const LayerNormGradProblem &p, cudaStream_t st
 
 // The norm of `count` tensors, and (out != nullptr) the tensors scaled to max_norm
 // (splitk_gradnorm.cu).  The arrays are the host's.
-constexpr int kGradNormParts = 8 * 152;         // blocks of the persistent grid
+constexpr int kGradNormParts = 24 * 152;        // blocks of the sum's grid at most
 struct GradNormProblem {
     const void *const *grads;
     void *const *out;
@@ -225,7 +225,7 @@ struct GradNormProblem {
     int64_t count;
     float max_norm;
     float *norm;
-    void *parts;                                // [kGradNormParts], 8 bytes each
+    void *parts;                                // [kGradNormParts] of 8 bytes, and 8 bytes more
 };
 cudaError_t launch_grad_norm(const GradNormProblem &p, cudaStream_t stream);
 
