@@ -366,7 +366,7 @@ cudaError_t launch_grad_norm(const GradNormProblem &p, cudaStream_t stream)
         return most;
     };
     // Chunks of 8192 values keep 4 loads in flight, and more blocks than the device holds
-    // even out what each meets: 1.6 GB in 290 tensors 909 us with 24 blocks to an SM, 954
+    // even out what each meets: 2.0 GB in 290 tensors 909 us with 24 blocks to an SM, 954
     // with 8.  A block to a chunk then scales, after a launch that finds the factor for
     // them all.  Few values: chunks of 2048, and no launch between.
     int64_t most = most_of(4);

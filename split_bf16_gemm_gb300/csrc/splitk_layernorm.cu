@@ -594,15 +594,21 @@ __global__ void __launch_bounds__(kSumThreads) layernorm_sum_kernel(const float 
     const int64_t c = static_cast<int64_t>(blockIdx.x) * kSumLanes + lane;
     float sum = 0.f;
     if (c < 2 * static_cast<int64_t>(K)) {
-        constexpr int kAtOnce = 10;   // loads in flight: two rounds for 152 parts
-        for (int b = slice; b < blocks; b += kAtOnce * kSumSlices) {
+        constexpr int kAtOnce = 8;   // loads in flight
+        int b = slice;
+        for (; b + (kAtOnce - 1) * kSumSlices < blocks; b += kAtOnce * kSumSlices) {
             float x[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i)
-                x[i] = b + i * kSumSlices < blocks ? parts[static_cast<size_t>(b + i * kSumSlices) * 2 * K + c] : 0.f;
+            for (int i = 0; i < kAtOnce; ++i) x[i] = parts[static_cast<size_t>(b + i * kSumSlices) * 2 * K + c];
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) sum += x[i];
         }
+        float x[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce - 1; ++i)
+            x[i] = b + i * kSumSlices < blocks ? parts[static_cast<size_t>(b + i * kSumSlices) * 2 * K + c] : 0.f;
+#pragma unroll
+        for (int i = 0; i < kAtOnce - 1; ++i) sum += x[i];
     }
     part[slice][lane] = sum;
     __syncthreads();
@@ -695,13 +701,14 @@ cudaError_t launch_layernorm(const LayerNormProblem &p, cudaStream_t stream)
 
 int64_t layernorm_grad_parts(int64_t M, int64_t K)
 {
-    // A block to an SM, as few as the same number of turns takes (333 rows of 5120 F16: 111
-    // blocks 9.9 us, 152 blocks 10.6).  Long rows have columns for many blocks of
-    // kColumnThreads, and fewer parts the longer they are.
+    // A block to an SM, and of four turns and more as few as take the same number (4096
+    // rows of 1024 BF16: 128 blocks 11.5 us, 152 blocks 13.4; 333 rows of 5120 F16, three
+    // turns: 111 blocks and the norm before them 17.0, 152 blocks 16.0).  Long rows have
+    // columns for many blocks of kColumnThreads, and fewer parts the longer they are.
     const int64_t vecs = K / kVec, rows = vecs <= kRingVecs ? kRingThreads / ring_row_threads(vecs) : 1;
     const int64_t across = (vecs + kColumnThreads - 1) / kColumnThreads, tiles = (M + rows - 1) / rows;
     const int64_t most = vecs <= kRingVecs ? kSmCount : across >= 40 ? 8 : across <= 5 ? 64 : 320 / across, turns = (tiles + most - 1) / most;
-    return turns ? (tiles + turns - 1) / turns : 0;
+    return turns >= 4 ? (tiles + turns - 1) / turns : tiles < most ? tiles : most;
 }
 
 cudaError_t launch_layernorm_grad(const LayerNormGradProblem &p, cudaStream_t stream)
