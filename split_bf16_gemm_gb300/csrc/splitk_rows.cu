@@ -325,14 +325,15 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchArgs a
             return;
         }
     }
-    // Vectors on their way while the rows are found.  (After the sort's launch: it lets
-    // this one start when what was before it is done, so x is there.)
+    // Vectors on their way while the rows are found.  (After a sort: it lets this launch
+    // start when what was before the sort is done, so x is there; read from L2, as this
+    // SM's L1 may hold what x was before that.)
     const uint4 *const x = a.x + static_cast<int64_t>(m) * a.vecs;
     constexpr int kAhead = 2;
     uint4 p[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-        if (static_cast<int>(threadIdx.x) + i * kThreads < a.vecs) p[i] = x[threadIdx.x + i * kThreads];
+        if (static_cast<int>(threadIdx.x) + i * kThreads < a.vecs) p[i] = __ldcg(x + threadIdx.x + i * kThreads);
     if constexpr (!HERE) {
         ptx::grid_dependency_wait();
         ptx::launch_dependents();
@@ -593,7 +594,7 @@ cudaError_t launch_sort(const DispatchProblem &p, cudaStream_t stream)
     const size_t smem = static_cast<size_t>(kSortWarps + 2) * G * sizeof(int);
     auto *const kernel = G <= 16 ? sort_for<4>(each) : G <= 64 ? sort_for<6>(each) : G <= 256 ? sort_for<8>(each) : sort_for<10>(each);
     cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024) e = allow_smem(kernel);
+    if (smem > 40 * 1024) e = allow_smem(kernel);   // (48 KB without, static shared memory included)
     if (e == cudaSuccess && blocks > 8)
         e = note_error(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), "sort_kernel cluster size");
     if (e != cudaSuccess) return e;

@@ -201,6 +201,17 @@ def test_sort_of_any_entries(sk, T, G):
         assert o.intact() and s.intact() and src.intact()
 
 
+@pytest.mark.parametrize("G", [15, 16, 17, 63, 64, 65, 255, 256, 257, 293, 301, 302, 341, 353, *range(357, 364), 511, 512, 513, 1023])
+def test_sort_with_any_number_of_experts(sk, G):
+    """The ends of what a launch takes shared memory and bits for."""
+    for T in (900, 2500, 17000):
+        e = torch.randint(0, G, (T, 1), device="cuda", generator=gen(G)).int()
+        o, s, src = guarded((G + 1,), INT), guarded((T, 1), INT), guarded((T,), INT)
+        sk.moe_sort(e, o.data, s.data, src.data, T, 1, G)
+        check_sort(e, G, o.data, s.data, src.data)
+        assert o.intact() and s.intact() and src.intact()
+
+
 def test_sort_of_no_tokens_gives_empty_runs(sk):
     for G in (1, 33, 1024):
         o = guarded((G + 1,), INT)
