@@ -227,12 +227,11 @@ struct NormGradArgs {
 __device__ __forceinline__ float normal_of(float h, float half_mean, float rstd2) { return fmaf(0.5f, h, -half_mean) * rstd2; }
 
 
-// ---- rows of up to 8192 values: copies into shared memory ahead of the sums
+// ---- rows in shared memory ahead of their sums
 
-constexpr int kRingThreads = 1024;
 constexpr int kSmCount = 152;
 
-// A thread takes pieces of 16 bytes of a row, piece q at (thread + q TPR) pieces.
+// A thread takes pieces of 16 bytes of a row, piece q at (thread + q row threads).
 template <typename T>
 constexpr int piece_values()
 {
@@ -240,17 +239,8 @@ constexpr int piece_values()
 }
 
 // Rows in flight for each thread: what 192 KB of shared memory hold of dy, h and dsum.
-template <int PIECES>
-constexpr int ring_stages()
-{
-    return 4 / PIECES;
-}
-
-template <int PIECES>
-constexpr size_t ring_bytes()
-{
-    return static_cast<size_t>(ring_stages<PIECES>()) * 3 * PIECES * kRingThreads * 16;
-}
+constexpr size_t kRingBytes = 192 * 1024;
+constexpr int ring_stages(int threads, int pieces) { return static_cast<int>(kRingBytes / (3 * 16 * threads * pieces)); }
 
 __device__ __forceinline__ void copy_ahead(uint4 *dst, const uint8_t *src)
 {
@@ -283,223 +273,134 @@ __device__ __forceinline__ uint4 piece(const float2 (&v)[4], T)
     return packed<T>(v).a;
 }
 
-// The sums of a row's TPR threads: a warp puts its own down, and after a barrier each
-// warp gets them all and joins them.
-template <int TPR>
-__device__ __forceinline__ void row_put(float2 v, float2 *part)
+// `threads` a row: whole warps, or 8 or 16 lanes (SMALL); groups of them take rows in
+// turn.  A thread copies its own pieces of the next rows into its own places of shared
+// memory, and reads them again when it comes to the row: no barrier but the row's sum.
+// SUMS: dw and db of the thread's columns stay in its registers; else dx alone is made.
+template <typename T, int THREADS, int PIECES, bool SUMS, bool SMALL>
+__global__ void __launch_bounds__(THREADS, 1) layernorm_grad_ring_kernel(const NormGradArgs a, const int threads)
 {
-    const float s = lanes_sum(v);
-    const int lane = threadIdx.x % 32, warp = threadIdx.x % TPR / 32;
-    if (lane % 16 == 0) reinterpret_cast<float *>(part + warp)[lane / 16] = s;
-}
-template <int TPR>
-__device__ __forceinline__ void row_barrier(int group)
-{
-    if constexpr (TPR == 32) __syncwarp();
-    else if constexpr (TPR == kRingThreads) __syncthreads();
-    else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
-}
-template <int TPR>
-__device__ __forceinline__ float2 row_get(const float2 *part)
-{
-    const int lane = threadIdx.x % 32;
-    return lane < TPR / 32 ? part[lane] : make_float2(0.f, 0.f);
-}
-template <int TPR>
-__device__ __forceinline__ float2 row_join(float2 v)
-{
-    if constexpr (TPR == 32) return make_float2(__shfl_sync(0xffffffffu, v.x, 0), __shfl_sync(0xffffffffu, v.y, 0));
-    const float s = lanes_sum(v);
-    return make_float2(__shfl_sync(0xffffffffu, s, 0), __shfl_sync(0xffffffffu, s, 16));
-}
-
-// TPR threads a row, PIECES pieces each; groups of them take rows in turn.  A thread
-// copies its own pieces of the next rows into its own places of shared memory, and
-// reads them again when it comes to the row: no barrier but the row's sum.
-//   kSums   8 values a thread at most: dw and db stay in its registers, and with more
-//           dx alone is made, a row's values worked out once more after its sum.
-//   kAhead  the next row's sums are under way while this row's are joined, and its
-//           values are worked out once more for dx (2048 x 4096 BF16 17.7 us, without
-//           19.8; not where a block is one group, 8192 x 8192: 106 us, without 93, as two
-//           of the four rows in flight are then in use).
-template <typename T, int TPR, int PIECES>
-__global__ void __launch_bounds__(kRingThreads, 1) layernorm_grad_ring_kernel(const NormGradArgs a)
-{
-    constexpr int kGroups = kRingThreads / TPR, kStages = ring_stages<PIECES>(), kValues = piece_values<T>(), kPairs = kValues / 2;
-    constexpr int kTensor = PIECES * kRingThreads;
-    constexpr bool kSums = PIECES * kValues <= kVec;
-    constexpr int kKept = kSums ? PIECES : 1;
-    constexpr bool kAhead = kSums && PIECES == 1 && TPR < kRingThreads;
+    constexpr int kStages = ring_stages(THREADS, PIECES), kValues = piece_values<T>(), kPairs = kValues / 2, kTensor = PIECES * THREADS;
+    constexpr int kWarps = THREADS / 32, kOwn = SUMS ? PIECES : 1;
     extern __shared__ __align__(16) uint8_t ring_raw[];
-    __shared__ float2 part[2][kRingThreads / 32];
+    __shared__ float2 part[2][kWarps];
     uint4 *const ring = reinterpret_cast<uint4 *>(ring_raw) + threadIdx.x;   // [stage][tensor][piece][thread]
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
-    const int group = threadIdx.x / TPR, v = threadIdx.x % TPR, pieces = a.K / kValues;
-    auto in = [&](int q) { return v + q * TPR < pieces; };
-    // rows are counted in 32 bits (M <= 2^22), their addresses by a running offset
-    const int M = static_cast<int>(a.M), step = static_cast<int>(gridDim.x) * kGroups, first = static_cast<int>(blockIdx.x) * kGroups + group;
+    const int groups = static_cast<int>(blockDim.x) / threads, group = threadIdx.x / threads, v = threadIdx.x % threads;
+    const int lane = threadIdx.x % 32, warps = threads / 32, pieces = a.K / kValues;
+    auto in = [&](int q) { return v + q * threads < pieces; };
+    // rows are counted in 32 bits (M <= 2^22), their addresses by a running offset; every
+    // thread goes through the same number of turns
+    const int M = static_cast<int>(a.M), step = static_cast<int>(gridDim.x) * groups, first = static_cast<int>(blockIdx.x) * groups + group;
     const size_t stride = static_cast<size_t>(step) * pieces * 16;
     size_t at = (static_cast<size_t>(first) * pieces + v) * 16;
-    uint4 weight[PIECES];
+    float2 w[PIECES][kPairs] = {};
 #pragma unroll
     for (int q = 0; q < PIECES; ++q)
-        if (in(q)) weight[q] = static_cast<const uint4 *>(a.weight)[v + q * TPR];
+        if (in(q)) pairs(static_cast<const uint4 *>(a.weight)[v + q * threads], w[q], T{});
     auto ahead = [&](bool there, size_t from, int stage) {
+        uint4 *const to = ring + stage * 3 * kTensor;
 #pragma unroll
         for (int q = 0; q < PIECES; ++q) {
             if (!in(q) || !there) continue;
-            uint4 *const to = ring + stage * 3 * kTensor + q * kRingThreads;
-            const size_t f = from + static_cast<size_t>(q) * TPR * 16;
-            copy_ahead(to, static_cast<const uint8_t *>(a.dy) + f);
-            copy_ahead(to + kTensor, static_cast<const uint8_t *>(a.h) + f);
-            if (a.dsum) copy_ahead(to + 2 * kTensor, static_cast<const uint8_t *>(a.dsum) + f);
+            const size_t f = from + static_cast<size_t>(q * threads) * 16;
+            copy_ahead(to + q * THREADS, static_cast<const uint8_t *>(a.dy) + f);
+            copy_ahead(to + q * THREADS + kTensor, static_cast<const uint8_t *>(a.h) + f);
+            if (a.dsum) copy_ahead(to + q * THREADS + 2 * kTensor, static_cast<const uint8_t *>(a.dsum) + f);
         }
         copies_commit();
     };
 #pragma unroll
     for (int s = 0; s < kStages; ++s) ahead(first + s * step < M, at + s * stride, s);
-    float2 dw[kKept][kPairs] = {}, db[kKept][kPairs] = {};
-    const float inv = 1.f / static_cast<float>(a.K);
-    struct Moments {
-        float mean, rstd;
-    };
-    auto moments_of = [&](int row) { return row < M ? Moments{a.mean[row], a.rstd[row]} : Moments{0.f, 0.f}; };
-    auto stage_of = [&](int stage) { return ring + stage * 3 * kTensor; };
-    // A row's factors, doubled for packed arithmetic.
-    struct Factors {
-        float2 off, r, r2;
-        __device__ __forceinline__ explicit Factors(Moments m)
-            : off(make_float2(-0.5f * m.mean, -0.5f * m.mean)), r(make_float2(m.rstd, m.rstd)), r2(make_float2(2.f * m.rstd, 2.f * m.rstd))
-        {
-        }
-    };
-    // g = dy w and x = the normal of h, from a stage; `first`: dw and db on the way
-    auto values = [&](const uint4 *from, const Factors &f, int q, float2 (&g)[kPairs], float2 (&x)[kPairs], const bool first) {
-        const float2 half = {0.5f, 0.5f};
-        float2 w[kPairs];
-        pairs(from[q * kRingThreads], g, T{});
-        pairs(from[q * kRingThreads + kTensor], x, T{});
-        pairs(weight[q], w, T{});
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
-            x[j] = __fmul2_rn(__ffma2_rn(half, x[j], f.off), f.r2);   // normal_of
-            if (kSums && first) {
-                float2 &w_sum = dw[kSums ? q : 0][j], &b_sum = db[kSums ? q : 0][j];
-                w_sum = __ffma2_rn(g[j], x[j], w_sum);
-                b_sum = __fadd2_rn(b_sum, g[j]);
-            }
-            g[j] = __fmul2_rn(g[j], w[j]);
-        }
-    };
-    auto output = [&](const uint4 *from, const Factors &f, int q, float2 mg, float2 mgx, const float2 (&g)[kPairs], const float2 (&x)[kPairs]) {
-        float2 o[kPairs] = {};
-        if (a.dsum) pairs(from[q * kRingThreads + 2 * kTensor], o, T{});
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) o[j] = __ffma2_rn(f.r, __ffma2_rn(x[j], mgx, __fadd2_rn(g[j], mg)), o[j]);
-        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.dx) + at + static_cast<size_t>(q) * TPR * 16) = piece(o, T{});
-    };
-    auto negated_mean = [&](float s) { return make_float2(-s * inv, -s * inv); };
+    float2 dw[kOwn][kPairs] = {}, db[kOwn][kPairs] = {};
+    float mean = 0.f, rstd = 0.f;
+    if (first < M) mean = a.mean[first], rstd = a.rstd[first];
     int stage = 0, turn = 0;
-    float2 *const row_part = &part[0][group * (TPR / 32)];
-    constexpr int kParts = kRingThreads / 32;   // to the other turn's
-    if constexpr (kAhead) {
-        auto sums_of = [&](const uint4 *from, Moments m) {
-            const Factors f(m);
-            float2 s0 = {0.f, 0.f}, s1 = {0.f, 0.f}, g[kPairs], x[kPairs];
-            if (in(0)) {
-                values(from, f, 0, g, x, true);
-#pragma unroll
-                for (int j = 0; j < kPairs; ++j) {
-                    s0 = __fadd2_rn(s0, g[j]);
-                    s1 = __ffma2_rn(g[j], x[j], s1);
-                }
-            }
-            return make_float2(s0.x + s0.y, s1.x + s1.y);
-        };
-        Moments now = moments_of(first), next = moments_of(first + step);
+    const float inv = 1.f / static_cast<float>(a.K);
+    const int blocks_first = static_cast<int>(blockIdx.x) * groups;
+    for (int row0 = blocks_first, row = first; row0 < M; row0 += step, row += step, at += stride, turn ^= 1) {
+        const bool live = row < M;
         copies_wait<kStages - 1>();
-        if (first < M) row_put<TPR>(sums_of(stage_of(0), now), row_part);
-        for (int row = first; row < M; row += step, at += stride, turn ^= 1) {
-            row_barrier<TPR>(group);
-            const float2 mine = row_get<TPR>(row_part + turn * kParts);
-            const int after = stage + 1 == kStages ? 0 : stage + 1;
-            const Moments later = moments_of(row + 2 * step);
-            copies_wait<kStages - 2>();
-            float2 s_next = {0.f, 0.f};
-            if (row + step < M) s_next = sums_of(stage_of(after), next);
-            const float2 s = row_join<TPR>(mine);
-            if (row + step < M) row_put<TPR>(s_next, row_part + (turn ^ 1) * kParts);
-            if (in(0)) {
-                const Factors f(now);
-                float2 g[kPairs], x[kPairs];
-                values(stage_of(stage), f, 0, g, x, false);
-                output(stage_of(stage), f, 0, negated_mean(s.x), negated_mean(s.y), g, x);
-            }
-            ahead(row + kStages * step < M, at + kStages * stride, stage);
-            stage = after;
-            now = next, next = later;
-        }
-    } else {
-        Moments now = moments_of(first);
-        for (int row = first; row < M; row += step, at += stride, turn ^= 1) {
-            copies_wait<kStages - 1>();
-            const Factors f(now);
-            if (row + step < M) now = {a.mean[row + step], a.rstd[row + step]};
-            const uint4 *const from = stage_of(stage);
-            float2 g[kKept][kPairs], x[kKept][kPairs], s0 = {0.f, 0.f}, s1 = {0.f, 0.f};
-#pragma unroll
-            for (int q = 0; q < PIECES; ++q) {
-                if (!in(q)) continue;
-                const int to = kSums ? q : 0;
-                values(from, f, q, g[to], x[to], true);
-#pragma unroll
-                for (int j = 0; j < kPairs; ++j) {
-                    s0 = __fadd2_rn(s0, g[to][j]);
-                    s1 = __ffma2_rn(g[to][j], x[to][j], s1);
-                }
-            }
-            row_put<TPR>(make_float2(s0.x + s0.y, s1.x + s1.y), row_part + turn * kParts);
-            row_barrier<TPR>(group);
-            const float2 s = row_join<TPR>(row_get<TPR>(row_part + turn * kParts)), mg = negated_mean(s.x), mgx = negated_mean(s.y);
-#pragma unroll
-            for (int q = 0; q < PIECES; ++q) {
-                if (!in(q)) continue;
-                const int to = kSums ? q : 0;
-                if constexpr (!kSums) values(from, f, q, g[0], x[0], false);
-                output(from, f, q, mg, mgx, g[to], x[to]);
-            }
-            ahead(row + kStages * step < M, at + kStages * stride, stage);
-            stage = stage + 1 == kStages ? 0 : stage + 1;
-        }
-    }
-    copies_wait<0>();
-    if constexpr (kSums) {
-        // Column k of dw, then of db; several groups' through shared memory, in their order.
-        constexpr int kRow = TPR * PIECES * kValues;
-        float *const to = a.parts + static_cast<size_t>(blockIdx.x) * 2 * a.K;
-        float *const sums = kGroups == 1 ? to : reinterpret_cast<float *>(ring_raw) + group * 2 * kRow;   // [group][2][kRow]
-        const int width = kGroups == 1 ? a.K : kRow;
-        if constexpr (kGroups > 1) __syncthreads();
+        const float2 half = {0.5f, 0.5f}, off = {-0.5f * mean, -0.5f * mean}, r = {rstd, rstd}, r2 = {2.f * rstd, 2.f * rstd};
+        if (row + step < M) mean = a.mean[row + step], rstd = a.rstd[row + step];
+        const uint4 *const from = ring + stage * 3 * kTensor;
+        float2 g[PIECES][kPairs], x[PIECES][kPairs], s0 = {0.f, 0.f}, s1 = {0.f, 0.f};
 #pragma unroll
         for (int q = 0; q < PIECES; ++q) {
-            if (kGroups == 1 && !in(q)) continue;
-            const int k = (v + q * TPR) * kValues;
+            if (!in(q) || !live) continue;
+            pairs(from[q * THREADS], g[q], T{});
+            pairs(from[q * THREADS + kTensor], x[q], T{});
 #pragma unroll
-            for (int j = 0; j < kPairs; j += 2) {
-                *reinterpret_cast<float4 *>(sums + k + 2 * j) = make_float4(dw[q][j].x, dw[q][j].y, dw[q][j + 1].x, dw[q][j + 1].y);
-                *reinterpret_cast<float4 *>(sums + width + k + 2 * j) = make_float4(db[q][j].x, db[q][j].y, db[q][j + 1].x, db[q][j + 1].y);
+            for (int j = 0; j < kPairs; ++j) {
+                x[q][j] = __fmul2_rn(__ffma2_rn(half, x[q][j], off), r2);   // normal_of
+                if constexpr (SUMS) {
+                    dw[q][j] = __ffma2_rn(g[q][j], x[q][j], dw[q][j]);
+                    db[q][j] = __fadd2_rn(db[q][j], g[q][j]);
+                }
+                g[q][j] = __fmul2_rn(g[q][j], w[q][j]);
+                s0 = __fadd2_rn(s0, g[q][j]);
+                s1 = __ffma2_rn(g[q][j], x[q][j], s1);
             }
         }
-        if constexpr (kGroups > 1) {
-            __syncthreads();
-            for (int c = threadIdx.x; c < 2 * kRow; c += kRingThreads) {
-                float sum = 0.f;
-#pragma unroll 8
-                for (int i = 0; i < kGroups; ++i) sum += reinterpret_cast<float *>(ring_raw)[i * 2 * kRow + c];
-                const int which = c / kRow, k = c % kRow;
-                if (k < a.K) to[which * a.K + k] = sum;
+        float2 s = make_float2(s0.x + s0.y, s1.x + s1.y);
+        if constexpr (SMALL) {
+            __syncwarp();
+            for (int d = threads / 2; d; d >>= 1) {
+                s.x += __shfl_xor_sync(0xffffffffu, s.x, d);
+                s.y += __shfl_xor_sync(0xffffffffu, s.y, d);
             }
+        } else {
+            __syncwarp();
+            float t = lanes_sum(s);
+            if (warps > 1) {
+                float2 *const mine = part[turn] + group * warps;
+                if (lane % 16 == 0) reinterpret_cast<float *>(mine + v / 32)[lane / 16] = t;
+                asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+                t = lanes_sum(lane < warps ? mine[lane] : make_float2(0.f, 0.f));
+            }
+            s = make_float2(__shfl_sync(0xffffffffu, t, 0), __shfl_sync(0xffffffffu, t, 16));
+        }
+        const float2 mg = {-s.x * inv, -s.x * inv}, mgx = {-s.y * inv, -s.y * inv};
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) {
+            if (!in(q) || !live) continue;
+            float2 o[kPairs] = {};
+            if (a.dsum) pairs(from[q * THREADS + 2 * kTensor], o, T{});
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) o[j] = __ffma2_rn(r, __ffma2_rn(x[q][j], mgx, __fadd2_rn(g[q][j], mg)), o[j]);
+            *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.dx) + at + static_cast<size_t>(q * threads) * 16) = piece(o, T{});
+        }
+        ahead(row + kStages * step < M, at + kStages * stride, stage);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    copies_wait<0>();
+    if constexpr (SUMS) {
+        // Column k of dw, then of db: the groups' through shared memory, in their order.
+        const int width = threads * PIECES * kValues;
+        float *const to = a.parts + static_cast<size_t>(blockIdx.x) * 2 * a.K, *const sums = reinterpret_cast<float *>(ring_raw);
+        const bool single = groups == 1;
+        float *const mine = single ? to : sums + group * 2 * width;   // [group][2][width]
+        const int db_at = single ? a.K : width;
+        if (!single) __syncthreads();
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) {
+            if (single && !in(q)) continue;
+            const int k = (v + q * threads) * kValues;
+#pragma unroll
+            for (int j = 0; j < kPairs; j += 2) {
+                *reinterpret_cast<float4 *>(mine + k + 2 * j) = make_float4(dw[q][j].x, dw[q][j].y, dw[q][j + 1].x, dw[q][j + 1].y);
+                *reinterpret_cast<float4 *>(mine + db_at + k + 2 * j) = make_float4(db[q][j].x, db[q][j].y, db[q][j + 1].x, db[q][j + 1].y);
+            }
+        }
+        if (single) return;
+        __syncthreads();
+        for (int c = threadIdx.x; c < 2 * width; c += static_cast<int>(blockDim.x)) {
+            float sum = 0.f;
+#pragma unroll 4
+            for (int i = 0; i < groups; ++i) sum += sums[i * 2 * width + c];
+            const int which = c >= width, k = c - which * width;
+            if (k < a.K) to[which * a.K + k] = sum;
         }
     }
 }
@@ -624,7 +525,17 @@ constexpr int kLongVecs = 2048;   // vectors of the longest row that a block's r
 constexpr int kRingVecs = 1024;   // the same for the ring with dw and db
 constexpr int kColumnThreads = 512;
 
-int ring_row_threads(int64_t vecs) { return vecs <= 32 ? 32 : vecs <= 128 ? 128 : vecs <= 256 ? 256 : vecs <= 512 ? 512 : 1024; }
+// How the ring takes rows of `vecs` vectors: two a thread, rows side by side.
+struct RingShape {
+    int threads;   // of a row: 8 or 16 lanes, or whole warps
+    int rows;      // side by side
+};
+RingShape ring_shape(int64_t vecs)
+{
+    const int64_t n = (vecs + 1) / 2;
+    const int threads = n <= 8 ? 8 : n <= 16 ? 16 : static_cast<int>((n + 31) / 32 * 32);
+    return {threads, 512 / threads};
+}
 
 template <typename T, int THREADS, int VPT, bool LONG = false>
 cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream)
@@ -651,30 +562,26 @@ cudaError_t launch_norm_type(const NormArgs &a, cudaStream_t stream)
     return launch_norm<T, 512, 4, true>(a, stream);
 }
 
-template <typename T, int TPR, int PIECES = kVec / piece_values<T>()>
-cudaError_t launch_ring(const NormGradArgs &a, int blocks, cudaStream_t stream)
+template <typename T, int THREADS, int VECS, bool SUMS, bool SMALL>
+cudaError_t launch_ring(const NormGradArgs &a, int blocks, RingShape shape, cudaStream_t stream)
 {
-    const cudaError_t e = note_error(cudaFuncSetAttribute(layernorm_grad_ring_kernel<T, TPR, PIECES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                          static_cast<int>(ring_bytes<PIECES>())),
+    auto *const kernel = layernorm_grad_ring_kernel<T, THREADS, VECS * kVec / piece_values<T>(), SUMS, SMALL>;
+    const cudaError_t e = note_error(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingBytes)),
                                      "layernorm_grad_ring_kernel shared memory");
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
-    cudaLaunchConfig_t cfg = config(static_cast<unsigned>(blocks), kRingThreads, stream, &attr);
-    cfg.dynamicSmemBytes = ring_bytes<PIECES>();
-    return note_error(cudaLaunchKernelEx(&cfg, layernorm_grad_ring_kernel<T, TPR, PIECES>, a), "layernorm_grad_ring_kernel launch");
+    cudaLaunchConfig_t cfg = config(static_cast<unsigned>(blocks), static_cast<unsigned>(shape.rows * shape.threads), stream, &attr);
+    cfg.dynamicSmemBytes = kRingBytes;
+    return note_error(cudaLaunchKernelEx(&cfg, kernel, a, shape.threads), "layernorm_grad_ring_kernel launch");
 }
 
 template <typename T>
 cudaError_t launch_grad_type(const NormGradArgs &a, int blocks, cudaStream_t stream)
 {
     if (a.vecs <= kRingVecs) {
-        switch (ring_row_threads(a.vecs)) {
-        case 32: return launch_ring<T, 32>(a, blocks, stream);
-        case 128: return launch_ring<T, 128>(a, blocks, stream);
-        case 256: return launch_ring<T, 256>(a, blocks, stream);
-        case 512: return launch_ring<T, 512>(a, blocks, stream);
-        default: return launch_ring<T, 1024>(a, blocks, stream);
-        }
+        const RingShape shape = ring_shape(a.vecs);
+        if (shape.threads < 32) return launch_ring<T, 512, 2, true, true>(a, blocks, shape, stream);
+        return launch_ring<T, 512, 2, true, false>(a, blocks, shape, stream);
     }
     constexpr int kThreads = kColumnThreads;
     cudaLaunchAttribute attr;
@@ -684,7 +591,8 @@ cudaError_t launch_grad_type(const NormGradArgs &a, int blocks, cudaStream_t str
     cudaError_t e = note_error(cudaLaunchKernelEx(&cfg, layernorm_grad_columns_kernel<T, kThreads>, a), "layernorm_grad_columns_kernel launch");
     if (e != cudaSuccess) return e;
     if constexpr (sizeof(T) == 2)
-        if (a.vecs <= 2 * kRingVecs) return launch_ring<T, 1024, 2>(a, static_cast<int>(a.M < kSmCount ? a.M : kSmCount), stream);
+        if (a.vecs <= 2 * kRingVecs)
+            return launch_ring<T, 512, 4, false, false>(a, static_cast<int>(a.M < kSmCount ? a.M : kSmCount), {512, 1}, stream);
     cfg.gridDim = dim3(static_cast<unsigned>(a.M), 1, 1);
     return note_error(cudaLaunchKernelEx(&cfg, layernorm_grad_long_kernel<T, kThreads>, a), "layernorm_grad_long_kernel launch");
 }
@@ -705,7 +613,7 @@ int64_t layernorm_grad_parts(int64_t M, int64_t K)
     // rows of 1024 BF16: 128 blocks 11.5 us, 152 blocks 13.4; 333 rows of 5120 F16, three
     // turns: 111 blocks and the norm before them 17.0, 152 blocks 16.0).  Long rows have
     // columns for many blocks of kColumnThreads, and fewer parts the longer they are.
-    const int64_t vecs = K / kVec, rows = vecs <= kRingVecs ? kRingThreads / ring_row_threads(vecs) : 1;
+    const int64_t vecs = K / kVec, rows = vecs <= kRingVecs ? ring_shape(vecs).rows : 1;
     const int64_t across = (vecs + kColumnThreads - 1) / kColumnThreads, tiles = (M + rows - 1) / rows;
     const int64_t most = vecs <= kRingVecs ? kSmCount : across >= 40 ? 8 : across <= 5 ? 64 : 320 / across, turns = (tiles + most - 1) / most;
     return turns >= 4 ? (tiles + turns - 1) / turns : tiles < most ? tiles : most;
