@@ -13,9 +13,10 @@
 // Blocks take rows in turn; a thread keeps the same columns for all its rows and
 // their dw and db in registers.  A second launch adds the blocks' parts in order.
 //
-// Longer rows than a block's registers hold dw and db of have them from a launch of
-// their own, which reads dy and h once more, and the longest are read twice for dx.
-// Bound by memory.
+// Rows longer than 8192 have dw and db from a launch of their own, which reads dy and h
+// once more, and rows longer than 16384 are read twice for dx (the norm: longer than
+// 16384, or 32768 of 16 bits).  GB300: 8192 x 8192 BF16 with the residual 80 us, 6.7 TB/s
+// (the copy rate), one row of 2048 1.8 us in a graph.
 
 #include <math.h>
 
@@ -277,6 +278,13 @@ __device__ __forceinline__ uint4 piece(const float2 (&v)[4], T)
 // turn.  A thread copies its own pieces of the next rows into its own places of shared
 // memory, and reads them again when it comes to the row: no barrier but the row's sum.
 // SUMS: dw and db of the thread's columns stay in its registers; else dx alone is made.
+//
+// 16 values a thread, 32 without SUMS: what a row costs besides its values (the sum's
+// exchanges and barrier, addresses, factors) is most of the instructions with 8 (8192
+// rows of 5120 BF16 71 us, with 16 67), and spills cost more than they save (640
+// threads: 89).  Bound by memory where rows stand side by side (16384 x 4096 BF16 87 us,
+// 0.92 of the copy rate), else by the wait for each row's sum (8192 x 8192 BF16 90 us,
+// 0.89; 8192 x 5120 67, 0.75).
 template <typename T, int THREADS, int PIECES, bool SUMS, bool SMALL>
 __global__ void __launch_bounds__(THREADS, 1) layernorm_grad_ring_kernel(const NormGradArgs a, const int threads)
 {
@@ -590,9 +598,8 @@ cudaError_t launch_grad_type(const NormGradArgs &a, int blocks, cudaStream_t str
     cfg.gridDim = dim3(static_cast<unsigned>((a.vecs + kThreads - 1) / kThreads), static_cast<unsigned>(blocks), 1);
     cudaError_t e = note_error(cudaLaunchKernelEx(&cfg, layernorm_grad_columns_kernel<T, kThreads>, a), "layernorm_grad_columns_kernel launch");
     if (e != cudaSuccess) return e;
-    if constexpr (sizeof(T) == 2)
-        if (a.vecs <= 2 * kRingVecs)
-            return launch_ring<T, 512, 4, false, false>(a, static_cast<int>(a.M < kSmCount ? a.M : kSmCount), {512, 1}, stream);
+    if (a.vecs <= 2 * kRingVecs)
+        return launch_ring<T, 512, 4, false, false>(a, static_cast<int>(a.M < kSmCount ? a.M : kSmCount), {512, 1}, stream);
     cfg.gridDim = dim3(static_cast<unsigned>(a.M), 1, 1);
     return note_error(cudaLaunchKernelEx(&cfg, layernorm_grad_long_kernel<T, kThreads>, a), "layernorm_grad_long_kernel launch");
 }

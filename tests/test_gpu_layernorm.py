@@ -150,7 +150,8 @@ def check_backward(sk, dy, h, w, mean, rstd, dsum, dtype, scale=False):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("M,K", ROWS + [(1500, 136), (2000, 1032), (309, 8192), (333, 512), (170, 12288), (150, 16392), (40, 400008)])
+@pytest.mark.parametrize("M,K", ROWS + [(1500, 136), (2000, 1032), (309, 8192), (333, 512), (170, 12288), (150, 16392), (40, 400008),
+                                        (40003, 72), (20001, 136), (9001, 264), (2503, 2056), (700, 5120), (321, 16384)])
 def test_layernorm_grad(sk, M, K, dtype):
     g = gen(M * 17 + K)
     h, w = (2 * randn(g, M, K) + 0.5).to(DT[dtype]), (1 + 0.3 * randn(g, K)).to(DT[dtype])
