@@ -151,7 +151,7 @@ def check_backward(sk, dy, h, w, mean, rstd, dsum, dtype, scale=False):
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("M,K", ROWS + [(1500, 136), (2000, 1032), (309, 8192), (333, 512), (170, 12288), (150, 16392), (40, 400008),
-                                        (40003, 72), (20001, 136), (9001, 264), (2503, 2056), (700, 5120), (321, 16384)])
+                                        (40003, 72), (20001, 136), (9001, 264), (2503, 2056), (700, 5120), (321, 16384), (1 << 22, 8)])
 def test_layernorm_grad(sk, M, K, dtype):
     g = gen(M * 17 + K)
     h, w = (2 * randn(g, M, K) + 0.5).to(DT[dtype]), (1 + 0.3 * randn(g, K)).to(DT[dtype])
@@ -246,6 +246,20 @@ def check_clip(sk, grads, most):
     for t, o in zip(grads, out):
         assert torch.equal(t, o.data)
     return want
+
+
+def test_some_in_place(sk):
+    g = gen(11)
+    grads = gradients(g, [5000, 33, 70000], ["f32", "bf16", "f16"])
+    kept, want = [t.clone() for t in grads], exact_norm(grads)
+    other = [torch.empty_like(t) for t in grads]
+    nbytes = sk.grad_norm_workspace_bytes()
+    ws, norm = torch.empty(nbytes, dtype=torch.uint8, device="cuda"), torch.empty(1, device="cuda")
+    sk.grad_clip(grads, want / 4, norm, ws, nbytes, out=[grads[0], other[1], grads[2]])
+    for got, k, name in ((grads[0], kept[0], "f32"), (other[1], kept[1], "bf16"), (grads[2], kept[2], "f16")):
+        within(got, k.double() / 4, (NORM + 2 * U) * k.double().abs() / 4, name)
+    assert torch.equal(grads[1], kept[1])
+    sk.grad_clip([grads[0], other[1]], 1e9, norm, ws, nbytes, out=[grads[0], other[0][:33].bfloat16()])   # a factor of 1, one in place
 
 
 SETS = [[1], [8], [7, 0, 1], [8191, 8192, 8193], [3] * 40, [100003], [1 << 20, 5, 1 << 18, 77], [129] * 600, [1 + 37 * i % 999 for i in range(1100)]]

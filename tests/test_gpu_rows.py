@@ -363,6 +363,34 @@ def test_rows_beyond_32_bits(sk):
     assert torch.equal(drows[s.flatten()[at].long()], 2 * x[at // top])
 
 
+def test_the_most_tokens(sk):
+    """2^22 tokens of one entry each, short rows: through route, dispatch and back."""
+    M, G, K = 1 << 22, 3, 8
+    g = gen(2)
+    logits = randn(g, M, G)
+    e, s, dl = torch.empty(M, 1, dtype=INT, device="cuda"), torch.empty(M, 1, device="cuda"), torch.empty(M, G, device="cuda")
+    sk.moe_route(logits, e, s, M, G, 1, "f32")
+    p = torch.softmax(logits.double(), 1)
+    assert torch.equal(e[:, 0].long(), logits.argmax(1))
+    within(s, p.amax(1, keepdim=True), 96 * U * p.amax(1, keepdim=True))
+    ones = torch.ones(M, 1, device="cuda")
+    sk.moe_route_grad(logits, e, ones, dl, M, G, 1, "f32")
+    top = p.gather(1, e.long())
+    want = -p * top
+    want.scatter_add_(1, e.long(), top)
+    within(dl, want, 256 * U * (p * top).clamp(min=0) + 256 * U * top * torch.zeros_like(p).scatter(1, e.long(), 1.0))
+    x = randn(g, M, K).half()
+    o, sl, src = torch.empty(G + 1, dtype=INT, device="cuda"), torch.empty(M, 1, dtype=INT, device="cuda"), torch.empty(M, dtype=INT, device="cuda")
+    rows, back, ds = torch.empty_like(x), torch.empty_like(x), torch.empty(M, 1, device="cuda")
+    sk.moe_dispatch(e, x, o, sl, src, rows, M, 1, G, K, "f16")
+    assert torch.equal(rows, x[src.long()]) and o.tolist() == [0, *torch.bincount(e.flatten(), minlength=G).cumsum(0).tolist()]
+    sk.moe_combine(rows, sl, None, back, M, 1, K, "f16", "f16")
+    assert torch.equal(back, x)
+    sk.moe_combine_grad(x, rows, sl, None, None, ds, M, 1, K, "f16")
+    size = x.double().square().sum(1, keepdim=True)
+    within(ds, size, 16 * U * size)
+
+
 # ------------------------------------------------------------------ together
 
 class Layer:
