@@ -102,10 +102,10 @@ typedef enum {
     SPLITK_ERR_ALIAS = -4,          /* an output range overlaps an input or another output */
     SPLITK_ERR_ALIGN = -5,          /* a pointer is not 16-byte aligned */
     SPLITK_ERR_DTYPE = -6,          /* unknown element type */
-    SPLITK_ERR_WORKSPACE = -7,      /* workspace smaller than gemm_bt_workspace_bytes() */
+    SPLITK_ERR_WORKSPACE = -7,      /* workspace smaller than the call's ..._workspace_bytes() */
     SPLITK_ERR_CUDA = -8,           /* a CUDA runtime call or launch failed */
     SPLITK_ERR_DEVICE_TIMEOUT = -9, /* a kernel's bounded wait ran out (see splitk_get_device_status) */
-    SPLITK_ERR_CONFIG = -10         /* an invalid tile override */
+    SPLITK_ERR_CONFIG = -10         /* an invalid value (tile override, eps, max_norm, a mode) */
 } splitk_status;
 
 #define SPLITK_MAX_DIM (1 << 22)

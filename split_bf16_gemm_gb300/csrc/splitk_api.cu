@@ -567,9 +567,9 @@ const char *splitk_status_string(int status)
     case SPLITK_ERR_SHAPE: return "a size breaks the call's rules (gemm_bt: M, K and k_per_split positive multiples of 32, N of 64) or limits";
     case SPLITK_ERR_SPLIT: return "splits must equal ceil(K / k_per_split): every split starts below K and they cover K";
     case SPLITK_ERR_ALIAS: return "an output range overlaps an input or another output";
-    case SPLITK_ERR_ALIGN: return "pointers must be 16-byte aligned";
+    case SPLITK_ERR_ALIGN: return "pointers must be 16-byte aligned (int32 tensors and the norm: 4-byte)";
     case SPLITK_ERR_DTYPE: return "unknown element type";
-    case SPLITK_ERR_WORKSPACE: return "workspace smaller than gemm_bt_workspace_bytes()";
+    case SPLITK_ERR_WORKSPACE: return "workspace smaller than the call needs (its ..._workspace_bytes())";
     case SPLITK_ERR_CUDA: return "a CUDA call or kernel launch failed";
     case SPLITK_ERR_DEVICE_TIMEOUT: return "a bounded wait inside a kernel ran out";
     case SPLITK_ERR_CONFIG: return "invalid configuration value";
