@@ -520,16 +520,18 @@ class GradList:
     grad_clip take them.  Keeps the tensors alive; made once, used every step."""
 
     def __init__(self, tensors):
+        import torch
+
+        codes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
         self.tensors = list(tensors)
-        n = max(len(self.tensors), 1)
-        for t in self.tensors:
-            if not t.is_contiguous():
-                raise ValueError("a gradient is not contiguous")
-        self.pointers = pointer_array(self.tensors)
-        self.sizes = (ctypes.c_int64 * n)(*(t.numel() for t in self.tensors))
-        self.dtypes = (ctypes.c_int * n)(*(dtype_code(t.dtype) for t in self.tensors))
         self.count = len(self.tensors)
-        self.kinds = tuple(self.sizes), tuple(self.dtypes)
+        n = max(self.count, 1)
+        if not all(t.is_contiguous() for t in self.tensors):
+            raise ValueError("a gradient is not contiguous")
+        sizes, dtypes = [t.numel() for t in self.tensors], [codes[t.dtype] for t in self.tensors]
+        self.pointers = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.tensors])
+        self.sizes, self.dtypes = (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*dtypes)
+        self.kinds = sizes, dtypes
 
 
 def grad_list(tensors) -> GradList:

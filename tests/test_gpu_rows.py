@@ -536,6 +536,59 @@ def test_streams_and_threads(sk):
             assert torch.equal(t, getattr(layer, n)), n
 
 
+def test_large_calls_at_once(sk):
+    """Clusters of 16 blocks, rings that fill an SM and grids over all SMs, from four
+    threads on their own streams: the bits of a single one."""
+    class Work:
+        def __init__(self, i):
+            g = gen(40 + i)
+            self.M, self.top, self.G, self.K = 6000 + 700 * i, 4, 300 + i, 520
+            M, K, T = self.M, self.K, self.M * 4
+            self.e, self.x = choose(g, M, 4, self.G, 17), randn(g, M, K).bfloat16()
+            self.o, self.s, self.src = (torch.empty(n, dtype=INT, device="cuda") for n in (self.G + 1, T, T))
+            self.rows, self.back = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda"), torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+            self.w, self.mean, self.rstd = torch.ones(K, device="cuda").bfloat16(), torch.zeros(M, device="cuda"), torch.ones(M, device="cuda")
+            self.dx, self.dw, self.db = torch.empty_like(self.back), torch.empty(K, device="cuda"), torch.empty(K, device="cuda")
+            self.nbytes = sk.layernorm_grad_workspace_bytes(M, K)
+            self.ws, self.gws = torch.empty(self.nbytes, dtype=torch.uint8, device="cuda"), torch.empty(sk.grad_norm_workspace_bytes(), dtype=torch.uint8, device="cuda")
+            self.norm, self.out = torch.empty(1, device="cuda"), [torch.empty_like(self.rows), torch.empty_like(self.dw)]
+
+        def step(self):
+            M, top, K = self.M, self.top, self.K
+            sk.moe_sort(self.e, self.o, self.s, self.src, M, top, self.G)
+            sk.moe_dispatch(self.e, self.x, self.o, self.s, self.src, self.rows, M, top, self.G, K, "bf16")
+            sk.moe_combine(self.rows, self.s, None, self.back, M, top, K, "bf16", "bf16")
+            sk.layernorm_grad(self.back, self.x, self.w, self.mean, self.rstd, self.dx, self.dw, self.db, self.ws, self.nbytes, M, K, "bf16")
+            sk.grad_clip([self.rows, self.dw], 3.0, self.norm, self.gws, sk.grad_norm_workspace_bytes(), out=self.out)
+
+        def outputs(self):
+            return [t.clone() for t in (self.o, self.s, self.src, self.rows, self.back, self.dx, self.dw, self.db, self.norm, *self.out)]
+
+    works, want, failed = [Work(i) for i in range(4)], [], []
+    for w in works:
+        w.step()
+        want.append(w.outputs())
+    torch.cuda.synchronize()
+
+    def run(w):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(8):
+                    w.step()
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(w,)) for w in works]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for w, kept in zip(works, want):
+        assert all(torch.equal(a, b) for a, b in zip(kept, w.outputs()))
+
+
 def test_captured_beside_the_split_k_product(sk):
     """Layer norm, a split-K product of its output, route of the product's rows, and back
     through the norm, captured in one graph: the eager bits."""
