@@ -13,7 +13,7 @@
 // choices of many logits, the lanes' maxima are taken first: the top-th largest of
 // them is a bound that at least `top` logits reach and few others.  Those that reach it
 // are moved to a lane each, in the order of their indexes, and a lane counts how many
-// are before its own (8192 tokens, 256 experts, top 8: 5.7 us, by choices alone 10.8).
+// are before its own (8192 tokens, 256 experts, top 8: 5.4 us, by choices alone 10.8).
 //
 // Gradient, with p = softmax over all G (or over the chosen; p = 0 elsewhere) and
 // c = sum_j p_{e_j} d_j:   dl_i = p_i (sum_{j: e_j = i} d_j - c).
@@ -32,19 +32,18 @@ namespace {
 
 constexpr int kRouteThreads = 256;
 
-// A number that rises with the logit; -inf has 0, and NaN the largest.  (-0 + 0 is
-// +0: the two zeros are equal.)
+// A number that rises with the logit; -inf has 0, and a NaN the largest.  (x + 0: -0 is
+// +0, the two zeros are equal, and any NaN is the positive one.)
+constexpr uint32_t kBelow = 0x007fffffu;   // what -inf would have
 __device__ __forceinline__ uint32_t key_of(float x)
 {
-    if (isnan(x)) return 0xffffffffu;
-    const uint32_t u = __float_as_uint(x + 0.f);
-    const uint32_t k = u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
-    return k == 0x007fffffu ? 0u : k;   // -inf
+    const uint32_t u = __float_as_uint(__fadd_rn(x, 0.f));
+    return (u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u)) - kBelow;
 }
 __device__ __forceinline__ float logit_of(uint32_t k)
 {
-    if (k == 0) return -INFINITY;
-    return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xffffffffu));
+    const uint32_t u = k + kBelow;
+    return __uint_as_float(u >> 31 ? u ^ 0x80000000u : ~u);
 }
 
 __device__ __forceinline__ float sum_of(float x)

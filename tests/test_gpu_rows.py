@@ -133,6 +133,19 @@ def test_route_extremes(sk):
     assert d[:2].isnan().all() and d[2:4].eq(0).all() and d[4].abs().max() < 16 * U
 
 
+@pytest.mark.parametrize("dtype,bits", [("f32", (0x7fc00000, -0x400000, 0x7f800001, -1)), ("f16", (0x7e00, -0x200, 0x7c01, -1)), ("bf16", (0x7fc0, -0x40, 0x7f81, -1))])
+@pytest.mark.parametrize("G", [9, 200])
+def test_route_takes_any_nan_for_the_largest(sk, G, dtype, bits):
+    whole = {"f32": torch.int32, "f16": torch.int16, "bf16": torch.int16}[dtype]
+    for b in bits:
+        logits = randn(gen(1), 3, G).to(DT[dtype])
+        logits[:, 3] = math.inf
+        logits.view(whole)[1, 7] = b
+        e, s = torch.empty(3, 4, dtype=INT, device="cuda"), torch.empty(3, 4, device="cuda")
+        sk.moe_route(logits, e, s, 3, G, 4, dtype)
+        assert e[:, 0].tolist() == [3, 7, 3] and e[1, 1] == 3 and s.isnan().all()
+
+
 def test_route_gradient_of_repeated_and_foreign_experts(sk):
     """An expert that is there twice counts twice; one outside [0, G) is passed over."""
     M, G, top = 2, 6, 5
