@@ -203,8 +203,9 @@ __global__ void __launch_bounds__(THREADS == 32 ? kRowThreads : THREADS) layerno
         outputs(false);
     } else {
         // deviations whose squares F32 does not hold: the row times a power of two,
-        // which the norm cancels
-        if (var < 1.f) wide = 0x1p100f;
+        // which the norm cancels.  (Small ones times 2^90: the squares of 2^22 values
+        // whose variance is below 2^-80 add up to 2^122 at most, and 2^-149's is 2^-118.)
+        if (var < 1.f) wide = 0x1p90f;
         else scale = 0x1p-80f;
         moments(true, part[2]);
         outputs(true);
