@@ -10,7 +10,7 @@ torch = pytest.importorskip("torch")
 
 import rows_reference as ref  # noqa: E402
 from rows_reference import DT, U, within  # noqa: E402
-from test_gpu_fp8_grouped import gen, randn, sk  # noqa: E402,F401
+from test_gpu_fp8_grouped import Guarded, gen, randn, sk  # noqa: E402,F401
 from test_gpu_layernorm import EPS, check_backward, check_forward, forward, row_terms  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -114,3 +114,17 @@ def test_spread_of_a_few_steps(sk, K, value):
     within(y, want, 2 * U * (c * (1 + n.abs() + n.abs().mean(1, keepdim=True)) * w.double().abs() + b.double().abs()))
     within(mean, m, 2 * U * (m.abs() + c / r))
     within(rstd, r, (c + 8) * U * r)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,K", [(3, 72), (5, 1024), (4, 2048), (3, 8200), (2, 16392), (2, 50008)])
+def test_the_input_in_its_own_place(sk, M, K, dtype):
+    """`sum` without a residual receives x: as x itself, and elsewhere (guarded)."""
+    g = gen(K)
+    x, w = (2 * randn(g, M, K) + 3).to(DT[dtype]), (1 + 0.3 * randn(g, K)).to(DT[dtype])
+    y, mean, rstd, _ = forward(sk, x, None, w, None, dtype)
+    own, other = x.clone(), Guarded((M, K), DT[dtype])
+    for place in (own, other.data):
+        z, m, r, total = forward(sk, own, None, w, None, dtype, in_place=place)
+        assert torch.equal(total, x) and torch.equal(z, y) and torch.equal(m, mean) and torch.equal(r, rstd)
+    assert other.intact()
