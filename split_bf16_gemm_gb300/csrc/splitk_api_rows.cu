@@ -271,7 +271,7 @@ int layernorm_grad(const void *dy, const void *h, const void *weight, const floa
         {dy, h, weight, dsum, mean, rstd, dx, dweight, dbias, static_cast<float *>(workspace), M, K, dtype}, static_cast<cudaStream_t>(stream)));
 }
 
-size_t grad_norm_workspace_bytes(void) { return (splitk::kGradNormParts + 1) * 8; }
+size_t grad_norm_workspace_bytes(void) { return (splitk::kGradNormParts + 1) * 8 + splitk::kGradNormParts * 4; }
 
 int grad_norm(const void *const *grads, const int64_t *sizes, const int *dtypes, int64_t count, float *norm, void *workspace,
               size_t workspace_bytes, void *stream)

@@ -7,11 +7,12 @@
 // The tensors are cut into chunks of 8192 values (2048 where there are few) that a
 // grid's blocks take in turn.  A thread squares 32 (8) values of a chunk in F32 and adds
 // that to a sum of two F32 numbers, the second of which holds what the first's
-// roundings lose.  A block writes one part, a number and a power of two; they are added
-// in the same order every time.  F64 is kept out of the way: this chip does two F64
-// operations a clock and SM (9 tensors of 1.3 M values 18 us with the parts, the root
-// and the quotient in F64, 6.4 without).  Squares that F32 does not hold (of gradients
-// beyond 2^43 or all below 2^-40) are taken again of the values times a power of two.
+// roundings lose.  A block writes one part, a number and a power of two; further launches
+// add to it, and keep what that loses beside it.  Parts are added in the same order every
+// time.  F64 is kept out of the way: this chip does two F64 operations a clock and SM (9
+// tensors of 1.3 M values 18 us with the parts, the root and the quotient in F64, 6.4
+// without).  Squares that F32 does not hold (of gradients beyond 2^43 or all below 2^-40)
+// are taken again of the values times a power of two.
 // The scaling goes through the chunks backwards, so that it finds the last ones of the
 // sum in L2.
 //
@@ -202,8 +203,10 @@ __device__ __forceinline__ int tensor_of(const Table<N> &t, int c)
     return lo;
 }
 
+// `lows`: behind the parts what their additions lose, where there are launches that add to
+// them (else nullptr; `more`: this is one).
 template <int N, int kVecs>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<N> t, Part *parts, int more)
+__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<N> t, Part *parts, float *lows, int more)
 {
     __shared__ Shared shared;
     ptx::launch_dependents();
@@ -224,17 +227,26 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     const Sum s = block_sum(mine, e, shared);
     if (threadIdx.x == 0) {
         Part p = {value(s), e};
-        if (more) {
-            const Part q = parts[blockIdx.x];
-            p.e = max(e, q.e);
-            p.m = p.m * power(e - p.e) + q.m * power(q.e - p.e);
+        if (lows) {
+            Sum both = {0.f, 0.f};
+            if (more) {
+                const Part q = parts[blockIdx.x];
+                p.e = max(e, q.e);
+                const float down = power(q.e - p.e);
+                both = {q.m * down, lows[blockIdx.x] * down};
+                add(both, p.m * power(e - p.e));
+                p.m = both.hi;
+            }
+            lows[blockIdx.x] = both.lo;
         }
         parts[blockIdx.x] = p;
     }
 }
 
-// The norm from the blocks' parts, as root * 2^half, in every thread.
-__device__ __forceinline__ float norm_of(const Part *parts, int blocks, int &half, Shared &shared)
+// The norm from the blocks' parts, as root * 2^half, in every thread.  MORE: several
+// launches made them.
+template <bool MORE>
+__device__ __forceinline__ float norm_of(const Part *parts, const float *lows, int blocks, int &half, Shared &shared)
 {
     constexpr int kAtOnce = (kFewParts + kThreads - 1) / kThreads;   // loads in flight
     Part mine = {0.f, kNothing};
@@ -253,6 +265,13 @@ __device__ __forceinline__ float norm_of(const Part *parts, int blocks, int &hal
         mine.e = most;
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) add(s, p[i].m * power(p[i].e - most));
+        if (MORE) {
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int at = from + i * kThreads + static_cast<int>(threadIdx.x);
+                if (at < blocks) s.lo += lows[at] * power(p[i].e - most);
+            }
+        }
     }
     mine.m = value(s);
     int e;
@@ -276,13 +295,15 @@ __device__ __forceinline__ float factor_of(float root, int half, float max_norm)
 }
 
 // The norm, and (factor != nullptr) the factor.
-__global__ void __launch_bounds__(kThreads) finish_kernel(const Part *parts, int blocks, float *norm, float max_norm, float *factor)
+template <bool MORE>
+__global__ void __launch_bounds__(kThreads) finish_kernel(const Part *parts, const float *lows, int blocks, float *norm, float max_norm,
+                                                          float *factor)
 {
     __shared__ Shared shared;
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     int half;
-    const float root = norm_of(parts, blocks, half, shared);
+    const float root = norm_of<MORE>(parts, lows, blocks, half, shared);
     if (threadIdx.x == 0) {
         *norm = norm_value(root, half);
         if (factor) *factor = factor_of(root, half, max_norm);
@@ -291,9 +312,9 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const Part *parts, int
 
 // FINISHED: the factor is there, and a block takes one chunk; else every block finds the
 // norm, the first writes it, and blocks take chunks in turn.
-template <int N, int kVecs, bool FINISHED>
-__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Table<N> t, const Part *parts, int blocks,
-                                                        float max_norm, float *norm, const float *factor)
+template <int N, int kVecs, bool FINISHED, bool MORE>
+__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Table<N> t, const Part *parts, const float *lows,
+                                                        int blocks, float max_norm, float *norm, const float *factor)
 {
     __shared__ Shared shared;
     ptx::launch_dependents();
@@ -303,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
         f = *factor;
     } else {
         int half;
-        const float root = norm_of(parts, blocks, half, shared);
+        const float root = norm_of<MORE>(parts, lows, blocks, half, shared);
         if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = norm_value(root, half);
         f = factor_of(root, half, max_norm);
     }
@@ -321,12 +342,15 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
 
 constexpr int kMostTensors = 512;   // of one launch
 
-// The factor's place behind the parts.
+// The factor's place behind the parts, and behind that what their additions lose where
+// several launches make them.
 float *factor_at(void *parts) { return reinterpret_cast<float *>(static_cast<Part *>(parts) + kGradNormParts); }
+bool several(const GradNormProblem &p) { return p.count > kMostTensors; }
+float *lows_of(const GradNormProblem &p) { return several(p) ? factor_at(p.parts) + 2 : nullptr; }
 
 int64_t chunks_of(int64_t n, int vecs) { return (n + chunk_of(vecs) - 1) / chunk_of(vecs); }
 
-template <int N, int kVecs>
+template <int N, int kVecs, bool MORE = false>
 cudaError_t launch(const GradNormProblem &p, int64_t begin, int64_t end, int blocks, bool clip, cudaStream_t stream)
 {
     Table<N> t;
@@ -342,10 +366,11 @@ cudaError_t launch(const GradNormProblem &p, int64_t begin, int64_t end, int blo
     Part *const parts = static_cast<Part *>(p.parts);
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = config(static_cast<unsigned>(blocks), kThreads, stream, &attr);
-    if (!clip) return note_error(cudaLaunchKernelEx(&cfg, norm_kernel<N, kVecs>, t, parts, begin ? 1 : 0), "norm_kernel launch");
+    if (!clip) return note_error(cudaLaunchKernelEx(&cfg, norm_kernel<N, kVecs>, t, parts, lows_of(p), begin ? 1 : 0), "norm_kernel launch");
     constexpr bool kFinished = kVecs > 1;
     if (kFinished) cfg.gridDim.x = static_cast<unsigned>(t.first[t.count] ? t.first[t.count] : 1);
-    return note_error(cudaLaunchKernelEx(&cfg, clip_kernel<N, kVecs, kFinished>, t, static_cast<const Part *>(parts), blocks, p.max_norm,
+    return note_error(cudaLaunchKernelEx(&cfg, clip_kernel<N, kVecs, kFinished, MORE>, t, static_cast<const Part *>(parts),
+                                         static_cast<const float *>(lows_of(p)), blocks, p.max_norm,
                                          begin == 0 ? p.norm : static_cast<float *>(nullptr), static_cast<const float *>(factor_at(p.parts))),
                       "clip_kernel launch");
 }
@@ -378,7 +403,8 @@ cudaError_t launch_grad_norm(const GradNormProblem &p, cudaStream_t stream)
         int64_t begin = 0;
         do {   // (no tensors: one launch that finds nothing)
             const int64_t end = begin + kMostTensors < p.count ? begin + kMostTensors : p.count;
-            const auto go = few ? end - begin <= kFew ? launch<kFew, 1> : launch<kMostTensors, 1>
+            const auto go = several(p) ? few ? launch<kMostTensors, 1, true> : launch<kMostTensors, 4, true>
+                            : few ? end - begin <= kFew ? launch<kFew, 1> : launch<kMostTensors, 1>
                             : end - begin <= kFew ? launch<kFew, 4> : launch<kMostTensors, 4>;
             const cudaError_t e = go(p, begin, end, blocks, clip, stream);
             if (e != cudaSuccess) return e;
@@ -391,7 +417,8 @@ cudaError_t launch_grad_norm(const GradNormProblem &p, cudaStream_t stream)
     if (!p.out || !few) {
         cudaLaunchAttribute attr;
         const cudaLaunchConfig_t cfg = config(1, kThreads, stream, &attr);
-        const cudaError_t f = note_error(cudaLaunchKernelEx(&cfg, finish_kernel, static_cast<const Part *>(p.parts), blocks, p.norm, p.max_norm,
+        const cudaError_t f = note_error(cudaLaunchKernelEx(&cfg, several(p) ? finish_kernel<true> : finish_kernel<false>, static_cast<const Part *>(p.parts),
+                                                            static_cast<const float *>(lows_of(p)), blocks, p.norm, p.max_norm,
                                                             p.out ? factor_at(p.parts) : static_cast<float *>(nullptr)),
                                          "finish_kernel launch");
         if (f != cudaSuccess || !p.out) return f;

@@ -225,7 +225,7 @@ struct GradNormProblem {
     int64_t count;
     float max_norm;
     float *norm;
-    void *parts;                                // [kGradNormParts] of 8 bytes, and 8 bytes more
+    void *parts;                                // [kGradNormParts] of 8 bytes, 8 bytes more, [kGradNormParts] F32
 };
 cudaError_t launch_grad_norm(const GradNormProblem &p, cudaStream_t stream);
 
