@@ -24,7 +24,8 @@ struct Range {
     uintptr_t lo, hi;   // [lo, hi)
 };
 
-inline bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
+// (An empty range overlaps nothing.)
+inline bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
 
 inline Range range_of(const void *p, uint64_t bytes)
 {
