@@ -565,9 +565,10 @@ int moe_combine_grad(const void *dout, const void *rows, const int32_t *slots,
  *   sum           device, [M,K] or NULL: receives h; may be exactly x or residual
  *   y             device, [M,K], rounded once from F32
  *   mean, rstd    device, F32 [M] or NULL: what layernorm_grad takes
- * Finite rows of any size have their norm, also where the squares leave F32's
- * range; a row that holds a NaN or an infinity is NaN.  eps >= 0 (else
- * SPLITK_ERR_CONFIG); with eps = 0 a row of equal values is 0 / 0. */
+ * Finite rows of any size have their norm, also where the sum or the squares leave
+ * F32's range; a row that holds a NaN or an infinity is NaN.  eps >= 0 (else
+ * SPLITK_ERR_CONFIG); with eps = 0 a row of equal values is 0 / 0, and the rstd of
+ * one whose deviations are below 2^-128 is infinite. */
 int layernorm(const void *x, const void *residual, const void *weight,
               const void *bias, void *sum, void *y, float *mean, float *rstd,
               int64_t M, int64_t K, float eps, int dtype, void *stream);
@@ -580,7 +581,8 @@ size_t layernorm_grad_workspace_bytes(int64_t M, int64_t K);
  *   dweight = sum_m dy * n,  dbias = sum_m dy
  *   dy          device, [M,K]
  *   h           device, [M,K]: the norm's input (`sum`, or x without a residual)
- *   mean, rstd  device, F32 [M], from layernorm
+ *   mean, rstd  device, F32 [M], from layernorm (n is that of the rounded mean;
+ *               rstd below 2^127)
  *   dsum        device, [M,K] or NULL: the gradient that reaches h besides
  *   dx          device, [M,K], rounded once: the gradient of x and of the
  *               residual; may be exactly dy or dsum
@@ -617,8 +619,9 @@ int grad_norm(const void *const *grads, const int64_t *sizes, const int *dtypes,
  *   out[i] = grads[i] * min(1, max_norm / norm)   rounded once
  *   out  device pointers of the same sizes and types, or NULL for grads (in
  *        place; so may any single out[i]); no other overlap, and no tensor twice
- * With a NaN norm every value becomes NaN, with an infinite one 0 (infinities
- * NaN).  max_norm finite and >= 0, else SPLITK_ERR_CONFIG. */
+ * With a NaN gradient every value becomes NaN, with an infinite one 0 (infinities
+ * NaN).  Finite gradients are scaled to max_norm also where F32 does not hold their
+ * norm (`norm` is infinite then).  max_norm finite and >= 0, else SPLITK_ERR_CONFIG. */
 int grad_clip(void *const *grads, void *const *out, const int64_t *sizes,
               const int *dtypes, int64_t count, float max_norm, float *norm,
               void *workspace, size_t workspace_bytes, void *stream);
