@@ -517,7 +517,10 @@ def layernorm_grad(dy, h, weight, mean, rstd, dx, dweight, dbias, workspace, wor
 
 class GradList:
     """The addresses, sizes and types of a model's gradients, as grad_norm and
-    grad_clip take them.  Keeps the tensors alive; made once, used every step."""
+    grad_clip take them.  Made once for gradients that stay where they are and used
+    every step; it keeps those tensors alive, and knows nothing of new ones.  Where a
+    step replaces the gradients (set to None in between, as torch's zero_grad does
+    unless told otherwise), or moves one, make a list anew or pass the tensors."""
 
     def __init__(self, tensors):
         import torch
