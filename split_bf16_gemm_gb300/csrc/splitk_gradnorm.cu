@@ -393,7 +393,9 @@ cudaError_t launch_grad_norm(const GradNormProblem &p, cudaStream_t stream)
     // Chunks of 8192 values keep 4 loads in flight, and more blocks than the device holds
     // even out what each meets: 2.0 GB in 290 tensors 909 us with 24 blocks to an SM, 954
     // with 8.  A block to a chunk then scales, after a launch that finds the factor for
-    // them all.  Few values: chunks of 2048, and no launch between.
+    // them all.  Few values: chunks of 2048, and no launch between (clipping with and
+    // without it, F32: 1 M values 7.8 and 7.4 us, 2 M 8.0 and 11.3, 4 M 10.6 and 15.4, 8 M 17.0
+    // and 17.4, 32 M 67 and 66; the norm alone 4.3 and 3.6, 5.9 and 4.7 of 4 M, 7.6 and 6.3 of 8).
     int64_t most = most_of(4);
     const bool few = most <= 512;
     if (few) most = most_of(1);

@@ -15,8 +15,8 @@
 // their dw and db in registers.  A second launch adds the blocks' parts in order.
 //
 // Rows longer than 8192 have dw and db from a launch of their own, which reads dy and h
-// once more, and rows longer than 16384 are read twice for dx (the norm: longer than
-// 16384, or 32768 of 16 bits).  GB300: 8192 x 8192 BF16 with the residual 80 us, 6.7 TB/s
+// once more, and rows longer than 16384 are read twice for dx.  The norm reads rows longer
+// than 16384 (32768 of 16 bits) three times: for the mean, the deviations and y.  GB300: 8192 x 8192 BF16 with the residual 80 us, 6.7 TB/s
 // (the copy rate), one row of 2048 1.8 us in a graph.
 
 #include <math.h>
@@ -590,6 +590,12 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream)
     return note_error(cudaLaunchKernelEx(&cfg, layernorm_kernel<T, THREADS, VPT, LONG>, a), "layernorm_kernel launch");
 }
 
+// Measured with the residual, BF16, in us, the other shapes beside it (threads x vectors):
+// 100000 x 256 35 (128 x 1 102), 60000 x 512 37 (128 x 1 63; one of 64 rows 2.1 and 1.7), 60000 x
+// 1024 71 (32 x 4 73, 64 x 2 72; 64 rows 1.7, 3.0, 2.0), 30000 x 2048 75 (128 x 2 71, 64 x 4 72; 64
+// rows 1.9, 2.0, 2.7), 20000 x 2560 67 (512 x 1 91, 128 x 4 60), 16384 x 4096 78 (91, 79), 12000 x
+// 6144 86 (512 x 2 97, 1024 x 1 159), 8192 x 8192 79 (512 x 2 80, 1024 x 1 120), 4096 x 16384 80
+// (1024 x 2 120).
 template <typename T>
 cudaError_t launch_norm_type(const NormArgs &a, cudaStream_t stream)
 {

@@ -10,8 +10,9 @@
 // find one another, one of them adds), the warps' counts become sums over the
 // warps, the blocks' over the cluster through distributed shared memory, the
 // experts' a scan; then each warp goes over its entries once more and knows every
-// entry's row.  One launch, no workspace, no atomics on memory: the same bits
-// every time.
+// entry's row.  One launch (and one that writes `source`, where it is asked for
+// without rows and more than 16384 entries), no workspace, no atomics on memory: the
+// same bits every time.
 //
 // dispatch_kernel: a token's row is read once and written to each of its rows.
 // For up to 2048 entries every block finds the rows of its own tokens by
@@ -219,7 +220,10 @@ struct DispatchArgs {
     int M, top, G, vecs, blocks;
 };
 
-constexpr int kHere = 2048;   // most entries that every block sorts by itself
+// Most entries that every block sorts by itself (rows of 2048 BF16, by themselves and
+// behind a sort: 1024 entries 3.5 and 5.0 us, 2048 as 512 tokens 5.1 and 6.2, as 256 tokens of
+// 256 experts 6.8 and 6.5).
+constexpr int kHere = 2048;
 constexpr int kMaxTop = 32;   // SPLITK_MAX_TOP
 
 // The block's token: where its entries go, by comparison with every entry, E of them
@@ -528,7 +532,9 @@ cudaError_t launch_combine_grad_type(const CombineArgs &a, cudaStream_t stream)
 {
     cudaLaunchAttribute attr;
     // Small blocks, so that their sums' barriers meet less often at once (8192 tokens of
-    // 2048 BF16, top 8: 85 us, with 8 warps 93); few tokens take all the warps they can.
+    // 2048 BF16, top 8: 85 us, with 8 warps 93); few tokens take all the warps they can (16
+    // and 4 warps: 304 tokens 4.5 and 5.9 us, 600 6.6 and 8.6, 1003 10.9 and 10.3, 2000 21 and
+    // 19; rows of 1544, top 3: 152 tokens 2.2 and 2.6, 600 3.6 and 4.0, 1003 4.7 and 4.9).
     const int units = (a.vecs + 31) / 32, most = a.M <= 2 * 152 ? kGradThreads / 32 : 4, turns = (units + most - 1) / most;
     const cudaLaunchConfig_t cfg = config(static_cast<unsigned>(a.M), static_cast<unsigned>((units + turns - 1) / turns * 32), stream, &attr);
     return note_error(cudaLaunchKernelEx(&cfg, combine_grad_kernel<T>, a), "combine_grad_kernel launch");
