@@ -85,8 +85,8 @@ __device__ __forceinline__ float2 block_sum(float2 v, float2 *part)
     return v;
 }
 
-// Whether F32 holds the squares that v + eps is made of.
-__device__ __forceinline__ bool in_range(float v) { return v >= 0x1p-80f && v <= 0x1p120f; }
+// The variances (with eps, and without) whose squares F32 holds as they are.
+constexpr float kLeast = 0x1p-80f, kMost = 0x1p120f;
 
 constexpr int kRowThreads = 256;   // of a block with a row to a warp
 
@@ -188,8 +188,8 @@ __global__ void __launch_bounds__(THREADS == 32 ? kRowThreads : THREADS, norm_bl
         }
         const float2 sums = block_sum<THREADS>(make_float2(s.x + s.y, q.x + q.y), p);
         rest = sums.x * inv;
-        const float v = sums.y * inv - rest * rest;
-        return v < 0.f ? 0.f : v;   // (keeps a NaN)
+        const float var = sums.y * inv - rest * rest;
+        return var < 0.f ? 0.f : var;   // (keeps a NaN)
     };
     auto outputs = [&](const bool scaled) {
         const float2 less = make_float2(-rest, -rest), r = make_float2(rstd, rstd);
@@ -213,9 +213,10 @@ __global__ void __launch_bounds__(THREADS == 32 ? kRowThreads : THREADS, norm_bl
         }
     };
     find_mean(false, part[0]);
-    const float var = spread(false, part[1]) + a.eps;
+    float v = spread(false, part[1]);
+    const float var = v + a.eps;
     rstd = rsqrtf(var);
-    if (__builtin_expect(in_range(var) && rest * rest <= var, true)) {
+    if (__builtin_expect(var >= kLeast && v <= kMost && rest * rest <= var, true)) {
         outputs(false);
     } else {
         // Squares that F32 does not hold: the row times 2^-80, or the deviations times
@@ -225,13 +226,12 @@ __global__ void __launch_bounds__(THREADS == 32 ? kRowThreads : THREADS, norm_bl
         // is left of that rounding is no variance): the mean is corrected until what is
         // left of it is below the root of the variance, mostly once.
         mean += rest;
-        if (var < 0x1p-80f) {
+        if (var < kLeast) {
             wide = 0x1p90f;
-        } else if (!in_range(var)) {
+        } else if (!(v <= kMost)) {
             scale = 0x1p-80f;
             find_mean(true, part[0]);
         }
-        float v = 0.f;
 #pragma unroll
         for (int again = 0; again < 2; ++again) {
             if (again) mean += rest / wide;

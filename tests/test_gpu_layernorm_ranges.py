@@ -79,6 +79,17 @@ def test_equal_values_with_any_eps(sk, K, value, eps):
     equal_rows(sk, x, 1 + 0.3 * randn(g, K), randn(g, K), "f32", float(x[0, 0]), eps=eps)
 
 
+@pytest.mark.parametrize("eps", [1e30, 1e36, 2e36, 1e38, 3.3e38])
+@pytest.mark.parametrize("size", [1e-15, 1.0, 1e15, 1e19])
+@pytest.mark.parametrize("K", [64, 2048, 16392])
+def test_large_eps(sk, K, size, eps):
+    """eps beyond the squares' range takes nothing from small values."""
+    g = gen(K)
+    x, w = size * randn(g, 3, K), 1 + 0.3 * randn(g, K)
+    y, mean, rstd, _ = forward(sk, x, None, w, None, "f32", eps=eps)
+    check_forward(y, mean, rstd, x, w, None, "f32", eps=eps)
+
+
 @pytest.mark.parametrize("K", [64, 2048, 16392])
 def test_equal_sums_of_any_size(sk, K):
     """The same where the values are sums that nothing keeps, and in the place of x."""
